@@ -22,6 +22,13 @@ Functions carry the C names:
 * ``bsa_adaptive_block_size(seq_len)`` -> 64, 128 or 256
 * ``bsa_forward_overlap(q, k, v, block_size, topk_ratio, overlap_ratio)`` -> o
   with overlapping key windows (and ``bsa_sparse_attn_fwd_overlap``)
+* ``bsa_cache_write(k, v, cache, k_sum, page_table, start, block_size)``,
+  ``bsa_cache_read(cache, page_table, start, T, block_size)`` -> (k, v),
+  ``bsa_cache_block_topk(q, k_sum, page_table, start, topk, block_size)`` -> idx,
+  ``bsa_cache_attn(q, cache, page_table, start, block_size, idx=None)`` -> o and
+  ``bsa_cache_forward(q, k, v, cache, k_sum, page_table, start, block_size,
+  topk)`` -> o: generation over a paged key/value cache held in 4 bits
+  (``bsa_cache_alloc(num_pages, H_kv, D, block_size)`` makes one)
 * ``bsa_topk_count``, ``bsa_forward_workspace_bytes``,
   ``bsa_forward_host_workspace_bytes``, ``workspace_views``, ``bsa_device_error``
 
@@ -57,7 +64,9 @@ EXPORTED = ("bsa_topk_count", "bsa_forward_workspace_bytes", "bsa_block_pool",
             "bsa_sparse_attn_fwd_train_gqa", "bsa_sparse_attn_bwd_gqa_workspace_bytes", "bsa_sparse_attn_bwd_gqa",
             "bsa_adaptive_block_size", "bsa_block_pool_ex", "bsa_overlap_window_count",
             "bsa_forward_overlap_workspace_bytes", "bsa_sparse_attn_fwd_overlap", "bsa_forward_overlap",
-            "bsa_block_pool_qk")
+            "bsa_block_pool_qk", "bsa_cache_bytes", "bsa_cache_write", "bsa_cache_read", "bsa_cache_block_topk",
+            "bsa_cache_attn_workspace_bytes", "bsa_cache_attn", "bsa_cache_forward_workspace_bytes",
+            "bsa_cache_forward")
 
 #: variant flags of the *_ex entry points (include/bsa.h)
 BSA_FLAG_CAUSAL, BSA_FLAG_FORCE_DIAG, BSA_FLAG_MAX_POOL = 1, 2, 4
@@ -117,6 +126,14 @@ def _load() -> ctypes.CDLL:
         "bsa_forward_overlap_workspace_bytes": ([I, I, I, I, I, I, D, D], Z),
         "bsa_sparse_attn_fwd_overlap": ([P, P, P, P, P, I, I, I, I, I, I, I, D, F, I, U, P], I),
         "bsa_forward_overlap": ([P, P, P, P, I, I, I, I, I, I, D, D, I, U, P, Z, P], I),
+        "bsa_cache_bytes": ([I, I, I, I], Z),
+        "bsa_cache_write": ([P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, P], I),
+        "bsa_cache_read": ([P, P, P, P, P, P, I, I, I, I, I, I, I, I, P], I),
+        "bsa_cache_block_topk": ([P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, U, P], I),
+        "bsa_cache_attn_workspace_bytes": ([I, I, I, I, I], Z),
+        "bsa_cache_attn": ([P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, I, P, Z, P], I),
+        "bsa_cache_forward_workspace_bytes": ([I, I, I, I, I, I], Z),
+        "bsa_cache_forward": ([P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, U, P, Z, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -560,3 +577,214 @@ def workspace_views(ws: torch.Tensor, B: int, N: int, H: int, D: int, block_size
     off = qpb + kpb + idxb
     S = base[off:off + B * Hk * nb * nb * 4].view(torch.float32).view(B, Hk, nb, nb)
     return qp, kp, idx, S
+
+
+# ---------------------------------------------------------------- the 4-bit key/value cache
+
+
+def bsa_cache_bytes(num_pages: int, H_kv: int, D: int, block_size: int) -> int:
+    return lib.bsa_cache_bytes(num_pages, H_kv, D, block_size)
+
+
+def bsa_cache_alloc(num_pages: int, H_kv: int, D: int, block_size: int, device="cuda"):
+    """An empty cache [num_pages, H_kv, block_size / 64, 72 D] uint8 and its key
+    sums [num_pages, H_kv, D] float32. Neither needs a first value."""
+    if bsa_cache_bytes(num_pages, H_kv, D, block_size) == 0:
+        raise ValueError("num_pages and H_kv must be positive, D 64 or 128, block_size 64, 128 or 256")
+    return (torch.empty((num_pages, H_kv, block_size // 64, 72 * D), device=device, dtype=torch.uint8),
+            torch.empty((num_pages, H_kv, D), device=device, dtype=torch.float32))
+
+
+def _same_device(*named):
+    """Every tensor contiguous on the first one's CUDA device, which is made the
+    current one of the call by _cache_call."""
+    for t, n in named:
+        if t is not None:
+            _dev(t, n)
+            if t.device != named[0][0].device:
+                raise ValueError(f"{n} is on {t.device}, {named[0][1]} on {named[0][0].device}")
+
+
+def _check_seqs(page_table, start, count, B: int):
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [{B}, max_blocks]")
+    _shape(start, (B,), "start")
+    if count is not None:
+        _shape(count, (B,), "count")
+    for t, n in ((page_table, "page_table"), (start, "start"), (count, "count")):
+        if t is not None and t.dtype != torch.int32:
+            raise TypeError(f"{n} must be int32")
+
+
+def _check_cache(cache, H_kv: int, D: int, block_size: int):
+    if cache.dim() != 4 or tuple(cache.shape[1:]) != (H_kv, block_size // 64, 72 * D) or block_size % 64:
+        raise ValueError(f"cache has shape {tuple(cache.shape)}, expected [num_pages, {H_kv}, {block_size} / 64, {72 * D}]")
+    if cache.dtype != torch.uint8:
+        raise TypeError("cache must be uint8")
+
+
+def _check_k_sum(k_sum, num_pages, H_kv: int, D: int):
+    if k_sum.dim() != 3 or tuple(k_sum.shape[1:]) != (H_kv, D) or num_pages not in (None, k_sum.shape[0]):
+        raise ValueError(f"k_sum has shape {tuple(k_sum.shape)}, expected [num_pages, {H_kv}, {D}]")
+    if k_sum.dtype != torch.float32:
+        raise TypeError("k_sum must be float32")
+
+
+def _cache_call(fn, t: torch.Tensor, *args):
+    """fn(*args, stream) with t's device current and its current stream."""
+    if t.device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(t)))
+    else:
+        with torch.cuda.device(t.device):
+            _check(fn(*args, _stream(t)))
+
+
+def bsa_cache_write(k, v, cache, k_sum, page_table, start, block_size: int, count=None) -> None:
+    """Writes k and v [B, T, H_kv, D] into the cache at the positions start[b] +
+    t, t < count[b] (all T without count), and renews k_sum of their pages."""
+    if k.dim() != 4:
+        raise ValueError("k and v must be [B, T, H_kv, D]")
+    _shape(v, k.shape, "v")
+    if v.dtype != k.dtype:
+        raise TypeError("k and v must share one dtype")
+    B, T, Hk, D = k.shape
+    _check_cache(cache, Hk, D, block_size)
+    _check_k_sum(k_sum, cache.shape[0], Hk, D)
+    _check_seqs(page_table, start, count, B)
+    _same_device((k, "k"), (v, "v"), (cache, "cache"), (k_sum, "k_sum"), (page_table, "page_table"), (start, "start"),
+                 (count, "count"))
+    _cache_call(lib.bsa_cache_write, k, _p(k), _p(v), _p(cache), _p(k_sum), _p(page_table), _p(start), _p(count), B, T,
+                Hk, D, block_size, cache.shape[0], page_table.shape[1], _dtype_code(k))
+
+
+def bsa_cache_read(cache, page_table, start, T: int, block_size: int, dtype: torch.dtype = torch.bfloat16, count=None,
+                   k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None):
+    """Keys and values [B, T, H_kv, D] of the positions start[b] + t, in dtype (or
+    k_out's). Rows t >= count[b] of k_out and v_out stay as they are; tensors
+    that the call makes hold zeros there."""
+    if cache.dim() != 4 or cache.shape[3] % 72:
+        raise ValueError(f"cache has shape {tuple(cache.shape)}, expected [num_pages, H_kv, block_size / 64, 72 D]")
+    B, Hk, D = page_table.shape[0], cache.shape[1], cache.shape[3] // 72
+    _check_cache(cache, Hk, D, block_size)
+    _check_seqs(page_table, start, count, B)
+    new = torch.empty if count is None else torch.zeros
+    if k_out is None:
+        k_out = new((B, T, Hk, D), device=cache.device, dtype=dtype if v_out is None else v_out.dtype)
+    if v_out is None:
+        v_out = new((B, T, Hk, D), device=cache.device, dtype=k_out.dtype)
+    _shape(k_out, (B, T, Hk, D), "k_out")
+    _shape(v_out, (B, T, Hk, D), "v_out")
+    if k_out.dtype != v_out.dtype:
+        raise TypeError("k_out and v_out must share one dtype")
+    _same_device((cache, "cache"), (page_table, "page_table"), (start, "start"), (count, "count"), (k_out, "k_out"),
+                 (v_out, "v_out"))
+    _cache_call(lib.bsa_cache_read, cache, _p(cache), _p(page_table), _p(start), _p(count), _p(k_out), _p(v_out), B, T,
+                Hk, D, block_size, cache.shape[0], page_table.shape[1], _dtype_code(k_out))
+    return k_out, v_out
+
+
+def _check_step_q(q, Hk: int, D: int):
+    if q.dim() != 4 or q.shape[3] != D or Hk < 1 or q.shape[2] % Hk:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected [B, T, H, {D}] with H a multiple of {Hk}")
+
+
+def bsa_cache_block_topk(q, k_sum, page_table, start, topk: int, block_size: int, count=None,
+                         idx_out: torch.Tensor | None = None, flags: int = 0) -> torch.Tensor:
+    """Blocks [B, H_kv, topk] int32 of the largest scores of the step's queries q
+    [B, T, H, D], ascending, padded with -1."""
+    if k_sum.dim() != 3:
+        raise ValueError("k_sum must be [num_pages, H_kv, D]")
+    Hk, D = k_sum.shape[1:]
+    _check_step_q(q, Hk, D)
+    _check_k_sum(k_sum, None, Hk, D)
+    B, T, H, _ = q.shape
+    _check_seqs(page_table, start, count, B)
+    if idx_out is not None:
+        _shape(idx_out, (B, Hk, topk), "idx_out")
+        if idx_out.dtype != torch.int32:
+            raise TypeError("idx_out must be int32")
+    _same_device((q, "q"), (k_sum, "k_sum"), (page_table, "page_table"), (start, "start"), (count, "count"),
+                 (idx_out, "idx_out"))
+    idx = idx_out if idx_out is not None else torch.empty((B, Hk, max(topk, 0)), device=q.device, dtype=torch.int32)
+    _cache_call(lib.bsa_cache_block_topk, q, _p(q), _p(k_sum), _p(page_table), _p(start), _p(count), _p(idx), B, T, H,
+                Hk, D, block_size, k_sum.shape[0], page_table.shape[1], topk, _dtype_code(q), flags)
+    return idx
+
+
+def bsa_cache_attn_workspace_bytes(B: int, T: int, H: int, H_kv: int, D: int) -> int:
+    return lib.bsa_cache_attn_workspace_bytes(B, T, H, H_kv, D)
+
+
+def _step_out(out, q, count):
+    """The output of a step: rows that no token has are zeros where the call makes it."""
+    if out is not None:
+        _check_out(out, q)
+        return out
+    return (torch.empty_like if count is None else torch.zeros_like)(q)
+
+
+def _workspace(workspace, need: int, q):
+    return torch.empty(max(need, 1), device=q.device, dtype=torch.uint8) if workspace is None else workspace
+
+
+def bsa_cache_attn(q, cache, page_table, start, block_size: int, idx: torch.Tensor | None = None,
+                   scale: float | None = None, count=None, workspace: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of q [B, T, H, D] (token t at position start[b] + t) over the
+    cache: over the blocks of idx [B, H_kv, topk], or all of them without."""
+    if cache.dim() != 4 or cache.shape[3] % 72:
+        raise ValueError(f"cache has shape {tuple(cache.shape)}, expected [num_pages, H_kv, block_size / 64, 72 D]")
+    Hk, D = cache.shape[1], cache.shape[3] // 72
+    _check_step_q(q, Hk, D)
+    _check_cache(cache, Hk, D, block_size)
+    B, T, H, _ = q.shape
+    _check_seqs(page_table, start, count, B)
+    if idx is not None:
+        if idx.dim() != 3 or tuple(idx.shape[:2]) != (B, Hk):
+            raise ValueError(f"idx has shape {tuple(idx.shape)}, expected [{B}, {Hk}, topk]")
+        if idx.dtype != torch.int32:
+            raise TypeError("idx must be int32")
+    if out is not None:
+        _check_out(out, q)
+    _same_device((q, "q"), (cache, "cache"), (page_table, "page_table"), (start, "start"), (count, "count"),
+                 (idx, "idx"), (workspace, "workspace"), (out, "out"))
+    workspace = _workspace(workspace, bsa_cache_attn_workspace_bytes(B, T, H, Hk, D), q)
+    o = _step_out(out, q, count)
+    _cache_call(lib.bsa_cache_attn, q, _p(q), _p(cache), _p(page_table), _p(start), _p(count), _p(idx), _p(o), B, T, H,
+                Hk, D, block_size, cache.shape[0], page_table.shape[1], 0 if idx is None else idx.shape[2],
+                1.0 / math.sqrt(D) if scale is None else float(scale), _dtype_code(q), _p(workspace),
+                workspace.numel() * workspace.element_size())
+    return o
+
+
+def bsa_cache_forward_workspace_bytes(B: int, T: int, H: int, H_kv: int, D: int, topk: int) -> int:
+    return lib.bsa_cache_forward_workspace_bytes(B, T, H, H_kv, D, topk)
+
+
+def bsa_cache_forward(q, k, v, cache, k_sum, page_table, start, block_size: int, topk: int = 0, count=None,
+                      workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                      flags: int = 0) -> torch.Tensor:
+    """One step of generation: writes k and v [B, T, H_kv, D], selects topk blocks
+    (0: all) for q [B, T, H, D] and attends over them."""
+    if k.dim() != 4:
+        raise ValueError("k and v must be [B, T, H_kv, D]")
+    _shape(v, k.shape, "v")
+    B, T, Hk, D = k.shape
+    _check_step_q(q, Hk, D)
+    H = q.shape[2]
+    _shape(q, (B, T, H, D), "q")
+    if not (q.dtype == k.dtype == v.dtype):
+        raise TypeError("q, k, v must share one dtype")
+    _check_cache(cache, Hk, D, block_size)
+    _check_k_sum(k_sum, cache.shape[0], Hk, D)
+    _check_seqs(page_table, start, count, B)
+    if out is not None:
+        _check_out(out, q)
+    _same_device((q, "q"), (k, "k"), (v, "v"), (cache, "cache"), (k_sum, "k_sum"), (page_table, "page_table"),
+                 (start, "start"), (count, "count"), (workspace, "workspace"), (out, "out"))
+    workspace = _workspace(workspace, bsa_cache_forward_workspace_bytes(B, T, H, Hk, D, topk), q)
+    o = _step_out(out, q, count)
+    _cache_call(lib.bsa_cache_forward, q, _p(q), _p(k), _p(v), _p(cache), _p(k_sum), _p(page_table), _p(start),
+                _p(count), _p(o), B, T, H, Hk, D, block_size, cache.shape[0], page_table.shape[1], topk, _dtype_code(q),
+                flags, _p(workspace), workspace.numel() * workspace.element_size())
+    return o

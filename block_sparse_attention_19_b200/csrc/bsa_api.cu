@@ -11,7 +11,9 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
+#include <type_traits>
 #include <utility>
 
 #include "attn_simt.cuh"
@@ -19,6 +21,8 @@
 #include "bwd.cuh"
 #include "bsa.h"
 #include "bsa_ptx.cuh"
+#include "cache.cuh"
+#include "cache_attn.cuh"
 #include "pool.cuh"
 #include "scores_tc.cuh"
 #include "select.cuh"
@@ -1226,3 +1230,227 @@ extern "C" bsa_status bsa_forward_host(const void* q, const void* k, const void*
   if ((e = cudaStreamWaitEvent(st, hs->end, 0)) != cudaSuccess) return cuda_fail(e, "stream wait");
   return ok();
 }
+
+// ==================================================================== the 4-bit key/value cache
+
+namespace {
+
+constexpr int kCacheMaxBlocks = 49152;  // keys of one row of the block selection in shared memory
+
+bsa_status check_cache_dims(int B, int T, int H, int Hkv, int D, int block_size) {
+  if (B < 1 || T < 1 || H < 1 || D < 1 || block_size < 1)
+    return fail(BSA_ERR_INVALID_ARG, "sizes must be positive (B=%d T=%d H=%d D=%d block_size=%d)", B, T, H, D,
+                block_size);
+  bsa_status s;
+  if ((s = check_heads(H, Hkv)) != BSA_OK) return s;
+  if (D != 64 && D != 128) return fail(BSA_ERR_UNSUPPORTED, "D=%d (supported: 64, 128)", D);
+  if (block_size != 64 && block_size != 128 && block_size != 256)
+    return fail(BSA_ERR_UNSUPPORTED, "block_size=%d (supported: 64, 128, 256)", block_size);
+  if (T > (1 << 29) || H > (1 << 16) || static_cast<long long>(B) * H > (1ll << 24) ||
+      static_cast<long long>(B) * T * H > (1ll << 30))
+    return fail(BSA_ERR_UNSUPPORTED, "B, T or H too large for the launch grid");
+  return BSA_OK;
+}
+
+bsa_status check_cache(int B, int T, int H, int Hkv, int D, int block_size, int num_pages, int max_blocks,
+                       bsa_dtype dt) {
+  bsa_status s;
+  if ((s = check_cache_dims(B, T, H, Hkv, D, block_size)) != BSA_OK) return s;
+  if (num_pages < 1 || max_blocks < 1)
+    return fail(BSA_ERR_INVALID_ARG, "num_pages=%d and max_blocks=%d must be positive", num_pages, max_blocks);
+  if (static_cast<long long>(max_blocks) * block_size > (1ll << 30))
+    return fail(BSA_ERR_UNSUPPORTED, "max_blocks * block_size beyond 2^30 positions");
+  if ((s = check_dtype(dt)) != BSA_OK) return s;
+  if (dt == BSA_E4M3) return fail(BSA_ERR_UNSUPPORTED, "the cache takes float32 and bfloat16 tensors");
+  return BSA_OK;
+}
+
+bsa_status check_cache_lists(const int32_t* table, const int32_t* start, const int32_t* count, const int32_t* idx) {
+  if (!table || !start) return fail(BSA_ERR_INVALID_ARG, "null page_table or start");
+  for (const void* p : {static_cast<const void*>(table), static_cast<const void*>(start),
+                        static_cast<const void*>(count), static_cast<const void*>(idx)})
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return fail(BSA_ERR_MISALIGNED, "an int32 list not 4-byte aligned");
+  return BSA_OK;
+}
+
+// The tensors of a call: none null, all 16-byte aligned.
+bsa_status check_tensors(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!p) return fail(BSA_ERR_INVALID_ARG, "null pointer");
+  for (const void* p : ps)
+    if (!aligned16(p)) return fail(BSA_ERR_MISALIGNED, "device pointers must be 16-byte aligned");
+  return BSA_OK;
+}
+
+bsa_status launched(cudaError_t e, const char* what) {
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? BSA_OK : cuda_fail(e, what);
+}
+
+// Calls f with a value of the element type and the head size as a constant.
+template <typename F>
+cudaError_t by_type(bsa_dtype dt, int D, F f) {
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  if (dt == BSA_F32) return D == 64 ? f(float{}, D64{}) : f(float{}, D128{});
+  return D == 64 ? f(__nv_bfloat16{}, D64{}) : f(__nv_bfloat16{}, D128{});
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t bsa_cache_bytes(int num_pages, int H_kv, int D, int block_size) {
+  if (num_pages < 1 || check_cache_dims(1, 1, H_kv, H_kv, D, block_size) != BSA_OK) return 0;
+  return static_cast<size_t>(num_pages) * H_kv * (block_size / bsa::kCacheTile) * bsa::cache_tile_bytes(D);
+}
+
+bsa_status bsa_cache_write(const void* k, const void* v, void* cache, float* k_sum, const int32_t* page_table,
+                           const int32_t* start, const int32_t* count, int B, int T, int H_kv, int D, int block_size,
+                           int num_pages, int max_blocks, bsa_dtype dt, void* stream) {
+  bsa_status s;
+  if ((s = check_cache(B, T, H_kv, H_kv, D, block_size, num_pages, max_blocks, dt)) != BSA_OK) return s;
+  if ((s = check_tensors({k, v, cache, k_sum})) != BSA_OK) return s;
+  if ((s = check_cache_lists(page_table, start, count, nullptr)) != BSA_OK) return s;
+  if ((s = check_device()) != BSA_OK) return s;
+  const long long nslot = (static_cast<long long>(T) + block_size - 2) / block_size + 1;  // blocks that T tokens touch
+  const long long grid = nslot * B * H_kv;
+  if (grid > 0x7fffffffll) return fail(BSA_ERR_UNSUPPORTED, "write grid too large");
+  const bsa::CacheSeqs seqs{page_table, start, count, T, num_pages, max_blocks, block_size};
+  const cudaError_t e = by_type(dt, D, [&](auto t, auto d) {
+    using E = decltype(t);
+    return launch_pdl(bsa::cache_write_kernel<E, decltype(d)::value>, static_cast<unsigned>(grid), 128, 0,
+                      static_cast<cudaStream_t>(stream), static_cast<const E*>(k), static_cast<const E*>(v),
+                      static_cast<uint8_t*>(cache), k_sum, seqs, H_kv, static_cast<int>(nslot));
+  });
+  if ((s = launched(e, "cache_write_kernel launch")) != BSA_OK) return s;
+  return ok();
+}
+
+bsa_status bsa_cache_read(const void* cache, const int32_t* page_table, const int32_t* start, const int32_t* count,
+                          void* k, void* v, int B, int T, int H_kv, int D, int block_size, int num_pages,
+                          int max_blocks, bsa_dtype dt, void* stream) {
+  bsa_status s;
+  if ((s = check_cache(B, T, H_kv, H_kv, D, block_size, num_pages, max_blocks, dt)) != BSA_OK) return s;
+  if ((s = check_tensors({cache, k, v})) != BSA_OK) return s;
+  if ((s = check_cache_lists(page_table, start, count, nullptr)) != BSA_OK) return s;
+  if ((s = check_device()) != BSA_OK) return s;
+  const long total = static_cast<long>(B) * T * H_kv * (D / 8);
+  const long grid = (total + 255) / 256;
+  if (grid > 0x7fffffffl) return fail(BSA_ERR_UNSUPPORTED, "read grid too large");
+  const bsa::CacheSeqs seqs{page_table, start, count, T, num_pages, max_blocks, block_size};
+  const cudaError_t e = by_type(dt, D, [&](auto t, auto d) {
+    using E = decltype(t);
+    return launch_pdl(bsa::cache_read_kernel<E, decltype(d)::value>, static_cast<unsigned>(grid), 256, 0,
+                      static_cast<cudaStream_t>(stream), static_cast<const uint8_t*>(cache), static_cast<E*>(k),
+                      static_cast<E*>(v), seqs, H_kv, total);
+  });
+  if ((s = launched(e, "cache_read_kernel launch")) != BSA_OK) return s;
+  return ok();
+}
+
+bsa_status bsa_cache_block_topk(const void* q, const float* k_sum, const int32_t* page_table, const int32_t* start,
+                                const int32_t* count, int32_t* idx, int B, int T, int H, int H_kv, int D,
+                                int block_size, int num_pages, int max_blocks, int topk, bsa_dtype dt, unsigned flags,
+                                void* stream) {
+  bsa_status s;
+  if ((s = check_cache(B, T, H, H_kv, D, block_size, num_pages, max_blocks, dt)) != BSA_OK) return s;
+  if ((s = check_flags(flags)) != BSA_OK) return s;
+  if (flags & ~(BSA_FLAG_CAUSAL | BSA_FLAG_FORCE_DIAG))
+    return fail(BSA_ERR_UNSUPPORTED, "the cache's selection takes no max pooling and no global heads");
+  if (topk < 1) return fail(BSA_ERR_INVALID_ARG, "topk=%d must be positive", topk);
+  if (max_blocks > kCacheMaxBlocks)
+    return fail(BSA_ERR_UNSUPPORTED, "max_blocks=%d (the selection holds up to %d)", max_blocks, kCacheMaxBlocks);
+  if ((s = check_tensors({q, k_sum})) != BSA_OK) return s;
+  if (!idx) return fail(BSA_ERR_INVALID_ARG, "null idx");
+  if ((s = check_cache_lists(page_table, start, count, idx)) != BSA_OK) return s;
+  if ((s = check_device()) != BSA_OK) return s;
+  const bsa::CacheSeqs seqs{page_table, start, count, T, num_pages, max_blocks, block_size};
+  const size_t smem = static_cast<size_t>(max_blocks) * sizeof(uint32_t);
+  const cudaError_t e = by_type(dt, D, [&](auto t, auto d) {
+    using E = decltype(t);
+    const auto kern = bsa::cache_topk_kernel<E, decltype(d)::value>;
+    const cudaError_t a = smem > 32768 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                              kCacheMaxBlocks * sizeof(uint32_t))
+                                       : cudaSuccess;
+    if (a != cudaSuccess) return a;
+    return launch_pdl(kern, static_cast<unsigned>(B) * H_kv, bsa::kCacheSelThreads, smem,
+                      static_cast<cudaStream_t>(stream), static_cast<const E*>(q), k_sum, idx, seqs, H, H_kv, topk,
+                      (flags & BSA_FLAG_FORCE_DIAG) ? 1 : 0);
+  });
+  if ((s = launched(e, "cache_topk_kernel launch")) != BSA_OK) return s;
+  return ok();
+}
+
+size_t bsa_cache_attn_workspace_bytes(int B, int T, int H, int H_kv, int D) {
+  if (check_cache_dims(B, T, H, H_kv, D, 64) != BSA_OK) return 0;
+  return 256;
+}
+
+bsa_status bsa_cache_attn(const void* q, const void* cache, const int32_t* page_table, const int32_t* start,
+                          const int32_t* count, const int32_t* idx, void* o, int B, int T, int H, int H_kv, int D,
+                          int block_size, int num_pages, int max_blocks, int topk, float scale, bsa_dtype dt,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  bsa_status s;
+  if ((s = check_cache(B, T, H, H_kv, D, block_size, num_pages, max_blocks, dt)) != BSA_OK) return s;
+  if (idx && topk < 1) return fail(BSA_ERR_INVALID_ARG, "topk=%d must be positive", topk);
+  if (!std::isfinite(scale) || scale <= 0.0f) return fail(BSA_ERR_INVALID_ARG, "scale must be positive and finite");
+  if ((s = check_tensors({q, cache, o})) != BSA_OK) return s;
+  if (o == q) return fail(BSA_ERR_INVALID_ARG, "o must not alias q");
+  if ((s = check_cache_lists(page_table, start, count, idx)) != BSA_OK) return s;
+  if (!workspace || workspace_bytes < bsa_cache_attn_workspace_bytes(B, T, H, H_kv, D))
+    return fail(BSA_ERR_WORKSPACE, "workspace missing or smaller than bsa_cache_attn_workspace_bytes()");
+  if (!aligned16(workspace)) return fail(BSA_ERR_MISALIGNED, "workspace not 16-byte aligned");
+  if ((s = check_device()) != BSA_OK) return s;
+  const bsa::CacheSeqs seqs{page_table, start, count, T, num_pages, max_blocks, block_size};
+  const cudaError_t e = by_type(dt, D, [&](auto t, auto d) {
+    using E = decltype(t);
+    return launch_pdl(bsa::cache_attn_kernel<E, decltype(d)::value>, static_cast<unsigned>(B) * T * H, 128, 0,
+                      static_cast<cudaStream_t>(stream), static_cast<const E*>(q), static_cast<const uint8_t*>(cache),
+                      idx, static_cast<E*>(o), seqs, H, H_kv, topk, scale * 1.4426950408889634f);
+  });
+  if ((s = launched(e, "cache_attn_kernel launch")) != BSA_OK) return s;
+  return ok();
+}
+
+size_t bsa_cache_forward_workspace_bytes(int B, int T, int H, int H_kv, int D, int topk) {
+  const size_t attn = bsa_cache_attn_workspace_bytes(B, T, H, H_kv, D);
+  if (attn == 0 || topk < 0) return 0;
+  return align256(static_cast<size_t>(B) * H_kv * topk * sizeof(int32_t)) + align256(attn);
+}
+
+bsa_status bsa_cache_forward(const void* q, const void* k, const void* v, void* cache, float* k_sum,
+                             const int32_t* page_table, const int32_t* start, const int32_t* count, void* o, int B,
+                             int T, int H, int H_kv, int D, int block_size, int num_pages, int max_blocks, int topk,
+                             bsa_dtype dt, unsigned flags, void* workspace, size_t workspace_bytes, void* stream) {
+  bsa_status s;
+  // everything that a later step would refuse is refused before the first one writes
+  if ((s = check_cache(B, T, H, H_kv, D, block_size, num_pages, max_blocks, dt)) != BSA_OK) return s;
+  if ((s = check_flags(flags)) != BSA_OK) return s;
+  if (flags & ~(BSA_FLAG_CAUSAL | BSA_FLAG_FORCE_DIAG))
+    return fail(BSA_ERR_UNSUPPORTED, "the cache's selection takes no max pooling and no global heads");
+  if (topk < 0) return fail(BSA_ERR_INVALID_ARG, "topk=%d must not be negative", topk);
+  if (topk && max_blocks > kCacheMaxBlocks)
+    return fail(BSA_ERR_UNSUPPORTED, "max_blocks=%d (the selection holds up to %d)", max_blocks, kCacheMaxBlocks);
+  if ((s = check_tensors({q, k, v, cache, k_sum, o})) != BSA_OK) return s;
+  if (o == q) return fail(BSA_ERR_INVALID_ARG, "o must not alias q");
+  if ((s = check_cache_lists(page_table, start, count, nullptr)) != BSA_OK) return s;
+  const size_t need = bsa_cache_forward_workspace_bytes(B, T, H, H_kv, D, topk);
+  if (!workspace || workspace_bytes < need)
+    return fail(BSA_ERR_WORKSPACE, "workspace missing or smaller than bsa_cache_forward_workspace_bytes()");
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(BSA_ERR_MISALIGNED, "workspace not 256-byte aligned");
+  int32_t* idx = topk ? static_cast<int32_t*>(workspace) : nullptr;
+  const size_t idx_bytes = align256(static_cast<size_t>(B) * H_kv * topk * sizeof(int32_t));
+  if ((s = bsa_cache_write(k, v, cache, k_sum, page_table, start, count, B, T, H_kv, D, block_size, num_pages,
+                           max_blocks, dt, stream)) != BSA_OK)
+    return s;
+  if (topk && (s = bsa_cache_block_topk(q, k_sum, page_table, start, count, idx, B, T, H, H_kv, D, block_size,
+                                        num_pages, max_blocks, topk, dt, flags, stream)) != BSA_OK)
+    return s;
+  return bsa_cache_attn(q, cache, page_table, start, count, idx, o, B, T, H, H_kv, D, block_size, num_pages, max_blocks,
+                        topk, static_cast<float>(1.0 / std::sqrt(static_cast<double>(D))), dt,
+                        static_cast<uint8_t*>(workspace) + idx_bytes, workspace_bytes - idx_bytes, stream);
+}
+
+}  // extern "C"

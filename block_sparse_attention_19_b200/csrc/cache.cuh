@@ -1,0 +1,385 @@
+// cache.cuh -- the paged 4-bit key/value cache: layout, writing, reading back,
+// and the selection of its blocks for a step's queries. (The attention over it
+// is in cache_attn.cuh.)
+//
+// One page holds one block of bs tokens of every key/value head, per head as
+// bs / 64 tiles of 64 tokens. A tile is 72 D bytes:
+//   K codes   [64 tokens][D / 2]          token r, channel c: see k_word
+//   V codes   [32 token pairs][D]         see v_chunk
+//   K scales  [64 tokens][D / 64] (scale, zero) bf16 pairs
+//   V scales  [64 tokens][D / 64] (scale, zero) bf16 pairs
+// The order of the codes is the one in which the attention kernel's matrix
+// instructions want them: each of its threads reads a tile with 16-byte (D =
+// 128; 8-byte for D = 64) shared-memory loads free of bank conflicts, and a
+// 32-bit word holds eight codes that two masks per byte of shift turn into
+// float16 pairs.
+//   K: word wi (of D / 32) of quarter t (0..3) of a token's row holds the
+//      channels 32 wi + 8 t + 0..7, the lowest four bits the first; words lie
+//      in the order [t][wi].
+//   V: word wi of chunk g (0..7) of token pair p holds the channels 32 wi + 4 g
+//      + 0..3 of token 2 p in its low half and of token 2 p + 1 in its high
+//      half; chunks lie in the order g ^ (2 (p % 4)), words in [chunk][wi].
+#pragma once
+
+#include <cuda_bf16.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "bsa_ptx.cuh"
+
+namespace bsa {
+
+constexpr int kCacheTile = 64;  // tokens of a tile
+
+__host__ __device__ constexpr int cache_tile_bytes(int D) { return 72 * D; }
+__host__ __device__ constexpr int cache_v_offset(int D) { return 32 * D; }
+__host__ __device__ constexpr int cache_ks_offset(int D) { return 64 * D; }
+__host__ __device__ constexpr int cache_vs_offset(int D) { return 68 * D; }
+
+// Byte of the 32-bit word with octet `oct` (channels 8 oct .. 8 oct + 7) in a
+// token's K row.
+__host__ __device__ constexpr int k_word(int oct, int D) { return (oct % 4) * (D / 8) + (oct / 4) * 4; }
+// Byte of the word with channels 8 oct + 4 hi .. + 3 in the V row of pair p.
+__host__ __device__ constexpr int v_word(int p, int oct, int hi, int D) {
+  return ((((oct % 4) * 2 + hi) ^ (2 * (p % 4))) * (D / 8)) + (oct / 4) * 4;
+}
+
+// What the cache operators know of one call's sequences.
+struct CacheSeqs {
+  const int32_t* table;  // [B, max_blocks]: page of each block; outside [0, num_pages): absent
+  const int32_t* start;  // [B]: tokens in the cache before this step's
+  const int32_t* count;  // [B]: this step's new tokens (null: T)
+  int T, num_pages, max_blocks, bs;
+};
+
+// Start and count of a sequence, brought into range: a negative start makes the
+// sequence empty, count lies in [0, T], start in [0, capacity].
+__device__ __forceinline__ void seq_step(const CacheSeqs& s, int b, int& start, int& count) {
+  start = s.start[b];
+  count = s.count ? s.count[b] : s.T;
+  count = start < 0 ? 0 : max(0, min(count, s.T));
+  start = max(0, min(start, s.max_blocks * s.bs));
+}
+
+// Page of a block, or -1 where the table has none.
+__device__ __forceinline__ int seq_page(const CacheSeqs& s, int b, int block) {
+  if (block < 0 || block >= s.max_blocks) return -1;
+  const int page = s.table[static_cast<long>(b) * s.max_blocks + block];
+  return page >= 0 && page < s.num_pages ? page : -1;
+}
+
+__device__ __forceinline__ uint8_t* tile_ptr(uint8_t* cache, int page, int h, int tile, int Hkv, int bs, int D) {
+  return cache + ((static_cast<long>(page) * Hkv + h) * (bs / kCacheTile) + tile) * cache_tile_bytes(D);
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Eight consecutive channels of x as float32.
+__device__ __forceinline__ void load_octet(const __nv_bfloat16* x, float (&f)[8]) {
+  const uint4 u = __ldg(reinterpret_cast<const uint4*>(x));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load_octet(const float* x, float (&f)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(x)), b = __ldg(reinterpret_cast<const float4*>(x) + 1);
+  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+__device__ __forceinline__ void store_octet(__nv_bfloat16* x, const float (&f)[8]) {
+  *reinterpret_cast<uint4*>(x) =
+      make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ void store_octet(float* x, const float (&f)[8]) {
+  reinterpret_cast<float4*>(x)[0] = make_float4(f[0], f[1], f[2], f[3]);
+  reinterpret_cast<float4*>(x)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+// The value that a code stands for: the product is exact, the sum rounds once.
+__device__ __forceinline__ float cache_value(float scale, float zero, float code) { return fmaf(scale, code, zero); }
+
+__device__ __forceinline__ void unpack_sz(uint32_t sz, float& scale, float& zero) {
+  scale = __uint_as_float(sz << 16);
+  zero = __uint_as_float(sz & 0xffff0000u);
+}
+
+// Quantises the eight channels of this lane; the eight lanes of an aligned
+// group hold the 64 channels that share a scale and a zero. Returns the codes
+// packed in channel order (lowest bits first), replaces f by the values that
+// they stand for, and gives the (scale, zero) pair.
+//   z = bf16(min), s = bf16((max - z) * fl(1/15)), code = rint((x - z) * fl(1/s))
+// in float32. A scale below the smallest normal float32 becomes 0 (all codes
+// 0: the group reads back as its zero). A group with a NaN or infinity, or
+// with a range beyond float32, gets NaN for both and reads back as NaN.
+__device__ __forceinline__ uint32_t quantise_octet(float (&f)[8], uint32_t& sz) {
+  float mx = f[0], mn = f[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) mx = max_nan(mx, f[i]), mn = min_nan(mn, f[i]);
+#pragma unroll
+  for (int d = 1; d < 8; d *= 2) {
+    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, d));
+  }
+  const __nv_bfloat16 zb = __float2bfloat16_rn(mn);
+  float z = __bfloat162float(zb);
+  const float range = __fsub_rn(mx, z);
+  const __nv_bfloat16 sb = __float2bfloat16_rn(__fmul_rn(range, 1.0f / 15.0f));
+  float s = __bfloat162float(sb);
+  if (s < 1.17549435e-38f) s = 0.0f;  // a NaN stays
+  const bool finite = fabsf(range) < CUDART_INF_F;
+  const float inv = s > 0.0f && finite ? __frcp_rn(s) : 0.0f;
+  if (!finite) s = z = CUDART_NAN_F;
+  sz = (__float_as_uint(s) >> 16) | (__float_as_uint(z) & 0xffff0000u);
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // 12582912 = 1.5 * 2^23: adding it rounds to a whole number, half to even,
+    // and leaves that number in the low bits
+    float t = __fmul_rn(__fsub_rn(f[i], z), inv);
+    t = fminf(fmaxf(t, 0.0f), 15.0f);  // also turns a NaN (not finite: 0 * inf) into 0
+    t = __fadd_rn(t, 12582912.0f);
+    w |= (__float_as_uint(t) & 15u) << (4 * i);
+    f[i] = cache_value(s, z, __fsub_rn(t, 12582912.0f));
+  }
+  return w;
+}
+
+// ------------------------------------------------------------------ write
+//
+// One CTA per (sequence, block that the new tokens touch, key/value head). It
+// quantises the block's new rows and sums the keys of all its rows up to the
+// last new one, as the cache holds them, so that k_sum depends on the cache's
+// contents alone: not on how the tokens were cut into calls, nor on rows that a
+// later write with a smaller start has replaced. Row r of a tile belongs to a
+// fixed warp and lane group and the partial sums are joined in a fixed order.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) cache_write_kernel(const T* __restrict__ k, const T* __restrict__ v,
+                                                          uint8_t* cache, float* k_sum, CacheSeqs s, int Hkv,
+                                                          int nslot) {
+  constexpr int kOct = D / 8, kRows = 32 / kOct, kStep = 4 * kRows;
+  __shared__ float part[4][D];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int h = blockIdx.x % Hkv, slot = blockIdx.x / Hkv % nslot, b = blockIdx.x / Hkv / nslot;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, oct = lane % kOct;
+  int start, count;
+  seq_step(s, b, start, count);
+  const int block = start / s.bs + slot;
+  const int first = block * s.bs;                       // the block's first token
+  const int r0 = max(start - first, 0), r1 = min(start + count - first, s.bs);  // new rows
+  const int page = seq_page(s, b, block);
+  if (page < 0 || r1 <= r0) return;
+  float acc[8] = {};
+  for (int tile = 0; tile * kCacheTile < r1; ++tile) {
+    uint8_t* base = tile_ptr(cache, page, h, tile, Hkv, s.bs, D);
+    for (int r = warp * kRows + lane / kOct; r < kCacheTile; r += kStep) {
+      const int row = tile * kCacheTile + r;
+      uint32_t* kw = reinterpret_cast<uint32_t*>(base + r * (D / 2) + k_word(oct, D));
+      uint32_t* ks = reinterpret_cast<uint32_t*>(base + cache_ks_offset(D) + (r * (D / 64) + oct / 8) * 4);
+      float f[8] = {};
+      uint32_t sz = 0;
+      const bool fresh = row >= r0 && row < r1;
+      const long at = ((static_cast<long>(b) * s.T + (first + row - start)) * Hkv + h) * D + oct * 8;
+      if (fresh) load_octet(k + at, f);
+      uint32_t w = quantise_octet(f, sz);
+      if (fresh) {
+        *kw = w;
+        if (oct % 8 == 0) *ks = sz;
+      } else if (row < r0) {
+        w = *kw;
+        float sc, ze;
+        unpack_sz(*ks, sc, ze);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = cache_value(sc, ze, static_cast<float>((w >> (4 * i)) & 15u));
+      }
+      if (row < r1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += f[i];
+      }
+      if (fresh) load_octet(v + at, f);
+      w = quantise_octet(f, sz);
+      if (fresh) {
+        uint8_t* pair = base + cache_v_offset(D) + (r / 2) * D + (r % 2) * 2;
+        *reinterpret_cast<uint16_t*>(pair + v_word(r / 2, oct, 0, D)) = static_cast<uint16_t>(w);
+        *reinterpret_cast<uint16_t*>(pair + v_word(r / 2, oct, 1, D)) = static_cast<uint16_t>(w >> 16);
+        if (oct % 8 == 0)
+          *reinterpret_cast<uint32_t*>(base + cache_vs_offset(D) + (r * (D / 64) + oct / 8) * 4) = sz;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int d = kOct; d < 32; d *= 2) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], d);
+  }
+  if (lane < kOct) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part[warp][oct * 8 + i] = acc[i];
+  }
+  __syncthreads();
+  if (threadIdx.x < D)
+    k_sum[(static_cast<long>(page) * Hkv + h) * D + threadIdx.x] =
+        (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
+}
+
+// ------------------------------------------------------------------ read
+//
+// One thread per eight channels of a token's key and value.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) cache_read_kernel(const uint8_t* cache, T* k, T* v, CacheSeqs s, int Hkv,
+                                                         long total) {
+  constexpr int kOct = D / 8;
+  pdl_launch_dependents();
+  pdl_wait();
+  const long i = static_cast<long>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= total) return;
+  const int oct = static_cast<int>(i % kOct), h = static_cast<int>(i / kOct % Hkv);
+  const long row = i / kOct / Hkv;  // b * T + t
+  const int b = static_cast<int>(row / s.T), t = static_cast<int>(row % s.T);
+  int start, count;
+  seq_step(s, b, start, count);
+  if (t >= count) return;
+  const int pos = start + t, page = seq_page(s, b, pos / s.bs), r = pos % kCacheTile;
+  float kf[8] = {}, vf[8] = {};
+  if (page >= 0) {
+    const uint8_t* base =
+        tile_ptr(const_cast<uint8_t*>(cache), page, h, pos % s.bs / kCacheTile, Hkv, s.bs, D);
+    const uint32_t kw = *reinterpret_cast<const uint32_t*>(base + r * (D / 2) + k_word(oct, D));
+    const uint8_t* pair = base + cache_v_offset(D) + (r / 2) * D + (r % 2) * 2;
+    const uint32_t vw = *reinterpret_cast<const uint16_t*>(pair + v_word(r / 2, oct, 0, D)) |
+                        static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(pair + v_word(r / 2, oct, 1, D)))
+                            << 16;
+    const int at = (r * (D / 64) + oct / 8) * 4;
+    float ks, kz, vs, vz;
+    unpack_sz(*reinterpret_cast<const uint32_t*>(base + cache_ks_offset(D) + at), ks, kz);
+    unpack_sz(*reinterpret_cast<const uint32_t*>(base + cache_vs_offset(D) + at), vs, vz);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      kf[j] = cache_value(ks, kz, static_cast<float>((kw >> (4 * j)) & 15u));
+      vf[j] = cache_value(vs, vz, static_cast<float>((vw >> (4 * j)) & 15u));
+    }
+  }
+  store_octet(k + i * 8, kf);
+  store_octet(v + i * 8, vf);
+}
+
+// ------------------------------------------------------------------ block selection
+//
+// One CTA per (sequence, key/value head): scores of all its blocks into shared
+// memory, then the topk largest by a radix selection on order-preserving keys.
+// The scores' dot products run in float64 and are rounded to float32 once, so
+// that which blocks are kept does not depend on an order of summation.
+constexpr int kCacheSelThreads = 512;
+
+__device__ __forceinline__ uint32_t cache_score_key(float x) {
+  if (x != x) return 0xffffffffu;  // NaN above everything, as any comparison sort that keeps it has to put it somewhere
+  const uint32_t u = __float_as_uint(x + 0.0f);  // -0 as +0
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kCacheSelThreads) cache_topk_kernel(const T* __restrict__ q,
+                                                                      const float* __restrict__ k_sum, int32_t* idx,
+                                                                      CacheSeqs s, int H, int Hkv, int topk,
+                                                                      int force) {
+  extern __shared__ uint32_t keys[];  // [max_blocks]
+  __shared__ double qs[D];
+  __shared__ uint32_t hist[256];
+  __shared__ uint32_t warp_sum[kCacheSelThreads / 32];
+  __shared__ uint32_t sh_prefix, sh_need, sh_present;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int h = blockIdx.x % Hkv, b = blockIdx.x / Hkv, G = H / Hkv;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  int start, count;
+  seq_step(s, b, start, count);
+  const int total = min(start + count, s.max_blocks * s.bs);
+  const int n = (total + s.bs - 1) / s.bs;
+  for (int d = tid; d < D; d += kCacheSelThreads) {
+    double sum = 0;
+    for (int t = 0; t < count; ++t)
+      for (int g = 0; g < G; ++g)
+        sum += to_float(q[((static_cast<long>(b) * s.T + t) * H + h * G + g) * D + d]);
+    qs[d] = sum;
+  }
+  if (tid == 0) sh_present = 0;
+  __syncthreads();
+  for (int j = warp; j < n; j += kCacheSelThreads / 32) {
+    const int page = seq_page(s, b, j);
+    uint32_t key = 0;  // absent
+    if (page >= 0) {
+      const float* ks = k_sum + (static_cast<long>(page) * Hkv + h) * D;
+      double x = 0;
+      for (int d = lane; d < D; d += 32) x += qs[d] * ks[d];
+#pragma unroll
+      for (int o = 16; o; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
+      key = cache_score_key(static_cast<float>(x / min(s.bs, total - j * s.bs)));
+      if (force && (j + 1) * s.bs > start) key = 0xffffffffu;
+    }
+    if (lane == 0) {
+      keys[j] = key;
+      if (key) atomicAdd(&sh_present, 1u);
+    }
+  }
+  __syncthreads();
+  const uint32_t want = min(static_cast<uint32_t>(topk), sh_present);
+  // the want-th largest key, eight bits at a time
+  if (tid == 0) sh_prefix = 0, sh_need = want;
+  for (int shift = 24; shift >= 0 && want; shift -= 8) {
+    if (tid < 256) hist[tid] = 0;
+    __syncthreads();
+    const uint32_t prefix = sh_prefix, need = sh_need;
+    for (int j = tid; j < n; j += kCacheSelThreads)
+      if (shift == 24 || keys[j] >> (shift + 8) == prefix >> (shift + 8)) atomicAdd(&hist[keys[j] >> shift & 255u], 1u);
+    __syncthreads();
+    if (tid == 0) {
+      uint32_t above = 0;
+      int bin = 255;
+      while (bin > 0 && above + hist[bin] < need) above += hist[bin--];
+      sh_prefix = prefix | static_cast<uint32_t>(bin) << shift;
+      sh_need = need - above;
+    }
+    __syncthreads();
+  }
+  __syncthreads();
+  // ids in ascending order: all keys above the threshold and the first sh_need equal to it
+  const uint32_t thr = sh_prefix, ties = sh_need;
+  int32_t* out = idx + static_cast<long>(blockIdx.x) * topk;
+  uint32_t above_before = 0, equal_before = 0;
+  for (int j0 = 0; j0 < n && want; j0 += kCacheSelThreads) {
+    const uint32_t key = j0 + tid < n ? keys[j0 + tid] : 0u;
+    const uint32_t above = key > thr, equal = key == thr && key != 0;
+    const uint32_t ma = __ballot_sync(0xffffffffu, above), me = __ballot_sync(0xffffffffu, equal);
+    if (lane == 0) warp_sum[warp] = __popc(ma) | __popc(me) << 16;
+    __syncthreads();
+    uint32_t a = above_before, e = equal_before;
+    for (int w = 0; w < kCacheSelThreads / 32; ++w) {
+      if (w == warp) {
+        const uint32_t below = (1u << lane) - 1u;
+        const uint32_t ea = e + __popc(me & below), pos = a + __popc(ma & below) + min(ea, ties);
+        if (above || (equal && ea < ties)) out[pos] = j0 + tid;
+      }
+      a += warp_sum[w] & 0xffffu;
+      e += warp_sum[w] >> 16;
+    }
+    above_before = a, equal_before = e;
+    __syncthreads();
+  }
+  for (int j = want + tid; j < topk; j += kCacheSelThreads) out[j] = -1;
+}
+
+}  // namespace bsa

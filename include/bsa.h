@@ -406,6 +406,119 @@ bsa_status bsa_forward_noalloc(const void* q, const void* k, const void* v, void
                                int H, int D, int block_size, double topk_ratio, bsa_dtype dt,
                                void* stream);
 
+/* ---- The 4-bit key/value cache: attention for generation ----------------
+ * A generating model has the keys and values of all earlier tokens in a cache
+ * and brings one or a few new tokens a step. The cache is paged: one page
+ * holds one block of block_size tokens of all H_kv heads, as 4-bit codes with
+ * a bfloat16 scale and zero for each group of 64 channels of a token (4.5 bits
+ * an element). A step writes its keys and values (bsa_cache_write), may pick
+ * topk blocks for each (sequence, key/value head) from the blocks' key sums
+ * (bsa_cache_block_topk, the two-stage method for a step's queries) and
+ * attends over those blocks or over all (bsa_cache_attn); bsa_cache_forward
+ * does the three. bsa_cache_read gives keys and values back, for the prefill
+ * kernels or for another cache.
+ *
+ * Common arguments of the entry points:
+ *   cache [num_pages, H_kv, block_size / 64, 72 D] bytes: tiles of 64 tokens,
+ *     each 32 D bytes of key codes, 32 D of value codes, 4 D of key and 4 D of
+ *     value (scale, zero) pairs. Channel c of the key of the tile's token r is
+ *     in byte r D / 2 + ((c % 32) / 8) (D / 8) + (c / 32) 4 + (c % 8) / 2, of
+ *     its value in byte 32 D + (r / 2) D + (((c % 32) / 4) ^ (2 ((r / 2) % 4)))
+ *     (D / 8) + (c / 32) 4 + (r % 2) 2 + (c % 4) / 2, the low four bits for
+ *     even c. It stands for zero + scale * code.
+ *   k_sum [num_pages, H_kv, D] float32: sum of each page's keys (as the cache
+ *     holds them) over the tokens written.
+ *   page_table [B, max_blocks] int32: page of each block of each sequence. An
+ *     id outside [0, num_pages) marks an absent block: nothing is written
+ *     there, its rows read as zeros, it is never selected and no query sees
+ *     its tokens. Sequences may share pages that no call writes; two places of
+ *     one call's new tokens must not share a page.
+ *   start [B], count [B] int32: sequence b has start[b] tokens before this
+ *     step and brings the new tokens t < count[b] of T (count NULL: all T), at
+ *     positions start[b] + t. Rows t >= count[b] of a padded batch are neither
+ *     read nor written. start and count are device memory, so a captured
+ *     graph follows them. A negative start makes the sequence empty; count is
+ *     clamped to [0, T]; positions at or past max_blocks * block_size are absent.
+ *   dt: BSA_F32 or BSA_BF16 (BSA_E4M3: BSA_ERR_UNSUPPORTED), the type of q, k,
+ *     v, o [B, T, heads, D]. D 64 or 128, block_size 64, 128 or 256, H a
+ *     multiple of H_kv, max_blocks * block_size <= 2^30.
+ * page_table, start, count and idx need 4-byte alignment only. */
+
+/* Bytes of a cache; 0 if the arguments are invalid. Pure host function. */
+size_t bsa_cache_bytes(int num_pages, int H_kv, int D, int block_size);
+
+/* Writes the new tokens' keys and values ([B, T, H_kv, D], read) into the
+ * cache and renews k_sum of every page that got a token. Per group of 64
+ * channels x, in float32 arithmetic:
+ *   zero = bf16(min x), scale = bf16((max x - zero) * fl(1/15)) (0 where that
+ *   is below 2^-126), code = clamp(rint((x - zero) * fl(1/scale)), 0, 15),
+ *   rint to even. A group that holds a NaN or an infinity, or whose range
+ *   passes float32, gets NaN for scale and zero and reads back as NaN.
+ * k_sum is the float32 sum of the page's keys as they read back, over its
+ * tokens up to the call's last one: rewriting from a smaller start (tokens
+ * that were drafted and rejected) leaves no trace of the replaced rows, and
+ * the result does not depend on how the tokens were cut into calls. One kernel
+ * launch. */
+bsa_status bsa_cache_write(const void* k, const void* v, void* cache, float* k_sum, const int32_t* page_table,
+                           const int32_t* start, const int32_t* count, int B, int T, int H_kv, int D,
+                           int block_size, int num_pages, int max_blocks, bsa_dtype dt, void* stream);
+
+/* Reads back the tokens start[b] + t, t < count[b], as k and v [B, T, H_kv, D]
+ * (written): zero + scale * code in float32, rounded to dt. Rows of absent
+ * blocks are zeros; rows t >= count[b] are left as they are. One launch. */
+bsa_status bsa_cache_read(const void* cache, const int32_t* page_table, const int32_t* start, const int32_t* count,
+                          void* k, void* v, int B, int T, int H_kv, int D, int block_size, int num_pages,
+                          int max_blocks, bsa_dtype dt, void* stream);
+
+/* Selects blocks for the step's queries, per sequence and key/value head g:
+ *   S[b, g, j] = (sum over t < count[b] and the query heads of g of q) .
+ *                (k_sum of block j / tokens in block j)
+ * over the blocks j with tokens in [0, start[b] + count[b]), with the dot
+ * product in float64 and S rounded once to float32. idx [B, H_kv, topk]
+ * (written): the min(topk, present blocks) blocks of largest S, ties to the
+ * lower j (-0 ties with +0, NaN ranks first), ascending, padded with -1.
+ * flags: 0 or BSA_FLAG_CAUSAL (the cache is causal: no effect), and
+ * BSA_FLAG_CAUSAL | BSA_FLAG_FORCE_DIAG ranks the blocks that hold the step's
+ * new tokens above all others. max_blocks <= 49152. One launch. */
+bsa_status bsa_cache_block_topk(const void* q, const float* k_sum, const int32_t* page_table, const int32_t* start,
+                                const int32_t* count, int32_t* idx, int B, int T, int H, int H_kv, int D,
+                                int block_size, int num_pages, int max_blocks, int topk, bsa_dtype dt,
+                                unsigned flags, void* stream);
+
+/* Workspace bytes of bsa_cache_attn; 0 if the arguments are invalid. */
+size_t bsa_cache_attn_workspace_bytes(int B, int T, int H, int H_kv, int D);
+
+/* Attention over the cache: the query of token t sees the tokens at positions
+ * <= start[b] + t,
+ *   o[b, t, h, :] = sum_i softmax_i(scale * q[b, t, h, :] . k_i) v_i,
+ * over the blocks idx[b, h / (H / H_kv), 0..topk) (int32, each at most once;
+ * an entry outside [0, max_blocks) selects nothing), or over all blocks where
+ * idx is NULL. A row that sees no token gives zeros; rows t >= count[b] of o
+ * are left as they are. The new tokens' own keys and values are read from the
+ * cache: write them first. q, o: [B, T, H, D]; o must not be q. Scores, the
+ * softmax's sums and the output sums are float32; bfloat16 queries' softmax
+ * weights times the values' scales are rounded to float16 for the tensor cores
+ * (relative 2^-11), float32 queries' parts are split in two. workspace: device
+ * memory of bsa_cache_attn_workspace_bytes() bytes, 16-byte aligned, not used
+ * by an overlapping call. Deterministic. */
+bsa_status bsa_cache_attn(const void* q, const void* cache, const int32_t* page_table, const int32_t* start,
+                          const int32_t* count, const int32_t* idx, void* o, int B, int T, int H, int H_kv, int D,
+                          int block_size, int num_pages, int max_blocks, int topk, float scale, bsa_dtype dt,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of bsa_cache_forward: the index list [B, H_kv, topk] and the
+ * attention's workspace, each section 256-byte aligned; 0 if the arguments are
+ * invalid. */
+size_t bsa_cache_forward_workspace_bytes(int B, int T, int H, int H_kv, int D, int topk);
+
+/* One step of generation: bsa_cache_write of k and v, bsa_cache_block_topk
+ * (flags as there) and bsa_cache_attn over the selected blocks with scale =
+ * 1/sqrt(D); topk = 0 attends over all blocks. */
+bsa_status bsa_cache_forward(const void* q, const void* k, const void* v, void* cache, float* k_sum,
+                             const int32_t* page_table, const int32_t* start, const int32_t* count, void* o, int B,
+                             int T, int H, int H_kv, int D, int block_size, int num_pages, int max_blocks, int topk,
+                             bsa_dtype dt, unsigned flags, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* bsa_status_string(bsa_status s);
 
