@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -1282,9 +1283,61 @@ bsa_status check_tensors(std::initializer_list<const void*> ps) {
   return BSA_OK;
 }
 
+// The attention counts a call's tiles of 64 tokens in 32 bits, and without an
+// index list keeps a table of the sequences in shared memory.
+bsa_status check_attn_tiles(int B, int T, int H, int Hkv, int block_size, int max_blocks, int topk) {
+  if (!topk && B > bsa::kCaMaxSeqs)
+    return fail(BSA_ERR_UNSUPPORTED, "B=%d (attention over all blocks takes up to %d sequences)", B, bsa::kCaMaxSeqs);
+  const double units = static_cast<double>(B) * Hkv * ((static_cast<long long>(T) * (H / Hkv) + 7) / 8);
+  if (units * (topk ? topk : max_blocks) * (block_size / 64) > 2.1e9)
+    return fail(BSA_ERR_UNSUPPORTED, "more than 2.1e9 tiles of 64 tokens");
+  return BSA_OK;
+}
+
 bsa_status launched(cudaError_t e, const char* what) {
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? BSA_OK : cuda_fail(e, what);
+}
+
+// CTAs of the attention over the cache: all that fit the device at once.
+template <int NT>
+long cache_attn_ctas() {
+  return static_cast<long>(sm_count()) * bsa::CaShape<128, NT>::kCtas;
+}
+
+// 16 query rows a unit when a (sequence, key/value head) has more than 8: its
+// tiles are then read and unpacked half as often. float32 queries, whose
+// operands come in two parts, stay at 8 (registers).
+bool cache_attn_wide(int T, int H, int Hkv, bsa_dtype dt) {
+  return dt == BSA_BF16 && static_cast<long long>(T) * (H / Hkv) > 8;
+}
+
+template <typename E, int D, int NT>
+cudaError_t launch_cache_attn(const void* q, const void* cache, const int32_t* idx, void* o, void* ws,
+                              const bsa::CacheSeqs& seqs, int B, int H, int Hkv, int topk, float scale_log2,
+                              void* stream) {
+  using Shape = bsa::CaShape<D, NT>;
+  const auto kern = bsa::cache_attn_kernel<E, D, NT>;
+  static bool attr_set[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !attr_set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(Shape::smem(bsa::kCaMaxSeqs)));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr_set[dev] = true;
+  }
+  const int nseq = idx ? 0 : B;
+  const unsigned ctas = static_cast<unsigned>(cache_attn_ctas<NT>());
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      launch_pdl(kern, ctas, bsa::kCaThreads, Shape::smem(nseq), st, static_cast<const E*>(q),
+                 static_cast<const uint8_t*>(cache), idx, static_cast<E*>(o), static_cast<float*>(ws), seqs, B, H, Hkv,
+                 topk, scale_log2);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(bsa::cache_attn_join_kernel<E, D, NT>, static_cast<unsigned>(B) * seqs.T * H,
+                    bsa::kCaJoinWarps * 32, (nseq + 1) * sizeof(int), st, static_cast<E*>(o),
+                    static_cast<const float*>(ws), seqs, B, H, Hkv, idx ? topk : 0, static_cast<int>(ctas));
 }
 
 // Calls f with a value of the element type and the head size as a constant.
@@ -1384,7 +1437,9 @@ bsa_status bsa_cache_block_topk(const void* q, const float* k_sum, const int32_t
 
 size_t bsa_cache_attn_workspace_bytes(int B, int T, int H, int H_kv, int D) {
   if (check_cache_dims(B, T, H, H_kv, D, 64) != BSA_OK) return 0;
-  return 256;
+  // two parts of a unit's query rows for each CTA; float32 and bfloat16 queries alike
+  const long ctas = std::max(cache_attn_ctas<1>(), cache_attn_ctas<2>());
+  return static_cast<size_t>(ctas) * 2 * 16 * (D + 2) * sizeof(float);
 }
 
 bsa_status bsa_cache_attn(const void* q, const void* cache, const int32_t* page_table, const int32_t* start,
@@ -1395,6 +1450,7 @@ bsa_status bsa_cache_attn(const void* q, const void* cache, const int32_t* page_
   if ((s = check_cache(B, T, H, H_kv, D, block_size, num_pages, max_blocks, dt)) != BSA_OK) return s;
   if (idx && topk < 1) return fail(BSA_ERR_INVALID_ARG, "topk=%d must be positive", topk);
   if (!std::isfinite(scale) || scale <= 0.0f) return fail(BSA_ERR_INVALID_ARG, "scale must be positive and finite");
+  if ((s = check_attn_tiles(B, T, H, H_kv, block_size, max_blocks, idx ? topk : 0)) != BSA_OK) return s;
   if ((s = check_tensors({q, cache, o})) != BSA_OK) return s;
   if (o == q) return fail(BSA_ERR_INVALID_ARG, "o must not alias q");
   if ((s = check_cache_lists(page_table, start, count, idx)) != BSA_OK) return s;
@@ -1405,9 +1461,13 @@ bsa_status bsa_cache_attn(const void* q, const void* cache, const int32_t* page_
   const bsa::CacheSeqs seqs{page_table, start, count, T, num_pages, max_blocks, block_size};
   const cudaError_t e = by_type(dt, D, [&](auto t, auto d) {
     using E = decltype(t);
-    return launch_pdl(bsa::cache_attn_kernel<E, decltype(d)::value>, static_cast<unsigned>(B) * T * H, 128, 0,
-                      static_cast<cudaStream_t>(stream), static_cast<const E*>(q), static_cast<const uint8_t*>(cache),
-                      idx, static_cast<E*>(o), seqs, H, H_kv, topk, scale * 1.4426950408889634f);
+    constexpr int kD = decltype(d)::value;
+    const float sl = scale * 1.4426950408889634f;
+    if constexpr (sizeof(E) == 2) {
+      if (cache_attn_wide(T, H, H_kv, dt))
+        return launch_cache_attn<E, kD, 2>(q, cache, idx, o, workspace, seqs, B, H, H_kv, topk, sl, stream);
+    }
+    return launch_cache_attn<E, kD, 1>(q, cache, idx, o, workspace, seqs, B, H, H_kv, topk, sl, stream);
   });
   if ((s = launched(e, "cache_attn_kernel launch")) != BSA_OK) return s;
   return ok();
@@ -1432,6 +1492,7 @@ bsa_status bsa_cache_forward(const void* q, const void* k, const void* v, void* 
   if (topk < 0) return fail(BSA_ERR_INVALID_ARG, "topk=%d must not be negative", topk);
   if (topk && max_blocks > kCacheMaxBlocks)
     return fail(BSA_ERR_UNSUPPORTED, "max_blocks=%d (the selection holds up to %d)", max_blocks, kCacheMaxBlocks);
+  if ((s = check_attn_tiles(B, T, H, H_kv, block_size, max_blocks, topk)) != BSA_OK) return s;
   if ((s = check_tensors({q, k, v, cache, k_sum, o})) != BSA_OK) return s;
   if (o == q) return fail(BSA_ERR_INVALID_ARG, "o must not alias q");
   if ((s = check_cache_lists(page_table, start, count, nullptr)) != BSA_OK) return s;

@@ -1,82 +1,606 @@
 // cache_attn.cuh -- attention of a step's queries over the 4-bit cache.
+//
+// For the R = T G query rows of a (sequence, key/value head) and its tokens i,
+//   x = scale log2(e) q.k_i,  o = sum 2^(x - M) v_i / sum 2^(x - M).
+// With k = zero + scale code the score splits per group of 64 channels into
+//   q.k = k_scale (q . code) + k_zero (sum of q's channels),
+// and the output into sum p v_scale code + sum p v_zero, so the codes go to the
+// matrix instructions as they are and scales and zeros meet sums only. The
+// products run as S^T = K q^T and O^T = V^T P^T (m16n8k16, float16 in, float32
+// sums): 16 tokens or 16 channels fill the tall side, and as few as 8 query rows
+// the short one.
+//
+// The bound is the cache's bytes (4.5 bits an element, read once) as long as a
+// tile of 64 tokens costs fewer issue slots than its 72 D bytes cost time at the
+// memory rate, so the unpacking is kept at five instructions per eight codes: a
+// four-bit code in the low bits of a float16 is the subnormal number code 2^-24,
+// in bits 4..7 it is 16 code 2^-24, and both are exact operands. The factor 16 of
+// every other channel is taken out of the query (keys) or of the sums (values).
+// For float16's range each query row is scaled by a power of two, and the
+// reference M of a row keeps 2^(x - M) v_scale below 2^15.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "cache.cuh"
 
 namespace bsa {
 
-// One CTA per (sequence, key/value head, query row); a tile of 64 tokens at a
-// time: a thread per token for the scores, a thread per channel for the sums.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) cache_attn_kernel(const T* __restrict__ q, const uint8_t* cache,
-                                                         const int32_t* __restrict__ idx, T* o, CacheSeqs s, int H,
-                                                         int Hkv, int topk, float scale_log2) {
-  __shared__ float qs[D], p[kCacheTile], red[4];
+constexpr int kCaWarps = 4;                      // consumer warps: 16 of a tile's 64 tokens each
+constexpr int kCaThreads = (kCaWarps + 1) * 32;  // and the producer warp
+constexpr int kCaMaxSeqs = 4096;                 // sequences whose tile counts fit the table in shared memory
+
+template <int D, int NT>
+struct CaShape {
+  static constexpr int kRows = 8 * NT;  // query rows of a unit
+  static constexpr int kCtas = NT == 1 ? 3 : 2;  // CTAs of an SM
+  static constexpr int kOStride = D + 4;  // floats of a row in the join buffer: 16-byte stores free of conflicts
+  static constexpr int kJoinBytes = kCaWarps * kRows * kOStride * 4;
+  static constexpr int kStages = (NT == 1 ? 50 : 68) * 1024 / cache_tile_bytes(D);
+  static constexpr int kPartFloats = kRows * (D + 2);
+  static size_t smem(int nseq) {
+    return static_cast<size_t>(kStages) * cache_tile_bytes(D) + kJoinBytes + (nseq + 1) * sizeof(int);
+  }
+};
+
+__device__ __forceinline__ void bulk_load(void* smem, const void* gmem, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(smem)),
+               "l"(__cvta_generic_to_global(gmem)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// What packing to float16 left of lo and hi.
+__device__ __forceinline__ uint32_t pack_f16_rest(float lo, float hi, uint32_t packed) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&packed));
+  return pack_f16(lo - f.x, hi - f.y);
+}
+
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kCaWarps * 32) : "memory"); }
+
+// How the tiles of all units are laid in one line and cut into equal pieces, one
+// for each CTA. A unit is (sequence, key/value head, run of kRows query rows).
+struct CaPlan {
+  const int* prefix;  // without idx: tiles before sequence b, [B + 1]
+  int per_seq;        // units of a sequence
+  int row_tiles;      // units of a (sequence, head)
+  int tiles;          // with idx: tiles of every unit
+  int total, chunk;
+  int B;
+
+  __device__ __forceinline__ void locate(int x, int& b, int& unit, int& first, int& n) const {
+    if (tiles) {
+      const int u = x / tiles;
+      b = u / per_seq, unit = u % per_seq, first = u * tiles, n = tiles;
+      return;
+    }
+    int lo = 0, hi = B - 1;  // the last sequence whose tiles begin at or before x
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (prefix[mid] <= x)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    b = lo;
+    n = (prefix[b + 1] - prefix[b]) / per_seq;
+    unit = (x - prefix[b]) / n;
+    first = prefix[b] + unit * n;
+  }
+};
+
+// Fills the plan; `table` is shared memory for B + 1 integers (not used with idx).
+// All threads of the block call it; it ends with a barrier.
+__device__ __forceinline__ CaPlan make_plan(const CacheSeqs& s, int B, int Hkv, int row_tiles, int topk, int ctas,
+                                            int* table) {
+  CaPlan p;
+  p.prefix = table, p.row_tiles = row_tiles, p.per_seq = Hkv * row_tiles, p.B = B;
+  p.tiles = topk * (s.bs / kCacheTile);
+  if (topk) {
+    p.total = B * p.per_seq * p.tiles;
+    __syncthreads();
+  } else {
+    // warp 0 sums up the sequences' tiles, 32 at a time
+    if (threadIdx.x < 32) {
+      int sum = 0;
+      for (int b0 = 0; b0 < B; b0 += 32) {
+        const int b = b0 + threadIdx.x;
+        int n = 0;
+        if (b < B) {
+          int start, count;
+          seq_step(s, b, start, count);
+          if (count) n = (min(start + count, s.max_blocks * s.bs) + kCacheTile - 1) / kCacheTile * p.per_seq;
+        }
+        int before = n;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+          const int other = __shfl_up_sync(0xffffffffu, before, d);
+          if (threadIdx.x >= d) before += other;
+        }
+        if (b < B) table[b] = sum + before - n;
+        sum += __shfl_sync(0xffffffffu, before, 31);
+      }
+      if (threadIdx.x == 0) table[B] = sum;
+    }
+    __syncthreads();
+    p.total = table[B];
+  }
+  p.chunk = max(1, (p.total + ctas - 1) / ctas);
+  return p;
+}
+
+// Where a CTA leaves its part of a unit that other CTAs share: slot 0 for the
+// unit that began before the CTA's tiles, slot 1 for the one that begins among
+// them. Floats: references [kRows], weight sums [kRows], sums [kRows][D].
+template <int D, int NT>
+__device__ __forceinline__ float* part_of(float* ws, int cta, int slot) {
+  return ws + (static_cast<long>(cta) * 2 + slot) * CaShape<D, NT>::kPartFloats;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_out(T* o, float x) {
+  if constexpr (sizeof(T) == 2)
+    *o = __float2bfloat16_rn(x);
+  else
+    *o = x;
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
+    cache_attn_kernel(const T* __restrict__ q, const uint8_t* __restrict__ cache, const int32_t* __restrict__ idx, T* o,
+                      float* ws, CacheSeqs s, int B, int H, int Hkv, int topk, float scale_log2) {
+  using Shape = CaShape<D, NT>;
+  constexpr int kStages = Shape::kStages, kRows = Shape::kRows, kTile = cache_tile_bytes(D);
+  constexpr int kWords = D / 32, kGroups = D / 64;
+  constexpr int kSplit = sizeof(T) == 4 ? 2 : 1;  // float16 parts of a query element and of a weight
+  constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t* stages = smem;
+  float* join = reinterpret_cast<float*>(smem + kStages * kTile);
+  int* table = reinterpret_cast<int*>(smem + kStages * kTile + Shape::kJoinBytes);
+  __shared__ uint64_t full[kStages], empty[kStages];
+  __shared__ int tile_pos[kStages];  // position of the stage's first token; -1: the tile's block is absent
+  __shared__ float join_m[2][kCaWarps][kRows], join_l[2][kCaWarps][kRows];
+  __shared__ int abort_flag;
   pdl_launch_dependents();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, G = H / Hkv;
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kCaWarps);
+    }
+    fence_mbarrier_init();
+  }
   pdl_wait();
-  const int G = H / Hkv, tid = threadIdx.x;
-  const int row = blockIdx.x % (s.T * G), h = blockIdx.x / (s.T * G) % Hkv, b = blockIdx.x / (s.T * G) / Hkv;
-  const int t = row / G, head = h * G + row % G;
-  int start, count;
-  seq_step(s, b, start, count);
-  if (t >= count) return;
-  const int limit = min(start + t + 1, s.max_blocks * s.bs);  // tokens that the row sees
-  const long at = ((static_cast<long>(b) * s.T + t) * H + head) * D;
-  if (tid < D) qs[tid] = to_float(q[at + tid]) * scale_log2;
-  float m = -CUDART_INF_F, l = 0.0f, acc = 0.0f;
-  const int nblocks = idx ? topk : (limit + s.bs - 1) / s.bs;
-  for (int n = 0; n < nblocks; ++n) {
-    const int block = idx ? idx[(static_cast<long>(b) * Hkv + h) * topk + n] : n;
-    const int page = seq_page(s, b, block);
-    if (page < 0) continue;
-    for (int tile = 0; tile < s.bs / kCacheTile; ++tile) {
-      const int pos = block * s.bs + tile * kCacheTile;
-      if (pos >= limit) break;
-      const uint8_t* base = tile_ptr(const_cast<uint8_t*>(cache), page, h, tile, Hkv, s.bs, D);
-      __syncthreads();
-      float x = -CUDART_INF_F;
-      if (tid < kCacheTile && pos + tid < limit) {
-        x = 0.0f;
-        for (int oct = 0; oct < D / 8; ++oct) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(base + tid * (D / 2) + k_word(oct, D));
-          float sc, ze;
-          unpack_sz(*reinterpret_cast<const uint32_t*>(base + cache_ks_offset(D) + (tid * (D / 64) + oct / 8) * 4), sc,
-                    ze);
-          for (int i = 0; i < 8; ++i)
-            x += qs[oct * 8 + i] * cache_value(sc, ze, static_cast<float>((w >> (4 * i)) & 15u));
+  const CaPlan plan = make_plan(s, B, Hkv, (s.T * G + kRows - 1) / kRows, idx ? topk : 0, gridDim.x, table);
+  const int begin = min(static_cast<long>(blockIdx.x) * plan.chunk, static_cast<long>(plan.total));
+  const int end = min(begin + plan.chunk, plan.total);
+  volatile int* abort = &abort_flag;
+
+  if (warp == kCaWarps) {
+    // ---------------- producer: 32 tiles' addresses at a time, one lane each, then one copy after the other
+    int issued = 0;
+    for (int x0 = begin; x0 < end && !*abort; x0 += 32) {
+      const int x = x0 + lane;
+      int pos = -1;
+      const uint8_t* src = nullptr;
+      if (x < end) {
+        int b, unit, first, n;
+        plan.locate(x, b, unit, first, n);
+        const int h = unit / plan.row_tiles, tile = x - first, per = s.bs / kCacheTile;
+        int start, count;
+        seq_step(s, b, start, count);
+        const int block = idx ? idx[(static_cast<long>(b) * Hkv + h) * topk + tile / per] : tile / per;
+        const int page = count ? seq_page(s, b, block) : -1;
+        if (page >= 0) {
+          pos = block * s.bs + tile % per * kCacheTile;
+          src = tile_ptr(const_cast<uint8_t*>(cache), page, h, tile % per, Hkv, s.bs, D);
+          if (pos >= start + count) pos = -1;
         }
       }
-      float mx = x;
-      for (int d = 16; d; d /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-      if (tid % 32 == 0) red[tid / 32] = mx;
-      __syncthreads();
-      mx = fmaxf(m, fmaxf(red[0], red[1]));
-      const float ref = mx == -CUDART_INF_F ? 0.0f : mx;
-      if (tid < kCacheTile) p[tid] = exp2f(x - ref);
-      const float f = exp2f(m - ref);
-      m = mx;
-      __syncthreads();
-      l *= f, acc *= f;
-      for (int r = 0; r < kCacheTile && pos + r < limit; ++r) {
-        l += p[r];
-        if (tid < D) {
-          const int c = tid;
-          const uint16_t w = *reinterpret_cast<const uint16_t*>(base + cache_v_offset(D) + (r / 2) * D + (r % 2) * 2 +
-                                                                v_word(r / 2, c / 8, c / 4 % 2, D));
-          float sc, ze;
-          unpack_sz(*reinterpret_cast<const uint32_t*>(base + cache_vs_offset(D) + (r * (D / 64) + c / 64) * 4), sc,
-                    ze);
-          acc += p[r] * cache_value(sc, ze, static_cast<float>((w >> (4 * (c % 4))) & 15));
+      for (int i = 0; i < 32 && x0 + i < end; ++i, ++issued) {
+        const int p = __shfl_sync(0xffffffffu, pos, i);
+        const uint8_t* from = reinterpret_cast<const uint8_t*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i));
+        const int st = issued % kStages;
+        if (issued >= kStages && !mbar_wait(&empty[st], (issued / kStages - 1) & 1, abort, 801)) break;
+        if (lane == 0) {
+          tile_pos[st] = p;
+          if (p >= 0) {
+            mbar_arrive_expect_tx(&full[st], kTile);
+            bulk_load(stages + st * kTile, from, kTile, &full[st]);
+          } else {
+            mbar_arrive(&full[st]);
+          }
         }
+        __syncwarp();
+      }
+    }
+    if (*abort && lane == 0) {  // copies in flight end before the block's shared memory does
+      for (int i = max(0, issued - kStages); i < issued; ++i) mbar_wait_teardown(&full[i % kStages], i / kStages & 1);
+    }
+    return;
+  }
+
+  // ---------------- consumers
+  const int g = lane / 4, t4 = lane % 4;
+  int flushes = 0;
+  for (int x = begin; x < end;) {
+    int b, unit, first, n;
+    plan.locate(x, b, unit, first, n);
+    const int stop = min(first + n, end);
+    const int h = unit / plan.row_tiles, row0 = unit % plan.row_tiles * kRows;
+    int start, count;
+    seq_step(s, b, start, count);
+    const int rows = min(kRows, count * G - row0);  // rows with a query (may be <= 0)
+
+    // the queries as the products' second operand, and per row what a score is multiplied by
+    uint32_t qb[kSplit][kWords][2][NT][2];
+    float mul[NT][2], qsum[NT][2][kGroups];
+    int limit[NT][2];
+    int low_limit = 0x7fffffff;  // positions below it are seen by all rows
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + g;
+      float f[kWords][8], amax = 0.0f, sum[kGroups] = {};
+      const int row = row0 + r;
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {
+        if (r < rows) {
+          load_octet(q + ((static_cast<long>(b) * s.T + row / G) * H + h * G + row % G) * D + w * 32 + t4 * 8, f[w]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[w][i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[w][i])), sum[w / 2] += f[w][i];
+      }
+#pragma unroll
+      for (int d = 1; d < 4; d *= 2) {
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
+      }
+      // the largest element goes to [2^13, 2^14): float16 keeps 11 bits of every element down to 2^-27 of
+      // it, and parts of 2^-37 of it
+      const int up = min(13 - static_cast<int>((__float_as_uint(amax) >> 23) & 255u) + 127, 126);
+      const float qscale = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+      const float back = __uint_as_float(static_cast<uint32_t>(24 - up + 127) << 23) * scale_log2;
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[w][i] *= i % 2 ? qscale * 0.0625f : qscale;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          qb[0][w][k][nt][0] = pack_f16(f[w][2 * k], f[w][2 * k + 4]);
+          qb[0][w][k][nt][1] = pack_f16(f[w][2 * k + 1], f[w][2 * k + 5]);
+          if constexpr (kSplit == 2) {
+            qb[1][w][k][nt][0] = pack_f16_rest(f[w][2 * k], f[w][2 * k + 4], qb[0][w][k][nt][0]);
+            qb[1][w][k][nt][1] = pack_f16_rest(f[w][2 * k + 1], f[w][2 * k + 5], qb[0][w][k][nt][1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {  // this thread's scores belong to rows 2 t4 and 2 t4 + 1
+        const int from = (2 * t4 + c) * 4;
+        mul[nt][c] = __shfl_sync(0xffffffffu, back, from);
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) qsum[nt][c][j] = __shfl_sync(0xffffffffu, sum[j] * scale_log2, from);
+        const int rr = nt * 8 + 2 * t4 + c;
+        limit[nt][c] = rr < rows ? start + (row0 + rr) / G + 1 : 0;
+      }
+    }
+    low_limit = start + row0 / G + 1;
+
+    float m[NT][2], l[NT][2], z[NT][2][kGroups], acc[kWords][2][NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        m[nt][c] = -1e30f, l[nt][c] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) z[nt][c][j] = 0.0f;
+      }
+#pragma unroll
+      for (int w = 0; w < kWords; ++w)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[w][k][nt][i] = 0.0f;
+    }
+
+    for (; x < stop; ++x) {
+      const int st = (x - begin) % kStages;
+      const bool ok = mbar_wait(&full[st], ((x - begin) / kStages) & 1, abort, 802);
+      const int pos = ok ? tile_pos[st] : -1;
+      if (pos >= 0) {
+        const uint8_t* base = stages + st * kTile;
+        const int p0 = pos + warp * 16 + g;  // positions p0 and p0 + 8
+        const bool edge = pos + kCacheTile > low_limit;
+        float xs[NT][4];
+        {
+          uint32_t kw[2][kWords];
+          uint32_t ks[2][kGroups];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint8_t* at = base + (warp * 16 + i * 8) * (D / 2) + lane * (D / 8);
+            const uint8_t* sc = base + cache_ks_offset(D) + (warp * 16 + i * 8 + g) * (D / 16);
+            if constexpr (D == 128) {
+              const uint4 u = *reinterpret_cast<const uint4*>(at);
+              kw[i][0] = u.x, kw[i][1] = u.y, kw[i][2] = u.z, kw[i][3] = u.w;
+              const uint2 v = *reinterpret_cast<const uint2*>(sc);
+              ks[i][0] = v.x, ks[i][1] = v.y;
+            } else {
+              const uint2 u = *reinterpret_cast<const uint2*>(at);
+              kw[i][0] = u.x, kw[i][1] = u.y;
+              ks[i][0] = *reinterpret_cast<const uint32_t*>(sc);
+            }
+          }
+          float dot[kGroups][NT][4] = {};
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t u = kw[0][w] >> (8 * k), v = kw[1][w] >> (8 * k);
+              const uint32_t a0 = u & kLow, a1 = v & kLow, a2 = u & kHigh, a3 = v & kHigh;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int sp = 0; sp < kSplit; ++sp)
+                  mma_f16(dot[w / 2][nt], a0, a1, a2, a3, qb[sp][w][k][nt][0], qb[sp][w][k][nt][1]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float sc[kGroups], ze[kGroups];
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) unpack_sz(ks[i][j], sc[j], ze[j]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                float a = 0.0f, d = 0.0f;
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j) {
+                  d = fmaf(sc[j], dot[j][nt][2 * i + c], d);
+                  a = fmaf(ze[j], qsum[nt][c][j], a);
+                }
+                float v = fmaf(d, mul[nt][c], a);
+                if (edge && p0 + 8 * i >= limit[nt][c]) v = -CUDART_INF_F;
+                xs[nt][2 * i + c] = v;
+              }
+          }
+        }
+        // values' scales and zeros of the two tokens; what a row does not see must not count, not even as 0 * NaN
+        float vs[2][kGroups], vz[2][kGroups], vmax[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint8_t* sc = base + cache_vs_offset(D) + (warp * 16 + i * 8 + g) * (D / 16);
+          uint32_t u[kGroups];
+          if constexpr (D == 128) {
+            const uint2 v = *reinterpret_cast<const uint2*>(sc);
+            u[0] = v.x, u[1] = v.y;
+          } else {
+            u[0] = *reinterpret_cast<const uint32_t*>(sc);
+          }
+          vmax[i] = 0x1p-48f;
+#pragma unroll
+          for (int j = 0; j < kGroups; ++j) {
+            unpack_sz(u[j], vs[i][j], vz[i][j]);
+            vmax[i] = fmaxf(vmax[i], fabsf(vs[i][j]));
+          }
+        }
+        float p[NT][4];
+        float top = 0.0f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            p[nt][i] = fast_exp2(xs[nt][i] - m[nt][i % 2]);
+            top = fmaxf(top, p[nt][i] * vmax[i / 2]);
+          }
+        if (__any_sync(0xffffffffu, top > 32768.0f)) {
+          // raise the references so that the largest weight times scale is 2^12
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float u = fmaxf(xs[nt][c] + __log2f(vmax[0]), xs[nt][2 + c] + __log2f(vmax[1]));
+#pragma unroll
+              for (int d = 4; d < 32; d *= 2) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, d));
+              const float now = fmaxf(m[nt][c], u - 12.0f), f = fast_exp2(m[nt][c] - now);
+              m[nt][c] = now;
+              l[nt][c] *= f;
+#pragma unroll
+              for (int j = 0; j < kGroups; ++j) z[nt][c][j] *= f;
+#pragma unroll
+              for (int w = 0; w < kWords; ++w)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) acc[w][k][nt][c] *= f, acc[w][k][nt][2 + c] *= f;
+              p[nt][c] = fast_exp2(xs[nt][c] - now);
+              p[nt][2 + c] = fast_exp2(xs[nt][2 + c] - now);
+            }
+        }
+        uint32_t pb[kSplit][kGroups][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) l[nt][c] += p[nt][c] + p[nt][2 + c];
+#pragma unroll
+          for (int j = 0; j < kGroups; ++j) {
+            float w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              w[i] = p[nt][i] * vs[i / 2][j];
+              float zi = p[nt][i] * vz[i / 2][j];
+              if (edge && p0 + 8 * (i / 2) >= limit[nt][i % 2]) w[i] = zi = 0.0f;
+              z[nt][i % 2][j] += zi;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t u = pack_f16(w[2 * i], w[2 * i + 1]);
+              pb[0][j][nt][i] = transpose8x8(u);
+              if constexpr (kSplit == 2) pb[1][j][nt][i] = transpose8x8(pack_f16_rest(w[2 * i], w[2 * i + 1], u));
+            }
+          }
+        }
+        uint32_t vw[2][kWords];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint8_t* at = base + cache_v_offset(D) + (warp * 8 + t4 + 4 * i) * D + (g ^ (2 * t4)) * (D / 8);
+          if constexpr (D == 128) {
+            const uint4 u = *reinterpret_cast<const uint4*>(at);
+            vw[i][0] = u.x, vw[i][1] = u.y, vw[i][2] = u.z, vw[i][3] = u.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(at);
+            vw[i][0] = u.x, vw[i][1] = u.y;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < kWords; ++w)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t u = vw[0][w] >> (8 * k), v = vw[1][w] >> (8 * k);
+            const uint32_t a0 = u & kLow, a1 = u & kHigh, a2 = v & kLow, a3 = v & kHigh;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int sp = 0; sp < kSplit; ++sp)
+                mma_f16(acc[w][k][nt], a0, a1, a2, a3, pb[sp][w / 2][nt][0], pb[sp][w / 2][nt][1]);
+          }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+    }
+
+    // ---------------- the unit's part of this CTA: the warps' sums joined in a fixed order
+    const int fb = flushes++ & 1;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int d = 4; d < 32; d *= 2) {
+          l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], d);
+#pragma unroll
+          for (int j = 0; j < kGroups; ++j) z[nt][c][j] += __shfl_xor_sync(0xffffffffu, z[nt][c][j], d);
+        }
+        if (g == 0) {
+          join_m[fb][warp][nt * 8 + 2 * t4 + c] = m[nt][c];
+          join_l[fb][warp][nt * 8 + 2 * t4 + c] = l[nt][c];
+        }
+      }
+    consumer_sync();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = nt * 8 + 2 * t4 + c;
+        float top = join_m[fb][0][r];
+#pragma unroll
+        for (int w = 1; w < kCaWarps; ++w) top = fmaxf(top, join_m[fb][w][r]);
+        const float f = fast_exp2(m[nt][c] - top);
+        float* to = join + (warp * kRows + r) * Shape::kOStride + 4 * g;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+          const float zz = z[nt][c][w / 2] * f, f0 = f * 0x1p24f, f1 = f * 0x1p20f;
+          *reinterpret_cast<float4*>(to + w * 32) =
+              make_float4(fmaf(acc[w][0][nt][c], f0, zz), fmaf(acc[w][0][nt][2 + c], f1, zz),
+                          fmaf(acc[w][1][nt][c], f0, zz), fmaf(acc[w][1][nt][2 + c], f1, zz));
+        }
+      }
+    consumer_sync();
+    const bool whole = first >= begin && first + n <= end;
+    float* part = part_of<D, NT>(ws, blockIdx.x, first < begin ? 0 : 1);
+    for (int i = threadIdx.x; i < rows * D; i += kCaWarps * 32) {
+      const int r = i / D, c = i % D;
+      float top = join_m[fb][0][r], sum = 0.0f, val = 0.0f;
+#pragma unroll
+      for (int w = 1; w < kCaWarps; ++w) top = fmaxf(top, join_m[fb][w][r]);
+#pragma unroll
+      for (int w = 0; w < kCaWarps; ++w) {
+        sum += join_l[fb][w][r] * fast_exp2(join_m[fb][w][r] - top);
+        val += join[(w * kRows + r) * Shape::kOStride + c];
+      }
+      if (whole) {
+        const int row = row0 + r;
+        store_out(o + ((static_cast<long>(b) * s.T + row / G) * H + h * G + row % G) * D + c,
+                  sum == 0.0f ? 0.0f : val / sum);
+      } else {
+        if (c == 0) part[r] = top, part[kRows + r] = sum;
+        part[2 * kRows + r * D + c] = val;
       }
     }
   }
-  if (tid < D) {
-    const float r = l > 0.0f || l != l ? acc / l : 0.0f;
-    if constexpr (sizeof(T) == 2)
-      o[at + tid] = __float2bfloat16_rn(r);
-    else
-      o[at + tid] = r;
+}
+
+// Joins the parts of the units that several CTAs share: one CTA per query row,
+// its 8 warps taking the parts in turn and meeting in a fixed order.
+constexpr int kCaJoinWarps = 8;
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kCaJoinWarps * 32)
+    cache_attn_join_kernel(T* o, const float* ws, CacheSeqs s, int B, int H, int Hkv, int topk, int ctas) {
+  using Shape = CaShape<D, NT>;
+  constexpr int kPer = D / 32;  // channels of a lane
+  extern __shared__ int table[];
+  __shared__ float sums[kCaJoinWarps][D], weights[kCaJoinWarps], tops[kCaJoinWarps];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int G = H / Hkv, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int row_tiles = (s.T * G + Shape::kRows - 1) / Shape::kRows;
+  const CaPlan plan = make_plan(s, B, Hkv, row_tiles, topk, ctas, table);
+  const int row = blockIdx.x % (s.T * G), h = blockIdx.x / (s.T * G) % Hkv, b = blockIdx.x / (s.T * G) / Hkv;
+  int start, count;
+  seq_step(s, b, start, count);
+  if (row / G >= count) return;
+  const int unit = h * row_tiles + row / Shape::kRows, r = row % Shape::kRows;
+  const int n = plan.tiles ? plan.tiles : (plan.prefix[b + 1] - plan.prefix[b]) / plan.per_seq;
+  const int first = (plan.tiles ? b * plan.per_seq * n : plan.prefix[b]) + unit * n;
+  const int c0 = first / plan.chunk, c1 = (first + n - 1) / plan.chunk;
+  if (c0 == c1) return;
+  float top = -1e30f;
+  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, part_of<D, NT>(const_cast<float*>(ws), c, c == c0)[r]);
+#pragma unroll
+  for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  float val[kPer] = {}, weight = 0.0f;
+#pragma unroll 4
+  for (int c = c0 + warp; c <= c1; c += kCaJoinWarps) {
+    const float* part = part_of<D, NT>(const_cast<float*>(ws), c, c == c0);
+    const float f = fast_exp2(part[r] - top);
+    weight += part[Shape::kRows + r] * f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) val[i] = fmaf(part[2 * Shape::kRows + r * D + lane * kPer + i], f, val[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) sums[warp][lane * kPer + i] = val[i];
+  if (lane == 0) weights[warp] = weight;
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float v = 0.0f, w = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kCaJoinWarps; ++i) v += sums[i][threadIdx.x], w += weights[i];
+    store_out(o + ((static_cast<long>(b) * s.T + row / G) * H + h * G + row % G) * D + threadIdx.x,
+              w == 0.0f ? 0.0f : v / w);
   }
 }
 
