@@ -26,7 +26,7 @@
 
 namespace bsa {
 
-constexpr int kCaWarps = 4;                      // consumer warps: 16 of a tile's 64 tokens each
+constexpr int kCaWarps = 4;                      // consumer warps, in two pairs: a tile goes to a pair
 constexpr int kCaThreads = (kCaWarps + 1) * 32;  // and the producer warp
 constexpr int kCaMaxSeqs = 4096;                 // sequences whose tile counts fit the table in shared memory
 
@@ -56,6 +56,28 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// N consecutive 32-bit words of shared memory, in one load.
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  } else if constexpr (N == 2) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x, w[1] = u.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -171,6 +193,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
   constexpr int kStages = Shape::kStages, kRows = Shape::kRows, kTile = cache_tile_bytes(D);
   constexpr int kWords = D / 32, kGroups = D / 64;
   constexpr int kSplit = sizeof(T) == 4 ? 2 : 1;  // float16 parts of a query element and of a weight
+  constexpr int kJoint = NT * kSplit == 1 ? 2 : 1;  // runs of 16 tokens computed together
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* stages = smem;
@@ -186,7 +209,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
     abort_flag = 0;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kCaWarps);
+      mbar_init(&empty[i], 2);
     }
     fence_mbarrier_init();
   }
@@ -243,7 +266,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
 
   // ---------------- consumers
   const int g = lane / 4, t4 = lane % 4;
-  int flushes = 0;
+  int flushes = 0, stage = 0, phase = 0;
   for (int x = begin; x < end;) {
     int b, unit, first, n;
     plan.locate(x, b, unit, first, n);
@@ -255,7 +278,8 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
 
     // the queries as the products' second operand, and per row what a score is multiplied by
     uint32_t qb[kSplit][kWords][2][NT][2];
-    float mul[NT][2], qsum[NT][2][kGroups];
+    uint32_t zb[NT][2];
+    float mul[NT][2];
     int limit[NT][2];
     int low_limit = 0x7fffffff;  // positions below it are seen by all rows
 #pragma unroll
@@ -299,12 +323,27 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
           }
         }
       }
+      // second operand of zero . (sum of q's channels): a token's (scale, zero) words are the first, group t4 % 2's
+      // in this thread's columns, and the sum meets the zero half in up to four bfloat16 parts
+      {
+        float rest = (kGroups == 2 && t4 % 2 ? sum[kGroups - 1] : sum[0]) * scale_log2;
+        uint32_t parts[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat16 h = __float2bfloat16_rn(rest);
+          parts[i] = static_cast<uint32_t>(__bfloat16_as_ushort(h)) << 16;
+          rest -= __bfloat162float(h);
+        }
+        if (kGroups == 2) {
+          zb[nt][0] = parts[t4 / 2], zb[nt][1] = parts[2 + t4 / 2];
+        } else {
+          zb[nt][0] = parts[t4], zb[nt][1] = 0;
+        }
+      }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {  // this thread's scores belong to rows 2 t4 and 2 t4 + 1
         const int from = (2 * t4 + c) * 4;
         mul[nt][c] = __shfl_sync(0xffffffffu, back, from);
-#pragma unroll
-        for (int j = 0; j < kGroups; ++j) qsum[nt][c][j] = __shfl_sync(0xffffffffu, sum[j] * scale_log2, from);
         const int rr = nt * 8 + 2 * t4 + c;
         limit[nt][c] = rr < rows ? start + (row0 + rr) / G + 1 : 0;
       }
@@ -328,153 +367,126 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
           for (int i = 0; i < 4; ++i) acc[w][k][nt][i] = 0.0f;
     }
 
-    for (; x < stop; ++x) {
-      const int st = (x - begin) % kStages;
-      const bool ok = mbar_wait(&full[st], ((x - begin) / kStages) & 1, abort, 802);
-      const int pos = ok ? tile_pos[st] : -1;
-      if (pos >= 0) {
-        const uint8_t* base = stages + st * kTile;
-        const int p0 = pos + warp * 16 + g;  // positions p0 and p0 + 8
-        const bool edge = pos + kCacheTile > low_limit;
-        float xs[NT][4];
-        {
-          uint32_t kw[2][kWords];
-          uint32_t ks[2][kGroups];
+    // kJoint runs of 16 tokens of a tile, from row r0: their scores, weights and sums. kEdge: some row does not see
+    // some token.
+    auto tokens = [&](const uint8_t* base, int pos, int r0, auto edge) {
+      constexpr bool kEdge = decltype(edge)::value;
+      float xs[kJoint][NT][4], vmax[kJoint][2];
+      uint32_t vsz[kJoint][2][kGroups];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint8_t* at = base + (warp * 16 + i * 8) * (D / 2) + lane * (D / 8);
-            const uint8_t* sc = base + cache_ks_offset(D) + (warp * 16 + i * 8 + g) * (D / 16);
-            if constexpr (D == 128) {
-              const uint4 u = *reinterpret_cast<const uint4*>(at);
-              kw[i][0] = u.x, kw[i][1] = u.y, kw[i][2] = u.z, kw[i][3] = u.w;
-              const uint2 v = *reinterpret_cast<const uint2*>(sc);
-              ks[i][0] = v.x, ks[i][1] = v.y;
-            } else {
-              const uint2 u = *reinterpret_cast<const uint2*>(at);
-              kw[i][0] = u.x, kw[i][1] = u.y;
-              ks[i][0] = *reinterpret_cast<const uint32_t*>(sc);
-            }
-          }
-          float dot[kGroups][NT][4] = {};
+      for (int e = 0; e < kJoint; ++e) {
+        const int r = r0 + 16 * e;
+        uint32_t kw[2][kWords], ksz[2][kGroups], zw[2];
 #pragma unroll
-          for (int w = 0; w < kWords; ++w) {
+        for (int i = 0; i < 2; ++i) {
+          load_words<kWords>(base + (r + i * 8) * (D / 2) + lane * (D / 8), kw[i]);
+          const uint8_t* sz = base + cache_ks_offset(D) + (r + i * 8 + g) * (D / 16);
+          load_words<kGroups>(sz, ksz[i]);
+          zw[i] = kGroups == 2 && t4 % 2 ? ksz[i][kGroups - 1] : ksz[i][0];
+        }
+        float dot[kGroups][NT][4] = {}, zero[NT][4] = {};
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t u = kw[0][w] >> (8 * k), v = kw[1][w] >> (8 * k);
-              const uint32_t a0 = u & kLow, a1 = v & kLow, a2 = u & kHigh, a3 = v & kHigh;
+        for (int nt = 0; nt < NT; ++nt) mma_bf16(zero[nt], zw[0], zw[1], zw[0], zw[1], zb[nt][0], zb[nt][1]);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+        for (int w = 0; w < kWords; ++w) {
 #pragma unroll
-                for (int sp = 0; sp < kSplit; ++sp)
-                  mma_f16(dot[w / 2][nt], a0, a1, a2, a3, qb[sp][w][k][nt][0], qb[sp][w][k][nt][1]);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float sc[kGroups], ze[kGroups];
-#pragma unroll
-            for (int j = 0; j < kGroups; ++j) unpack_sz(ks[i][j], sc[j], ze[j]);
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t u = kw[0][w] >> (8 * k), v = kw[1][w] >> (8 * k);
+            const uint32_t a0 = u & kLow, a1 = v & kLow, a2 = u & kHigh, a3 = v & kHigh;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                float a = 0.0f, d = 0.0f;
-#pragma unroll
-                for (int j = 0; j < kGroups; ++j) {
-                  d = fmaf(sc[j], dot[j][nt][2 * i + c], d);
-                  a = fmaf(ze[j], qsum[nt][c][j], a);
-                }
-                float v = fmaf(d, mul[nt][c], a);
-                if (edge && p0 + 8 * i >= limit[nt][c]) v = -CUDART_INF_F;
-                xs[nt][2 * i + c] = v;
-              }
+              for (int sp = 0; sp < kSplit; ++sp)
+                mma_f16(dot[w / 2][nt], a0, a1, a2, a3, qb[sp][w][k][nt][0], qb[sp][w][k][nt][1]);
           }
         }
-        // values' scales and zeros of the two tokens; what a row does not see must not count, not even as 0 * NaN
-        float vs[2][kGroups], vz[2][kGroups], vmax[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint8_t* sc = base + cache_vs_offset(D) + (warp * 16 + i * 8 + g) * (D / 16);
-          uint32_t u[kGroups];
-          if constexpr (D == 128) {
-            const uint2 v = *reinterpret_cast<const uint2*>(sc);
-            u[0] = v.x, u[1] = v.y;
-          } else {
-            u[0] = *reinterpret_cast<const uint32_t*>(sc);
-          }
-          vmax[i] = 0x1p-48f;
+          load_words<kGroups>(base + cache_vs_offset(D) + (r + i * 8 + g) * (D / 16), vsz[e][i]);
+          vmax[e][i] = 0x1p-48f;
 #pragma unroll
-          for (int j = 0; j < kGroups; ++j) {
-            unpack_sz(u[j], vs[i][j], vz[i][j]);
-            vmax[i] = fmaxf(vmax[i], fabsf(vs[i][j]));
-          }
-        }
-        float p[NT][4];
-        float top = 0.0f;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            p[nt][i] = fast_exp2(xs[nt][i] - m[nt][i % 2]);
-            top = fmaxf(top, p[nt][i] * vmax[i / 2]);
-          }
-        if (__any_sync(0xffffffffu, top > 32768.0f)) {
-          // raise the references so that the largest weight times scale is 2^12
+          for (int j = 0; j < kGroups; ++j) vmax[e][i] = fmaxf(vmax[e][i], fabsf(__uint_as_float(vsz[e][i][j] << 16)));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float u = fmaxf(xs[nt][c] + __log2f(vmax[0]), xs[nt][2 + c] + __log2f(vmax[1]));
-#pragma unroll
-              for (int d = 4; d < 32; d *= 2) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, d));
-              const float now = fmaxf(m[nt][c], u - 12.0f), f = fast_exp2(m[nt][c] - now);
-              m[nt][c] = now;
-              l[nt][c] *= f;
-#pragma unroll
-              for (int j = 0; j < kGroups; ++j) z[nt][c][j] *= f;
-#pragma unroll
-              for (int w = 0; w < kWords; ++w)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) acc[w][k][nt][c] *= f, acc[w][k][nt][2 + c] *= f;
-              p[nt][c] = fast_exp2(xs[nt][c] - now);
-              p[nt][2 + c] = fast_exp2(xs[nt][2 + c] - now);
+              float d = __uint_as_float(ksz[i][0] << 16) * dot[0][nt][2 * i + c];
+              if constexpr (kGroups == 2) d = fmaf(__uint_as_float(ksz[i][1] << 16), dot[1][nt][2 * i + c], d);
+              float v = fmaf(d, mul[nt][c], zero[nt][2 * i + c]);
+              if (kEdge && pos + r + 8 * i + g >= limit[nt][c]) v = -CUDART_INF_F;
+              xs[e][nt][2 * i + c] = v;
             }
         }
+      }
+      float p[kJoint][NT][4], top = 0.0f;
+#pragma unroll
+      for (int e = 0; e < kJoint; ++e)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            p[e][nt][i] = fast_exp2(xs[e][nt][i] - m[nt][i % 2]);
+            top = fmaxf(top, p[e][nt][i] * vmax[e][i / 2]);
+          }
+      if (__any_sync(0xffffffffu, top > 32768.0f)) {
+        // raise the references so that the largest weight times scale is 2^12
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float u = -CUDART_INF_F;
+#pragma unroll
+            for (int e = 0; e < kJoint; ++e)
+              u = fmaxf(u, fmaxf(xs[e][nt][c] + __log2f(vmax[e][0]), xs[e][nt][2 + c] + __log2f(vmax[e][1])));
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, d));
+            const float now = fmaxf(m[nt][c], u - 12.0f), f = fast_exp2(m[nt][c] - now);
+            m[nt][c] = now;
+            l[nt][c] *= f;
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) z[nt][c][j] *= f;
+#pragma unroll
+            for (int w = 0; w < kWords; ++w)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) acc[w][k][nt][c] *= f, acc[w][k][nt][2 + c] *= f;
+#pragma unroll
+            for (int e = 0; e < kJoint; ++e) {
+              p[e][nt][c] = fast_exp2(xs[e][nt][c] - now);
+              p[e][nt][2 + c] = fast_exp2(xs[e][nt][2 + c] - now);
+            }
+          }
+      }
+#pragma unroll
+      for (int e = 0; e < kJoint; ++e) {
+        const int r = r0 + 16 * e;
         uint32_t pb[kSplit][kGroups][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) l[nt][c] += p[nt][c] + p[nt][2 + c];
+          for (int c = 0; c < 2; ++c) l[nt][c] += p[e][nt][c] + p[e][nt][2 + c];
 #pragma unroll
           for (int j = 0; j < kGroups; ++j) {
-            float w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              w[i] = p[nt][i] * vs[i / 2][j];
-              float zi = p[nt][i] * vz[i / 2][j];
-              if (edge && p0 + 8 * (i / 2) >= limit[nt][i % 2]) w[i] = zi = 0.0f;
-              z[nt][i % 2][j] += zi;
-            }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint32_t u = pack_f16(w[2 * i], w[2 * i + 1]);
+              float vs, vz, w[2];
+              unpack_sz(vsz[e][i][j], vs, vz);
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                // what a row does not see must not count, not even as 0 * NaN
+                const bool seen = !kEdge || pos + r + 8 * i + g < limit[nt][c];
+                w[c] = seen ? p[e][nt][2 * i + c] * vs : 0.0f;
+                if (seen) z[nt][c][j] = fmaf(p[e][nt][2 * i + c], vz, z[nt][c][j]);
+              }
+              const uint32_t u = pack_f16(w[0], w[1]);
               pb[0][j][nt][i] = transpose8x8(u);
-              if constexpr (kSplit == 2) pb[1][j][nt][i] = transpose8x8(pack_f16_rest(w[2 * i], w[2 * i + 1], u));
+              if constexpr (kSplit == 2) pb[1][j][nt][i] = transpose8x8(pack_f16_rest(w[0], w[1], u));
             }
           }
         }
         uint32_t vw[2][kWords];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint8_t* at = base + cache_v_offset(D) + (warp * 8 + t4 + 4 * i) * D + (g ^ (2 * t4)) * (D / 8);
-          if constexpr (D == 128) {
-            const uint4 u = *reinterpret_cast<const uint4*>(at);
-            vw[i][0] = u.x, vw[i][1] = u.y, vw[i][2] = u.z, vw[i][3] = u.w;
-          } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(at);
-            vw[i][0] = u.x, vw[i][1] = u.y;
-          }
-        }
+        for (int i = 0; i < 2; ++i)
+          load_words<kWords>(base + cache_v_offset(D) + (r / 2 + t4 + 4 * i) * D + (g ^ (2 * t4)) * (D / 8), vw[i]);
 #pragma unroll
         for (int w = 0; w < kWords; ++w)
 #pragma unroll
@@ -487,6 +499,25 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
               for (int sp = 0; sp < kSplit; ++sp)
                 mma_f16(acc[w][k][nt], a0, a1, a2, a3, pb[sp][w / 2][nt][0], pb[sp][w / 2][nt][1]);
           }
+      }
+    };
+
+    // a tile goes to one pair of warps, 32 tokens each; the pairs take the CTA's tiles in turn
+    for (; x < stop; ++x) {
+      const int st = stage, ph = phase;
+      if (++stage == kStages) stage = 0, phase ^= 1;
+      if (((x - begin) & 1) != warp / 2) continue;
+      const int pos = mbar_wait(&full[st], ph, abort, 802) ? tile_pos[st] : -1;
+      if (pos >= 0) {
+        const uint8_t* base = stages + st * kTile;
+        const bool edge = pos + kCacheTile > low_limit;
+        for (int half = 0; half < 2 / kJoint; ++half) {
+          const int r0 = (warp % 2) * 32 + half * 16;
+          if (edge)
+            tokens(base, pos, r0, std::true_type{});
+          else
+            tokens(base, pos, r0, std::false_type{});
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
