@@ -36,7 +36,10 @@ struct CaShape {
   static constexpr int kCtas = NT == 1 ? 3 : 2;  // CTAs of an SM
   static constexpr int kOStride = D + 4;  // floats of a row in the join buffer: 16-byte stores free of conflicts
   static constexpr int kJoinBytes = kCaWarps * kRows * kOStride * 4;
-  static constexpr int kStages = (NT == 1 ? 50 : 68) * 1024 / cache_tile_bytes(D);
+  // Even, so that a stage always serves the same pair of warps: a pair then waits for a stage's next fill only
+  // after it has used the last one (a wait by parity cannot tell the fill to come from the one before the last).
+  static constexpr int kStages = (NT == 1 ? 6 : 8) * 128 / D;
+  static_assert(kStages % 2 == 0);
   static constexpr int kPartFloats = kRows * (D + 2);
   static size_t smem(int nseq) {
     return static_cast<size_t>(kStages) * cache_tile_bytes(D) + kJoinBytes + (nseq + 1) * sizeof(int);
@@ -58,26 +61,33 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
+// The same without a sum to add to, and of bfloat16 operands.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma_bf16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // N consecutive 32-bit words of shared memory, in one load.
 template <int N>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
-  if constexpr (N == 4) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-  } else if constexpr (N == 2) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    w[0] = u.x, w[1] = u.y;
-  } else {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
-  }
+__device__ __forceinline__ void load_words(uint32_t p, uint32_t (&w)[N]) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(p));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(p));
+  else
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(p));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -266,7 +276,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
 
   // ---------------- consumers
   const int g = lane / 4, t4 = lane % 4;
-  int flushes = 0, stage = 0, phase = 0;
+  int flushes = 0, phase = 0, stage = warp / 2, mine = begin + stage;  // this pair's next tile and its place
   for (int x = begin; x < end;) {
     int b, unit, first, n;
     plan.locate(x, b, unit, first, n);
@@ -331,13 +341,13 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const __nv_bfloat16 h = __float2bfloat16_rn(rest);
-          parts[i] = static_cast<uint32_t>(__bfloat16_as_ushort(h)) << 16;
+          parts[i] = static_cast<uint32_t>(__bfloat16_as_ushort(h)) << 16;  // the zero half
           rest -= __bfloat162float(h);
         }
         if (kGroups == 2) {
-          zb[nt][0] = parts[t4 / 2], zb[nt][1] = parts[2 + t4 / 2];
+          zb[nt][0] = t4 < 2 ? parts[0] : parts[1], zb[nt][1] = t4 < 2 ? parts[2] : parts[3];
         } else {
-          zb[nt][0] = parts[t4], zb[nt][1] = 0;
+          zb[nt][0] = t4 < 2 ? (t4 ? parts[1] : parts[0]) : (t4 == 2 ? parts[2] : parts[3]), zb[nt][1] = 0;
         }
       }
 #pragma unroll
@@ -369,9 +379,9 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
 
     // kJoint runs of 16 tokens of a tile, from row r0: their scores, weights and sums. kEdge: some row does not see
     // some token.
-    auto tokens = [&](const uint8_t* base, int pos, int r0, auto edge) {
+    auto tokens = [&](uint32_t base, int pos, int r0, auto edge) {
       constexpr bool kEdge = decltype(edge)::value;
-      float xs[kJoint][NT][4], vmax[kJoint][2];
+      float xs[kJoint][NT][4];
       uint32_t vsz[kJoint][2][kGroups];
 #pragma unroll
       for (int e = 0; e < kJoint; ++e) {
@@ -379,14 +389,13 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
         uint32_t kw[2][kWords], ksz[2][kGroups], zw[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          load_words<kWords>(base + (r + i * 8) * (D / 2) + lane * (D / 8), kw[i]);
-          const uint8_t* sz = base + cache_ks_offset(D) + (r + i * 8 + g) * (D / 16);
-          load_words<kGroups>(sz, ksz[i]);
+          load_words(base + (r + i * 8) * (D / 2) + lane * (D / 8), kw[i]);
+          load_words(base + cache_ks_offset(D) + (r + i * 8 + g) * (D / 16), ksz[i]);
           zw[i] = kGroups == 2 && t4 % 2 ? ksz[i][kGroups - 1] : ksz[i][0];
         }
-        float dot[kGroups][NT][4] = {}, zero[NT][4] = {};
+        float dot[kGroups][NT][4], zero[NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_bf16(zero[nt], zw[0], zw[1], zw[0], zw[1], zb[nt][0], zb[nt][1]);
+        for (int nt = 0; nt < NT; ++nt) mma_bf16_first(zero[nt], zw[0], zw[1], zw[0], zw[1], zb[nt][0], zb[nt][1]);
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
 #pragma unroll
@@ -397,15 +406,15 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int sp = 0; sp < kSplit; ++sp)
-                mma_f16(dot[w / 2][nt], a0, a1, a2, a3, qb[sp][w][k][nt][0], qb[sp][w][k][nt][1]);
+                if (w % 2 == 0 && k == 0 && sp == 0)
+                  mma_f16_first(dot[w / 2][nt], a0, a1, a2, a3, qb[sp][w][k][nt][0], qb[sp][w][k][nt][1]);
+                else
+                  mma_f16(dot[w / 2][nt], a0, a1, a2, a3, qb[sp][w][k][nt][0], qb[sp][w][k][nt][1]);
           }
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          load_words<kGroups>(base + cache_vs_offset(D) + (r + i * 8 + g) * (D / 16), vsz[e][i]);
-          vmax[e][i] = 0x1p-48f;
-#pragma unroll
-          for (int j = 0; j < kGroups; ++j) vmax[e][i] = fmaxf(vmax[e][i], fabsf(__uint_as_float(vsz[e][i][j] << 16)));
+          load_words(base + cache_vs_offset(D) + (r + i * 8 + g) * (D / 16), vsz[e][i]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -418,17 +427,47 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
             }
         }
       }
-      float p[kJoint][NT][4], top = 0.0f;
-#pragma unroll
-      for (int e = 0; e < kJoint; ++e)
+      // weights against the references as they stand, times the values' scales, in float16; what a row does not
+      // see must not count, not even as 0 * NaN
+      float p[kJoint][NT][4], sum[NT][2];
+      uint32_t w16[kJoint][kGroups][NT][2], high = 0;
+      auto weigh = [&]() {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            p[e][nt][i] = fast_exp2(xs[e][nt][i] - m[nt][i % 2]);
-            top = fmaxf(top, p[e][nt][i] * vmax[e][i / 2]);
-          }
-      if (__any_sync(0xffffffffu, top > 32768.0f)) {
+          for (int c = 0; c < 2; ++c) sum[nt][c] = l[nt][c];
+#pragma unroll
+        for (int e = 0; e < kJoint; ++e)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                p[e][nt][2 * i + c] = fast_exp2(xs[e][nt][2 * i + c] - m[nt][c]);
+                sum[nt][c] += p[e][nt][2 * i + c];
+              }
+#pragma unroll
+              for (int j = 0; j < kGroups; ++j) {
+                const float vs = __uint_as_float(vsz[e][i][j] << 16);
+                float w[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  w[c] = p[e][nt][2 * i + c] * vs;
+                  if (kEdge && pos + r0 + 16 * e + 8 * i + g >= limit[nt][c]) w[c] = 0.0f;
+                }
+                w16[e][j][nt][i] = pack_f16(w[0], w[1]);
+                high = __vmaxu2(high, w16[e][j][nt][i]);
+              }
+            }
+      };
+      weigh();
+      float most = sum[0][0];
+#pragma unroll
+      for (int i = 1; i < 2 * NT; ++i) most = fmaxf(most, sum[i / 2][i % 2]);
+      // Is a weight times scale at 2^15 or above (0x7800), or a sum of weights beyond 2^90 (scales near zero)?
+      // Scales are not negative, so the codes of the float16 halves rank as they do.
+      if (__any_sync(0xffffffffu, __vmaxu2(high, 0x78007800u) != 0x78007800u || most > 0x1p90f)) {
         // raise the references so that the largest weight times scale is 2^12
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -437,7 +476,13 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
             float u = -CUDART_INF_F;
 #pragma unroll
             for (int e = 0; e < kJoint; ++e)
-              u = fmaxf(u, fmaxf(xs[e][nt][c] + __log2f(vmax[e][0]), xs[e][nt][2 + c] + __log2f(vmax[e][1])));
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float vmax = 0x1p-48f;
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j) vmax = fmaxf(vmax, __uint_as_float(vsz[e][i][j] << 16));
+                u = fmaxf(u, xs[e][nt][2 * i + c] + __log2f(vmax));
+              }
 #pragma unroll
             for (int d = 4; d < 32; d *= 2) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, d));
             const float now = fmaxf(m[nt][c], u - 12.0f), f = fast_exp2(m[nt][c] - now);
@@ -449,44 +494,38 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
             for (int w = 0; w < kWords; ++w)
 #pragma unroll
               for (int k = 0; k < 2; ++k) acc[w][k][nt][c] *= f, acc[w][k][nt][2 + c] *= f;
-#pragma unroll
-            for (int e = 0; e < kJoint; ++e) {
-              p[e][nt][c] = fast_exp2(xs[e][nt][c] - now);
-              p[e][nt][2 + c] = fast_exp2(xs[e][nt][2 + c] - now);
-            }
           }
+        weigh();
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) l[nt][c] = sum[nt][c];
 #pragma unroll
       for (int e = 0; e < kJoint; ++e) {
         const int r = r0 + 16 * e;
         uint32_t pb[kSplit][kGroups][NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) l[nt][c] += p[e][nt][c] + p[e][nt][2 + c];
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int j = 0; j < kGroups; ++j) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int j = 0; j < kGroups; ++j) {
+              pb[0][j][nt][i] = transpose8x8(w16[e][j][nt][i]);
               float vs, vz, w[2];
               unpack_sz(vsz[e][i][j], vs, vz);
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                // what a row does not see must not count, not even as 0 * NaN
                 const bool seen = !kEdge || pos + r + 8 * i + g < limit[nt][c];
                 w[c] = seen ? p[e][nt][2 * i + c] * vs : 0.0f;
                 if (seen) z[nt][c][j] = fmaf(p[e][nt][2 * i + c], vz, z[nt][c][j]);
               }
-              const uint32_t u = pack_f16(w[0], w[1]);
-              pb[0][j][nt][i] = transpose8x8(u);
-              if constexpr (kSplit == 2) pb[1][j][nt][i] = transpose8x8(pack_f16_rest(w[0], w[1], u));
+              if constexpr (kSplit == 2) pb[1][j][nt][i] = transpose8x8(pack_f16_rest(w[0], w[1], w16[e][j][nt][i]));
             }
-          }
-        }
         uint32_t vw[2][kWords];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          load_words<kWords>(base + cache_v_offset(D) + (r / 2 + t4 + 4 * i) * D + (g ^ (2 * t4)) * (D / 8), vw[i]);
+          load_words(base + cache_v_offset(D) + (r / 2 + t4 + 4 * i) * D + (g ^ (2 * t4)) * (D / 8), vw[i]);
 #pragma unroll
         for (int w = 0; w < kWords; ++w)
 #pragma unroll
@@ -503,13 +542,10 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
     };
 
     // a tile goes to one pair of warps, 32 tokens each; the pairs take the CTA's tiles in turn
-    for (; x < stop; ++x) {
-      const int st = stage, ph = phase;
-      if (++stage == kStages) stage = 0, phase ^= 1;
-      if (((x - begin) & 1) != warp / 2) continue;
-      const int pos = mbar_wait(&full[st], ph, abort, 802) ? tile_pos[st] : -1;
+    for (; mine < stop; mine += 2) {
+      const int pos = mbar_wait(&full[stage], phase, abort, 802) ? tile_pos[stage] : -1;
       if (pos >= 0) {
-        const uint8_t* base = stages + st * kTile;
+        const uint32_t base = smem_u32(stages) + stage * kTile;
         const bool edge = pos + kCacheTile > low_limit;
         for (int half = 0; half < 2 / kJoint; ++half) {
           const int r0 = (warp % 2) * 32 + half * 16;
@@ -520,8 +556,11 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
+      if (lane == 0) mbar_arrive(&empty[stage]);
+      stage += 2;
+      if (stage >= kStages) stage -= kStages, phase ^= 1;
     }
+    x = stop;
 
     // ---------------- the unit's part of this CTA: the warps' sums joined in a fixed order
     const int fb = flushes++ & 1;
