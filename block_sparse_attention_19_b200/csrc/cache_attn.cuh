@@ -12,12 +12,16 @@
 //
 // The bound is the cache's bytes (4.5 bits an element, read once) as long as a
 // tile of 64 tokens costs fewer issue slots than its 72 D bytes cost time at the
-// memory rate, so the unpacking is kept at five instructions per eight codes: a
-// four-bit code in the low bits of a float16 is the subnormal number code 2^-24,
-// in bits 4..7 it is 16 code 2^-24, and both are exact operands. The factor 16 of
-// every other channel is taken out of the query (keys) or of the sums (values).
-// For float16's range each query row is scaled by a power of two, and the
-// reference M of a row keeps 2^(x - M) v_scale below 2^15.
+// memory rate, so the unpacking is kept short. Codes are operands as they are:
+//   keys: a code in the low bits of a float16 is the subnormal code 2^-24, in bits
+//     4..7 it is 16 code 2^-24, and that factor is taken out of the query. (As e4m3
+//     numbers a byte of shift would do for eight codes instead of four, but those
+//     matrix instructions made the kernel slower: 110 against 89 us at two CTAs an SM.)
+//   values: float16 subnormals, of the byte lo + 16 hi and of lo alone; hi is the
+//     difference of the two sums.
+// All of these operands are exact. For float16's range each query row is
+// scaled by a power of two, and the reference M of a row keeps 2^(x - M) v_scale
+// below 2^15.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -33,7 +37,7 @@ constexpr int kCaMaxSeqs = 4096;                 // sequences whose tile counts 
 template <int D, int NT>
 struct CaShape {
   static constexpr int kRows = 8 * NT;  // query rows of a unit
-  static constexpr int kCtas = NT == 1 ? 3 : 2;  // CTAs of an SM
+  static constexpr int kCtas = NT == 1 ? 3 : 2;  // CTAs of an SM: up to four (three) warps to each of its quarters
   static constexpr int kOStride = D + 4;  // floats of a row in the join buffer: 16-byte stores free of conflicts
   static constexpr int kJoinBytes = kCaWarps * kRows * kOStride * 4;
   // Even, so that a stage always serves the same pair of warps: a pair then waits for a stage's next fill only
@@ -69,14 +73,17 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
-__device__ __forceinline__ void mma_bf16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                               uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %10, %10, %10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+// (16 x 8) (8 x 8) of bfloat16.
+__device__ __forceinline__ void mma_bf16_k8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(b0));
 }
-
+__device__ __forceinline__ void mma_bf16_k8_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%7, %7, %7, %7};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(b0), "f"(0.0f));
+}
 // N consecutive 32-bit words of shared memory, in one load.
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t p, uint32_t (&w)[N]) {
@@ -295,7 +302,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = nt * 8 + g;
-      float f[kWords][8], amax = 0.0f, sum[kGroups] = {};
+      float f[kWords][8], amax = 0.0f, sum[kGroups] = {};  // this thread: channels 32 w + 8 t4 + 0..7
       const int row = row0 + r;
 #pragma unroll
       for (int w = 0; w < kWords; ++w) {
@@ -314,8 +321,8 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
 #pragma unroll
         for (int j = 0; j < kGroups; ++j) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
       }
-      // the largest element goes to [2^13, 2^14): float16 keeps 11 bits of every element down to 2^-27 of
-      // it, and parts of 2^-37 of it
+      // the largest element goes to [2^13, 2^14): float16 holds the eight bits of a bfloat16 element down to 2^-27
+      // (odd channels 2^-23) of it
       const int up = min(13 - static_cast<int>((__float_as_uint(amax) >> 23) & 255u) + 127, 126);
       const float qscale = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
       const float back = __uint_as_float(static_cast<uint32_t>(24 - up + 127) << 23) * scale_log2;
@@ -347,7 +354,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
         if (kGroups == 2) {
           zb[nt][0] = t4 < 2 ? parts[0] : parts[1], zb[nt][1] = t4 < 2 ? parts[2] : parts[3];
         } else {
-          zb[nt][0] = t4 < 2 ? (t4 ? parts[1] : parts[0]) : (t4 == 2 ? parts[2] : parts[3]), zb[nt][1] = 0;
+          zb[nt][0] = t4 < 2 ? (t4 ? parts[1] : parts[0]) : (t4 == 2 ? parts[2] : parts[3]);
         }
       }
 #pragma unroll
@@ -386,16 +393,20 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
 #pragma unroll
       for (int e = 0; e < kJoint; ++e) {
         const int r = r0 + 16 * e;
-        uint32_t kw[2][kWords], ksz[2][kGroups], zw[2];
+        uint32_t kw[2][kWords], ksz[2][kGroups], zw[2][1];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+          const uint32_t sz = base + cache_ks_offset(D) + (r + i * 8 + g) * (D / 16);
           load_words(base + (r + i * 8) * (D / 2) + lane * (D / 8), kw[i]);
-          load_words(base + cache_ks_offset(D) + (r + i * 8 + g) * (D / 16), ksz[i]);
-          zw[i] = kGroups == 2 && t4 % 2 ? ksz[i][kGroups - 1] : ksz[i][0];
+          load_words(sz, ksz[i]);
+          load_words(sz + (t4 % kGroups) * 4, zw[i]);
         }
         float dot[kGroups][NT][4], zero[NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_bf16_first(zero[nt], zw[0], zw[1], zw[0], zw[1], zb[nt][0], zb[nt][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_bf16_k8_first(zero[nt], zw[0][0], zw[1][0], zb[nt][0]);
+          if constexpr (kGroups == 2) mma_bf16_k8(zero[nt], zw[0][0], zw[1][0], zb[nt][1]);
+        }
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
 #pragma unroll
@@ -530,8 +541,9 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
         for (int w = 0; w < kWords; ++w)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const uint32_t u = vw[0][w] >> (8 * k), v = vw[1][w] >> (8 * k);
-            const uint32_t a0 = u & kLow, a1 = u & kHigh, a2 = v & kLow, a3 = v & kHigh;
+            // the byte with channels 2 k and 2 k + 1, and the first one alone
+            const uint32_t a1 = k ? __byte_perm(vw[0][w], 0, 0x4341) : vw[0][w] & 0x00ff00ffu, a0 = a1 & kLow;
+            const uint32_t a3 = k ? __byte_perm(vw[1][w], 0, 0x4341) : vw[1][w] & 0x00ff00ffu, a2 = a3 & kLow;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -594,8 +606,8 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
         for (int w = 0; w < kWords; ++w) {
           const float zz = z[nt][c][w / 2] * f, f0 = f * 0x1p24f, f1 = f * 0x1p20f;
           *reinterpret_cast<float4*>(to + w * 32) =
-              make_float4(fmaf(acc[w][0][nt][c], f0, zz), fmaf(acc[w][0][nt][2 + c], f1, zz),
-                          fmaf(acc[w][1][nt][c], f0, zz), fmaf(acc[w][1][nt][2 + c], f1, zz));
+              make_float4(fmaf(acc[w][0][nt][c], f0, zz), fmaf(acc[w][0][nt][2 + c] - acc[w][0][nt][c], f1, zz),
+                          fmaf(acc[w][1][nt][c], f0, zz), fmaf(acc[w][1][nt][2 + c] - acc[w][1][nt][c], f1, zz));
         }
       }
     consumer_sync();
