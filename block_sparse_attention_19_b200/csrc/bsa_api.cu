@@ -1328,10 +1328,13 @@ cudaError_t launch_cache_attn(const void* q, const void* cache, const int32_t* i
     if (dev < 64) attr_set[dev] = true;
   }
   const int nseq = idx ? 0 : B;
-  const unsigned ctas = static_cast<unsigned>(cache_attn_ctas<NT>());
+  // with a long table of sequences one CTA fewer fits an SM's 228 KB (each takes 1 KB more, and up to 2 KB of static memory)
+  const size_t smem = Shape::smem(nseq);
+  const unsigned per_sm = std::min<unsigned>(Shape::kCtas, 228 * 1024 / (smem + 3072));
+  const unsigned ctas = per_sm * sm_count();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
-      launch_pdl(kern, ctas, bsa::kCaThreads, Shape::smem(nseq), st, static_cast<const E*>(q),
+      launch_pdl(kern, ctas, bsa::kCaThreads, smem, st, static_cast<const E*>(q),
                  static_cast<const uint8_t*>(cache), idx, static_cast<E*>(o), static_cast<float*>(ws), seqs, B, H, Hkv,
                  topk, scale_log2);
   if (e != cudaSuccess) return e;

@@ -30,23 +30,20 @@
 
 namespace bsa {
 
-constexpr int kCaWarps = 4;                      // consumer warps, in two pairs: a tile goes to a pair
-constexpr int kCaThreads = (kCaWarps + 1) * 32;  // and the producer warp
+constexpr int kCaWarps = 4;  // in two pairs: a tile goes to a pair, 32 tokens to a warp
+constexpr int kCaThreads = kCaWarps * 32;
 constexpr int kCaMaxSeqs = 4096;                 // sequences whose tile counts fit the table in shared memory
 
 template <int D, int NT>
 struct CaShape {
   static constexpr int kRows = 8 * NT;  // query rows of a unit
-  static constexpr int kCtas = NT == 1 ? 3 : 2;  // CTAs of an SM: up to four (three) warps to each of its quarters
+  static constexpr int kCtas = NT == 1 ? 4 : 3;  // CTAs of an SM: four (three) warps to each of its quarters
   static constexpr int kOStride = D + 4;  // floats of a row in the join buffer: 16-byte stores free of conflicts
   static constexpr int kJoinBytes = kCaWarps * kRows * kOStride * 4;
-  // Even, so that a stage always serves the same pair of warps: a pair then waits for a stage's next fill only
-  // after it has used the last one (a wait by parity cannot tell the fill to come from the one before the last).
-  static constexpr int kStages = (NT == 1 ? 6 : 8) * 128 / D;
-  static_assert(kStages % 2 == 0);
+  static constexpr int kStages = 2 * 128 / D;  // tiles of a pair's ring
   static constexpr int kPartFloats = kRows * (D + 2);
   static size_t smem(int nseq) {
-    return static_cast<size_t>(kStages) * cache_tile_bytes(D) + kJoinBytes + (nseq + 1) * sizeof(int);
+    return 2 * static_cast<size_t>(kStages) * cache_tile_bytes(D) + kJoinBytes + (nseq + 1) * sizeof(int);
   }
 };
 
@@ -112,8 +109,6 @@ __device__ __forceinline__ uint32_t pack_f16_rest(float lo, float hi, uint32_t p
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&packed));
   return pack_f16(lo - f.x, hi - f.y);
 }
-
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kCaWarps * 32) : "memory"); }
 
 // How the tiles of all units are laid in one line and cut into equal pieces, one
 // for each CTA. A unit is (sequence, key/value head, run of kRows query rows).
@@ -213,21 +208,24 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
   constexpr int kJoint = NT * kSplit == 1 ? 2 : 1;  // runs of 16 tokens computed together
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t* stages = smem;
-  float* join = reinterpret_cast<float*>(smem + kStages * kTile);
-  int* table = reinterpret_cast<int*>(smem + kStages * kTile + Shape::kJoinBytes);
-  __shared__ uint64_t full[kStages], empty[kStages];
-  __shared__ int tile_pos[kStages];  // position of the stage's first token; -1: the tile's block is absent
+  float* join = reinterpret_cast<float*>(smem + 2 * kStages * kTile);
+  int* table = reinterpret_cast<int*>(smem + 2 * kStages * kTile + Shape::kJoinBytes);
+  __shared__ uint64_t bars[2][2][kStages];
+  __shared__ int tile_pos[2][kStages];  // position of the stage's first token; -1: the tile's block is absent
+  __shared__ int next_pos[2][32];       // the same of the pair's next 32 tiles, and where they lie
+  __shared__ const uint8_t* next_src[2][32];
   __shared__ float join_m[2][kCaWarps][kRows], join_l[2][kCaWarps][kRows];
   __shared__ int abort_flag;
   pdl_launch_dependents();
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, G = H / Hkv;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, G = H / Hkv, pair = warp / 2;
+  const bool leader = warp % 2 == 0;  // the pair's first warp loads its tiles
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 2);
-    }
+    for (int i = 0; i < kStages; ++i)
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(&bars[j][0][i], 1);  // filled
+        mbar_init(&bars[j][1][i], 1);  // the other warp is done with it
+      }
     fence_mbarrier_init();
   }
   pdl_wait();
@@ -235,12 +233,15 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
   const int begin = min(static_cast<long>(blockIdx.x) * plan.chunk, static_cast<long>(plan.total));
   const int end = min(begin + plan.chunk, plan.total);
   volatile int* abort = &abort_flag;
+  uint8_t* stages = smem + pair * kStages * kTile;
+  uint64_t *full = bars[pair][0], *empty = bars[pair][1];
 
-  if (warp == kCaWarps) {
-    // ---------------- producer: 32 tiles' addresses at a time, one lane each, then one copy after the other
-    int issued = 0;
-    for (int x0 = begin; x0 < end && !*abort; x0 += 32) {
-      const int x = x0 + lane;
+  // The leader: copies tile x (the pair's next to load) into its stage. Where the 32 tiles from x on lie is looked up
+  // at once, one lane each.
+  int load = begin + pair, load_stage = 0, loads = 0;
+  auto fetch = [&]() {
+    if (loads % 32 == 0) {
+      const int x = load + 2 * lane;
       int pos = -1;
       const uint8_t* src = nullptr;
       if (x < end) {
@@ -257,33 +258,30 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
           if (pos >= start + count) pos = -1;
         }
       }
-      for (int i = 0; i < 32 && x0 + i < end; ++i, ++issued) {
-        const int p = __shfl_sync(0xffffffffu, pos, i);
-        const uint8_t* from = reinterpret_cast<const uint8_t*>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i));
-        const int st = issued % kStages;
-        if (issued >= kStages && !mbar_wait(&empty[st], (issued / kStages - 1) & 1, abort, 801)) break;
-        if (lane == 0) {
-          tile_pos[st] = p;
-          if (p >= 0) {
-            mbar_arrive_expect_tx(&full[st], kTile);
-            bulk_load(stages + st * kTile, from, kTile, &full[st]);
-          } else {
-            mbar_arrive(&full[st]);
-          }
-        }
-        __syncwarp();
+      next_pos[pair][lane] = pos;
+      next_src[pair][lane] = src;
+      __syncwarp();
+    }
+    if (lane == 0) {
+      const int pos = next_pos[pair][loads % 32];
+      tile_pos[pair][load_stage] = pos;
+      if (pos >= 0) {
+        mbar_arrive_expect_tx(&full[load_stage], kTile);
+        bulk_load(stages + load_stage * kTile, next_src[pair][loads % 32], kTile, &full[load_stage]);
+      } else {
+        mbar_arrive(&full[load_stage]);
       }
     }
-    if (*abort && lane == 0) {  // copies in flight end before the block's shared memory does
-      for (int i = max(0, issued - kStages); i < issued; ++i) mbar_wait_teardown(&full[i % kStages], i / kStages & 1);
-    }
-    return;
-  }
+    __syncwarp();
+    ++loads;
+    load += 2;
+    if (++load_stage == kStages) load_stage = 0;
+  };
+  if (leader)
+    while (loads < kStages && load < end) fetch();
 
-  // ---------------- consumers
   const int g = lane / 4, t4 = lane % 4;
-  int flushes = 0, phase = 0, stage = warp / 2, mine = begin + stage;  // this pair's next tile and its place
+  int flushes = 0, phase = 0, stage = 0, mine = begin + pair;  // this pair's next tile and its place
   for (int x = begin; x < end;) {
     int b, unit, first, n;
     plan.locate(x, b, unit, first, n);
@@ -555,7 +553,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
 
     // a tile goes to one pair of warps, 32 tokens each; the pairs take the CTA's tiles in turn
     for (; mine < stop; mine += 2) {
-      const int pos = mbar_wait(&full[stage], phase, abort, 802) ? tile_pos[stage] : -1;
+      const int pos = mbar_wait(&full[stage], phase, abort, 802) ? tile_pos[pair][stage] : -1;
       if (pos >= 0) {
         const uint32_t base = smem_u32(stages) + stage * kTile;
         const bool edge = pos + kCacheTile > low_limit;
@@ -568,9 +566,12 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[stage]);
-      stage += 2;
-      if (stage >= kStages) stage -= kStages, phase ^= 1;
+      if (!leader) {
+        if (lane == 0) mbar_arrive(&empty[stage]);
+      } else if (load < end && mbar_wait(&empty[stage], phase, abort, 801)) {
+        fetch();
+      }
+      if (++stage == kStages) stage = 0, phase ^= 1;
     }
     x = stop;
 
@@ -591,7 +592,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
           join_l[fb][warp][nt * 8 + 2 * t4 + c] = l[nt][c];
         }
       }
-    consumer_sync();
+    __syncthreads();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -610,7 +611,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
                           fmaf(acc[w][1][nt][c], f0, zz), fmaf(acc[w][1][nt][2 + c] - acc[w][1][nt][c], f1, zz));
         }
       }
-    consumer_sync();
+    __syncthreads();
     const bool whole = first >= begin && first + n <= end;
     float* part = part_of<D, NT>(ws, blockIdx.x, first < begin ? 0 : 1);
     for (int i = threadIdx.x; i < rows * D; i += kCaWarps * 32) {
@@ -633,6 +634,9 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
       }
     }
   }
+  // after a wait that ran out: copies in flight end before the block's shared memory does
+  if (*abort && leader && lane == 0)
+    for (int i = max(0, loads - kStages); i < loads; ++i) mbar_wait_teardown(&full[i % kStages], i / kStages & 1);
 }
 
 // Joins the parts of the units that several CTAs share: one CTA per query row,
