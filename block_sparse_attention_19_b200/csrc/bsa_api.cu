@@ -1299,25 +1299,12 @@ bsa_status launched(cudaError_t e, const char* what) {
   return e == cudaSuccess ? BSA_OK : cuda_fail(e, what);
 }
 
-// CTAs of the attention over the cache: all that fit the device at once.
-template <int NT>
-long cache_attn_ctas() {
-  return static_cast<long>(sm_count()) * bsa::CaShape<128, NT>::kCtas;
-}
-
-// 16 query rows a unit when a (sequence, key/value head) has more than 8: its
-// tiles are then read and unpacked half as often. float32 queries, whose
-// operands come in two parts, stay at 8 (registers).
-bool cache_attn_wide(int T, int H, int Hkv, bsa_dtype dt) {
-  return dt == BSA_BF16 && static_cast<long long>(T) * (H / Hkv) > 8;
-}
-
-template <typename E, int D, int NT>
+template <typename E, int D, int NT, int FOLD>
 cudaError_t launch_cache_attn(const void* q, const void* cache, const int32_t* idx, void* o, void* ws,
                               const bsa::CacheSeqs& seqs, int B, int H, int Hkv, int topk, float scale_log2,
                               void* stream) {
-  using Shape = bsa::CaShape<D, NT>;
-  const auto kern = bsa::cache_attn_kernel<E, D, NT>;
+  using Shape = bsa::CaShape<D, NT, FOLD>;
+  const auto kern = bsa::cache_attn_kernel<E, D, NT, FOLD>;
   static bool attr_set[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1340,7 +1327,7 @@ cudaError_t launch_cache_attn(const void* q, const void* cache, const int32_t* i
   if (e != cudaSuccess) return e;
   // A plain launch: as a programmatic one its waiting CTAs and the next call's early ones share the SMs so that
   // some of the latter start late (a run of dense calls: 117 against 82 us each).
-  bsa::cache_attn_join_kernel<E, D, NT><<<static_cast<unsigned>(B) * seqs.T * H, bsa::kCaJoinWarps * 32,
+  bsa::cache_attn_join_kernel<E, D, NT, FOLD><<<static_cast<unsigned>(B) * seqs.T * H, bsa::kCaJoinWarps * 32,
                                           (nseq + 1) * sizeof(int), st>>>(
       static_cast<E*>(o), static_cast<const float*>(ws), seqs, B, H, Hkv, idx ? topk : 0, static_cast<int>(ctas));
   return cudaGetLastError();
@@ -1444,8 +1431,8 @@ bsa_status bsa_cache_block_topk(const void* q, const float* k_sum, const int32_t
 size_t bsa_cache_attn_workspace_bytes(int B, int T, int H, int H_kv, int D) {
   if (check_cache_dims(B, T, H, H_kv, D, 64) != BSA_OK) return 0;
   // two parts of a unit's query rows for each CTA; float32 and bfloat16 queries alike
-  const long ctas = std::max(cache_attn_ctas<1>(), cache_attn_ctas<2>());
-  return static_cast<size_t>(ctas) * 2 * 16 * (D + 2) * sizeof(float);
+  const long rows = std::max(8 * bsa::CaShape<128, 1, 1>::kCtas, 16 * bsa::CaShape<128, 2, 1>::kCtas);
+  return static_cast<size_t>(sm_count()) * rows * 2 * (D + 2) * sizeof(float);
 }
 
 bsa_status bsa_cache_attn(const void* q, const void* cache, const int32_t* page_table, const int32_t* start,
@@ -1469,11 +1456,17 @@ bsa_status bsa_cache_attn(const void* q, const void* cache, const int32_t* page_
     using E = decltype(t);
     constexpr int kD = decltype(d)::value;
     const float sl = scale * 1.4426950408889634f;
+    // Query rows of a (sequence, key/value head): up to four are folded (everything between the products once for two
+    // runs of tokens: dense 32768-token batch, four rows, XX us against 69); more than eight go 16 to a unit, whose
+    // tiles are then read and unpacked half as often. float32 queries, whose operands come in two parts, stay at 8.
+    const long long rows = static_cast<long long>(T) * (H / H_kv);
+    if (rows <= 4)
+      return launch_cache_attn<E, kD, 1, 2>(q, cache, idx, o, workspace, seqs, B, H, H_kv, topk, sl, stream);
     if constexpr (sizeof(E) == 2) {
-      if (cache_attn_wide(T, H, H_kv, dt))
-        return launch_cache_attn<E, kD, 2>(q, cache, idx, o, workspace, seqs, B, H, H_kv, topk, sl, stream);
+      if (rows > 8)
+        return launch_cache_attn<E, kD, 2, 1>(q, cache, idx, o, workspace, seqs, B, H, H_kv, topk, sl, stream);
     }
-    return launch_cache_attn<E, kD, 1>(q, cache, idx, o, workspace, seqs, B, H, H_kv, topk, sl, stream);
+    return launch_cache_attn<E, kD, 1, 1>(q, cache, idx, o, workspace, seqs, B, H, H_kv, topk, sl, stream);
   });
   if ((s = launched(e, "cache_attn_kernel launch")) != BSA_OK) return s;
   return ok();

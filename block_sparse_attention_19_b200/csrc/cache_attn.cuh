@@ -34,12 +34,16 @@ constexpr int kCaWarps = 4;  // in two pairs: a tile goes to a pair, 32 tokens t
 constexpr int kCaThreads = kCaWarps * 32;
 constexpr int kCaMaxSeqs = 4096;                 // sequences whose tile counts fit the table in shared memory
 
-template <int D, int NT>
+// How many query rows a unit has and how they fill the products' 8 NT columns: each once, or (FOLD = 2, up to four
+// rows) twice, the two halves for different tokens.
+template <int D, int NT, int FOLD>
 struct CaShape {
-  static constexpr int kRows = 8 * NT;  // query rows of a unit
+  static_assert(FOLD == 1 || NT == 1);
+  static constexpr int kCols = 8 * NT;
+  static constexpr int kRows = kCols / FOLD;  // query rows of a unit
   static constexpr int kCtas = NT == 1 ? 4 : 3;  // CTAs of an SM: four (three) warps to each of its quarters
   static constexpr int kOStride = D + 4;  // floats of a row in the join buffer: 16-byte stores free of conflicts
-  static constexpr int kJoinBytes = kCaWarps * kRows * kOStride * 4;
+  static constexpr int kJoinBytes = kCaWarps * kCols * kOStride * 4;
   static constexpr int kStages = 2 * 128 / D;  // tiles of a pair's ring
   static constexpr int kPartFloats = kRows * (D + 2);
   static size_t smem(int nseq) {
@@ -92,6 +96,12 @@ __device__ __forceinline__ void load_words(uint32_t p, uint32_t (&w)[N]) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(p));
   else
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(p));
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -184,9 +194,9 @@ __device__ __forceinline__ CaPlan make_plan(const CacheSeqs& s, int B, int Hkv, 
 // Where a CTA leaves its part of a unit that other CTAs share: slot 0 for the
 // unit that began before the CTA's tiles, slot 1 for the one that begins among
 // them. Floats: references [kRows], weight sums [kRows], sums [kRows][D].
-template <int D, int NT>
+template <typename Shape>
 __device__ __forceinline__ float* part_of(float* ws, int cta, int slot) {
-  return ws + (static_cast<long>(cta) * 2 + slot) * CaShape<D, NT>::kPartFloats;
+  return ws + (static_cast<long>(cta) * 2 + slot) * Shape::kPartFloats;
 }
 
 template <typename T>
@@ -197,15 +207,17 @@ __device__ __forceinline__ void store_out(T* o, float x) {
     *o = x;
 }
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
+template <typename T, int D, int NT, int FOLD>
+__global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT, FOLD>::kCtas))
     cache_attn_kernel(const T* __restrict__ q, const uint8_t* __restrict__ cache, const int32_t* __restrict__ idx, T* o,
                       float* ws, CacheSeqs s, int B, int H, int Hkv, int topk, float scale_log2) {
-  using Shape = CaShape<D, NT>;
-  constexpr int kStages = Shape::kStages, kRows = Shape::kRows, kTile = cache_tile_bytes(D);
+  using Shape = CaShape<D, NT, FOLD>;
+  constexpr int kStages = Shape::kStages, kRows = Shape::kRows, kCols = Shape::kCols, kTile = cache_tile_bytes(D);
   constexpr int kWords = D / 32, kGroups = D / 64;
   constexpr int kSplit = sizeof(T) == 4 ? 2 : 1;  // float16 parts of a query element and of a weight
-  constexpr int kJoint = NT * kSplit == 1 ? 2 : 1;  // runs of 16 tokens computed together
+  // runs of 16 tokens computed together; folded, two runs share the columns and everything between the products is
+  // computed once for both, each thread looking after the tokens of its half
+  constexpr int kRuns = NT * kSplit == 1 || FOLD == 2 ? 2 : 1, kSoft = kRuns / FOLD;
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
   extern __shared__ __align__(128) uint8_t smem[];
   float* join = reinterpret_cast<float*>(smem + 2 * kStages * kTile);
@@ -214,7 +226,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
   __shared__ int tile_pos[2][kStages];  // position of the stage's first token; -1: the tile's block is absent
   __shared__ int next_pos[2][32];       // the same of the pair's next 32 tiles, and where they lie
   __shared__ const uint8_t* next_src[2][32];
-  __shared__ float join_m[2][kCaWarps][kRows], join_l[2][kCaWarps][kRows];
+  __shared__ float join_m[2][kCaWarps][kCols], join_l[2][kCaWarps][kCols];
   __shared__ int abort_flag;
   pdl_launch_dependents();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, G = H / Hkv, pair = warp / 2;
@@ -294,12 +306,12 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
     // the queries as the products' second operand, and per row what a score is multiplied by
     uint32_t qb[kSplit][kWords][2][NT][2];
     uint32_t zb[NT][2];
-    float mul[NT][2];
+    float mul[NT][2], qsum[2][kGroups];  // qsum: folded only, in the place of zb
     int limit[NT][2];
     int low_limit = 0x7fffffff;  // positions below it are seen by all rows
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = nt * 8 + g;
+      const int r = (nt * 8 + g) % kRows;
       float f[kWords][8], amax = 0.0f, sum[kGroups] = {};  // this thread: channels 32 w + 8 t4 + 0..7
       const int row = row0 + r;
 #pragma unroll
@@ -359,7 +371,11 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
       for (int c = 0; c < 2; ++c) {  // this thread's scores belong to rows 2 t4 and 2 t4 + 1
         const int from = (2 * t4 + c) * 4;
         mul[nt][c] = __shfl_sync(0xffffffffu, back, from);
-        const int rr = nt * 8 + 2 * t4 + c;
+        if constexpr (FOLD == 2) {
+#pragma unroll
+          for (int j = 0; j < kGroups; ++j) qsum[c][j] = __shfl_sync(0xffffffffu, sum[j] * scale_log2, from);
+        }
+        const int rr = (nt * 8 + 2 * t4 + c) % kRows;
         limit[nt][c] = rr < rows ? start + (row0 + rr) / G + 1 : 0;
       }
     }
@@ -382,28 +398,34 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
           for (int i = 0; i < 4; ++i) acc[w][k][nt][i] = 0.0f;
     }
 
-    // kJoint runs of 16 tokens of a tile, from row r0: their scores, weights and sums. kEdge: some row does not see
+    // kRuns runs of 16 tokens of a tile, from row r0: their scores, weights and sums. kEdge: some row does not see
     // some token.
     auto tokens = [&](uint32_t base, int pos, int r0, auto edge) {
       constexpr bool kEdge = decltype(edge)::value;
-      float xs[kJoint][NT][4];
-      uint32_t vsz[kJoint][2][kGroups];
+      const int half = FOLD == 2 ? t4 / 2 : 0;  // the run that this thread looks after
+      float xs[kSoft][NT][4], dot[kRuns][kGroups][NT][4], zero[kRuns][NT][4];
+      uint32_t ksz[kSoft][2][kGroups], vsz[kSoft][2][kGroups];
 #pragma unroll
-      for (int e = 0; e < kJoint; ++e) {
+      for (int u = 0; u < kSoft; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          load_words(base + cache_ks_offset(D) + (r0 + 16 * (u + half) + i * 8 + g) * (D / 16), ksz[u][i]);
+#pragma unroll
+      for (int e = 0; e < kRuns; ++e) {
         const int r = r0 + 16 * e;
-        uint32_t kw[2][kWords], ksz[2][kGroups], zw[2][1];
+        uint32_t kw[2][kWords];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t sz = base + cache_ks_offset(D) + (r + i * 8 + g) * (D / 16);
-          load_words(base + (r + i * 8) * (D / 2) + lane * (D / 8), kw[i]);
-          load_words(sz, ksz[i]);
-          load_words(sz + (t4 % kGroups) * 4, zw[i]);
-        }
-        float dot[kGroups][NT][4], zero[NT][4];
+        for (int i = 0; i < 2; ++i) load_words(base + (r + i * 8) * (D / 2) + lane * (D / 8), kw[i]);
+        if constexpr (FOLD == 1) {
+          uint32_t zw[2][1];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_bf16_k8_first(zero[nt], zw[0][0], zw[1][0], zb[nt][0]);
-          if constexpr (kGroups == 2) mma_bf16_k8(zero[nt], zw[0][0], zw[1][0], zb[nt][1]);
+          for (int i = 0; i < 2; ++i)
+            load_words(base + cache_ks_offset(D) + (r + i * 8 + g) * (D / 16) + (t4 % kGroups) * 4, zw[i]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_bf16_k8_first(zero[e][nt], zw[0][0], zw[1][0], zb[nt][0]);
+            if constexpr (kGroups == 2) mma_bf16_k8(zero[e][nt], zw[0][0], zw[1][0], zb[nt][1]);
+          }
         }
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
@@ -416,37 +438,48 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
 #pragma unroll
               for (int sp = 0; sp < kSplit; ++sp)
                 if (w % 2 == 0 && k == 0 && sp == 0)
-                  mma_f16_first(dot[w / 2][nt], a0, a1, a2, a3, qb[sp][w][k][nt][0], qb[sp][w][k][nt][1]);
+                  mma_f16_first(dot[e][w / 2][nt], a0, a1, a2, a3, qb[sp][w][k][nt][0], qb[sp][w][k][nt][1]);
                 else
-                  mma_f16(dot[w / 2][nt], a0, a1, a2, a3, qb[sp][w][k][nt][0], qb[sp][w][k][nt][1]);
+                  mma_f16(dot[e][w / 2][nt], a0, a1, a2, a3, qb[sp][w][k][nt][0], qb[sp][w][k][nt][1]);
           }
         }
+      }
+#pragma unroll
+      for (int u = 0; u < kSoft; ++u)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          load_words(base + cache_vs_offset(D) + (r + i * 8 + g) * (D / 16), vsz[e][i]);
+          load_words(base + cache_vs_offset(D) + (r0 + 16 * (u + half) + i * 8 + g) * (D / 16), vsz[u][i]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float d = __uint_as_float(ksz[i][0] << 16) * dot[0][nt][2 * i + c];
-              if constexpr (kGroups == 2) d = fmaf(__uint_as_float(ksz[i][1] << 16), dot[1][nt][2 * i + c], d);
-              float v = fmaf(d, mul[nt][c], zero[nt][2 * i + c]);
-              if (kEdge && pos + r + 8 * i + g >= limit[nt][c]) v = -CUDART_INF_F;
-              xs[e][nt][2 * i + c] = v;
+              const int at = 2 * i + c;
+              float d = 0.0f, a = 0.0f;
+#pragma unroll
+              for (int j = 0; j < kGroups; ++j) {
+                const float one = FOLD == 2 && half ? dot[kRuns - 1][j][nt][at] : dot[u][j][nt][at];
+                float sc, ze;
+                unpack_sz(ksz[u][i][j], sc, ze);
+                d = j ? fmaf(sc, one, d) : sc * one;
+                if constexpr (FOLD == 2) a = j ? fmaf(ze, qsum[c][j], a) : ze * qsum[c][j];
+              }
+              if constexpr (FOLD == 1) a = zero[u][nt][at];
+              float v = fmaf(d, mul[nt][c], a);
+              if (kEdge && pos + r0 + 16 * (u + half) + 8 * i + g >= limit[nt][c]) v = -CUDART_INF_F;
+              xs[u][nt][at] = v;
             }
         }
-      }
       // weights against the references as they stand, times the values' scales, in float16; what a row does not
       // see must not count, not even as 0 * NaN
-      float p[kJoint][NT][4], sum[NT][2];
-      uint32_t w16[kJoint][kGroups][NT][2], high = 0;
+      float p[kSoft][NT][4], sum[NT][2];
+      uint32_t w16[kSoft][kGroups][NT][2], high = 0;
       auto weigh = [&]() {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) sum[nt][c] = l[nt][c];
 #pragma unroll
-        for (int e = 0; e < kJoint; ++e)
+        for (int e = 0; e < kSoft; ++e)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -463,10 +496,10 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                   w[c] = p[e][nt][2 * i + c] * vs;
-                  if (kEdge && pos + r0 + 16 * e + 8 * i + g >= limit[nt][c]) w[c] = 0.0f;
+                  if (kEdge && pos + r0 + 16 * (e + half) + 8 * i + g >= limit[nt][c]) w[c] = 0.0f;
                 }
                 w16[e][j][nt][i] = pack_f16(w[0], w[1]);
-                high = __vmaxu2(high, w16[e][j][nt][i]);
+                high = max_u16x2(high, w16[e][j][nt][i]);
               }
             }
       };
@@ -476,7 +509,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
       for (int i = 1; i < 2 * NT; ++i) most = fmaxf(most, sum[i / 2][i % 2]);
       // Is a weight times scale at 2^15 or above (0x7800), or a sum of weights beyond 2^90 (scales near zero)?
       // Scales are not negative, so the codes of the float16 halves rank as they do.
-      if (__any_sync(0xffffffffu, __vmaxu2(high, 0x78007800u) != 0x78007800u || most > 0x1p90f)) {
+      if (__any_sync(0xffffffffu, max_u16x2(high, 0x78007800u) != 0x78007800u || most > 0x1p90f)) {
         // raise the references so that the largest weight times scale is 2^12
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -484,7 +517,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
           for (int c = 0; c < 2; ++c) {
             float u = -CUDART_INF_F;
 #pragma unroll
-            for (int e = 0; e < kJoint; ++e)
+            for (int e = 0; e < kSoft; ++e)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 float vmax = 0x1p-48f;
@@ -510,27 +543,36 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) l[nt][c] = sum[nt][c];
+      uint32_t pb[kSoft][kSplit][kGroups][NT][2];
 #pragma unroll
-      for (int e = 0; e < kJoint; ++e) {
-        const int r = r0 + 16 * e;
-        uint32_t pb[kSplit][kGroups][NT][2];
+      for (int e = 0; e < kSoft; ++e)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
-              pb[0][j][nt][i] = transpose8x8(w16[e][j][nt][i]);
+              pb[e][0][j][nt][i] = transpose8x8(w16[e][j][nt][i]);
               float vs, vz, w[2];
               unpack_sz(vsz[e][i][j], vs, vz);
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                const bool seen = !kEdge || pos + r + 8 * i + g < limit[nt][c];
+                const bool seen = !kEdge || pos + r0 + 16 * (e + half) + 8 * i + g < limit[nt][c];
                 w[c] = seen ? p[e][nt][2 * i + c] * vs : 0.0f;
                 if (seen) z[nt][c][j] = fmaf(p[e][nt][2 * i + c], vz, z[nt][c][j]);
               }
-              if constexpr (kSplit == 2) pb[1][j][nt][i] = transpose8x8(pack_f16_rest(w[0], w[1], w16[e][j][nt][i]));
+              if constexpr (kSplit == 2)
+                pb[e][1][j][nt][i] = transpose8x8(pack_f16_rest(w[0], w[1], w16[e][j][nt][i]));
             }
+#pragma unroll
+      for (int e = 0; e < kRuns; ++e) {
+        const int r = r0 + 16 * e;
+        // folded: this run's weights are in columns 4 e .. 4 e + 3, the others' must not meet its values
+        const uint32_t mine = FOLD == 1 || g / 4 == e ? 0xffffffffu : 0u;
+        uint32_t wb[kSplit][kGroups][NT][2];
+#pragma unroll
+        for (int i = 0; i < 2 * kSplit * kGroups * NT; ++i)
+          (&wb[0][0][0][0])[i] = (&pb[FOLD == 2 ? 0 : e][0][0][0][0])[i] & mine;
         uint32_t vw[2][kWords];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -546,7 +588,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int sp = 0; sp < kSplit; ++sp)
-                mma_f16(acc[w][k][nt], a0, a1, a2, a3, pb[sp][w / 2][nt][0], pb[sp][w / 2][nt][1]);
+                mma_f16(acc[w][k][nt], a0, a1, a2, a3, wb[sp][w / 2][nt][0], wb[sp][w / 2][nt][1]);
           }
       }
     };
@@ -557,8 +599,8 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
       if (pos >= 0) {
         const uint32_t base = smem_u32(stages) + stage * kTile;
         const bool edge = pos + kCacheTile > low_limit;
-        for (int half = 0; half < 2 / kJoint; ++half) {
-          const int r0 = (warp % 2) * 32 + half * 16;
+        for (int run = 0; run < 2; run += kRuns) {
+          const int r0 = (warp % 2) * 32 + run * 16;
           if (edge)
             tokens(base, pos, r0, std::true_type{});
           else
@@ -575,7 +617,15 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
     }
     x = stop;
 
-    // ---------------- the unit's part of this CTA: the warps' sums joined in a fixed order
+    // ---------------- the unit's part of this CTA: the warps' (and halves') sums joined in a fixed order
+    auto join_top = [](const float (&m)[kCaWarps][kCols], int r) {
+      float top = m[0][r];
+#pragma unroll
+      for (int w = 0; w < kCaWarps; ++w)
+#pragma unroll
+        for (int e = 0; e < FOLD; ++e) top = fmaxf(top, m[w][r + e * kRows]);
+      return top;
+    };
     const int fb = flushes++ & 1;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -597,12 +647,9 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int r = nt * 8 + 2 * t4 + c;
-        float top = join_m[fb][0][r];
-#pragma unroll
-        for (int w = 1; w < kCaWarps; ++w) top = fmaxf(top, join_m[fb][w][r]);
-        const float f = fast_exp2(m[nt][c] - top);
-        float* to = join + (warp * kRows + r) * Shape::kOStride + 4 * g;
+        const int col = nt * 8 + 2 * t4 + c;
+        const float f = fast_exp2(m[nt][c] - join_top(join_m[fb], col % kRows));
+        float* to = join + (warp * kCols + col) * Shape::kOStride + 4 * g;
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
           const float zz = z[nt][c][w / 2] * f, f0 = f * 0x1p24f, f1 = f * 0x1p20f;
@@ -613,17 +660,18 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
       }
     __syncthreads();
     const bool whole = first >= begin && first + n <= end;
-    float* part = part_of<D, NT>(ws, blockIdx.x, first < begin ? 0 : 1);
+    float* part = part_of<Shape>(ws, blockIdx.x, first < begin ? 0 : 1);
     for (int i = threadIdx.x; i < rows * D; i += kCaWarps * 32) {
       const int r = i / D, c = i % D;
-      float top = join_m[fb][0][r], sum = 0.0f, val = 0.0f;
+      const float top = join_top(join_m[fb], r);
+      float sum = 0.0f, val = 0.0f;
 #pragma unroll
-      for (int w = 1; w < kCaWarps; ++w) top = fmaxf(top, join_m[fb][w][r]);
+      for (int w = 0; w < kCaWarps; ++w)
 #pragma unroll
-      for (int w = 0; w < kCaWarps; ++w) {
-        sum += join_l[fb][w][r] * fast_exp2(join_m[fb][w][r] - top);
-        val += join[(w * kRows + r) * Shape::kOStride + c];
-      }
+        for (int e = 0; e < FOLD; ++e) {
+          sum += join_l[fb][w][r + e * kRows] * fast_exp2(join_m[fb][w][r + e * kRows] - top);
+          val += join[(w * kCols + r + e * kRows) * Shape::kOStride + c];
+        }
       if (whole) {
         const int row = row0 + r;
         store_out(o + ((static_cast<long>(b) * s.T + row / G) * H + h * G + row % G) * D + c,
@@ -643,10 +691,10 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT>::kCtas))
 // its 8 warps taking the parts in turn and meeting in a fixed order.
 constexpr int kCaJoinWarps = 8;
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, int FOLD>
 __global__ void __launch_bounds__(kCaJoinWarps * 32)
     cache_attn_join_kernel(T* o, const float* ws, CacheSeqs s, int B, int H, int Hkv, int topk, int ctas) {
-  using Shape = CaShape<D, NT>;
+  using Shape = CaShape<D, NT, FOLD>;
   constexpr int kPer = D / 32;  // channels of a lane
   extern __shared__ int table[];
   __shared__ float sums[kCaJoinWarps][D], weights[kCaJoinWarps], tops[kCaJoinWarps];
@@ -665,13 +713,13 @@ __global__ void __launch_bounds__(kCaJoinWarps * 32)
   const int c0 = first / plan.chunk, c1 = (first + n - 1) / plan.chunk;
   if (c0 == c1) return;
   float top = -1e30f;
-  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, part_of<D, NT>(const_cast<float*>(ws), c, c == c0)[r]);
+  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, part_of<Shape>(const_cast<float*>(ws), c, c == c0)[r]);
 #pragma unroll
   for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   float val[kPer] = {}, weight = 0.0f;
 #pragma unroll 4
   for (int c = c0 + warp; c <= c1; c += kCaJoinWarps) {
-    const float* part = part_of<D, NT>(const_cast<float*>(ws), c, c == c0);
+    const float* part = part_of<Shape>(const_cast<float*>(ws), c, c == c0);
     const float f = fast_exp2(part[r] - top);
     weight += part[Shape::kRows + r] * f;
 #pragma unroll
