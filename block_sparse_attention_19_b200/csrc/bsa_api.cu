@@ -1420,9 +1420,25 @@ bsa_status bsa_cache_block_topk(const void* q, const float* k_sum, const int32_t
                                                               kCacheMaxBlocks * sizeof(uint32_t))
                                        : cudaSuccess;
     if (a != cudaSuccess) return a;
-    return launch_pdl(kern, static_cast<unsigned>(B) * H_kv, bsa::kCacheSelThreads, smem,
-                      static_cast<cudaStream_t>(stream), static_cast<const E*>(q), k_sum, idx, seqs, H, H_kv, topk,
-                      (flags & BSA_FLAG_FORCE_DIAG) ? 1 : 0);
+    // a cluster for each row: as many CTAs as give the device about four each SM, 64 blocks a CTA at least
+    unsigned ctas = 1;
+    while (ctas < 8 && static_cast<long long>(B) * H_kv * ctas * 2 <= 4 * sm_count() &&
+           max_blocks >= static_cast<int>(ctas) * 2 * 64)
+      ctas *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(B) * H_kv * ctas);
+    cfg.blockDim = dim3(bsa::kCacheSelThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<const E*>(q), k_sum, idx, seqs, H, H_kv, topk,
+                              (flags & BSA_FLAG_FORCE_DIAG) ? 1 : 0);
   });
   if ((s = launched(e, "cache_topk_kernel launch")) != BSA_OK) return s;
   return ok();

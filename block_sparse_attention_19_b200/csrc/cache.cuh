@@ -276,14 +276,19 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const uint8_t* cache, T
 
 // ------------------------------------------------------------------ block selection
 //
-// One CTA per (sequence, key/value head): scores of all its blocks into shared
-// memory, then the topk largest by a radix selection on order-preserving keys.
-// The scores' dot products run in float64 and are rounded to float32 once, so
-// that which blocks are kept does not depend on an order of summation.
-constexpr int kCacheSelThreads = 512;
+// One cluster of 1 to 8 CTAs per (sequence, key/value head). Its CTAs score a
+// slice of the row's blocks each (eight lanes a block, so that a block's sums are
+// one read of D float32 by neighbouring lanes) and store order-preserving keys in
+// the first CTA's shared memory; that CTA finds the topk-th largest key bit by
+// bit, one count of the keys a bit, and writes the ids in ascending order.
+// The bytes of the sums bound it (B H_kv blocks D 4 bytes) where there are many;
+// a short row is a chain of latencies: lengths, pages, sums, about 20 counts.
+// The dot products run in float64 and are rounded to float32 once, so that which
+// blocks are kept does not depend on an order of summation.
+constexpr int kCacheSelThreads = 256, kCacheSelWarps = kCacheSelThreads / 32;
 
 __device__ __forceinline__ uint32_t cache_score_key(float x) {
-  if (x != x) return 0xffffffffu;  // NaN above everything, as any comparison sort that keeps it has to put it somewhere
+  if (x != x) return 0xffffffffu;  // a NaN ranks first
   const uint32_t u = __float_as_uint(x + 0.0f);  // -0 as +0
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
@@ -291,93 +296,163 @@ __device__ __forceinline__ uint32_t cache_score_key(float x) {
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// The address of this CTA's shared-memory address `a` in the cluster's first CTA.
+__device__ __forceinline__ uint32_t first_cta_addr(uint32_t a) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kCacheSelThreads) cache_topk_kernel(const T* __restrict__ q,
                                                                       const float* __restrict__ k_sum, int32_t* idx,
                                                                       CacheSeqs s, int H, int Hkv, int topk,
                                                                       int force) {
-  extern __shared__ uint32_t keys[];  // [max_blocks]
-  __shared__ double qs[D];
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t warp_sum[kCacheSelThreads / 32];
-  __shared__ uint32_t sh_prefix, sh_need, sh_present;
+  constexpr int kVec = D / 32;     // float4s of a lane
+  constexpr int kUnroll = 2;       // blocks of a lane in flight
+  constexpr int kSplit = kCacheSelThreads / D;
+  extern __shared__ uint32_t keys[];  // [max_blocks], of the first CTA
+  __shared__ double q_part[kSplit][D];
+  __shared__ int warp_n[2][kCacheSelWarps];
   pdl_launch_dependents();
+  const uint32_t rank = cluster_rank(), ctas = cluster_size();
+  cluster_sync();  // the first CTA's shared memory is there before anyone stores to it
   pdl_wait();
-  const int h = blockIdx.x % Hkv, b = blockIdx.x / Hkv, G = H / Hkv;
+  const int row = blockIdx.x / ctas, h = row % Hkv, b = row / Hkv, G = H / Hkv;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   int start, count;
   seq_step(s, b, start, count);
   const int total = min(start + count, s.max_blocks * s.bs);
   const int n = (total + s.bs - 1) / s.bs;
-  for (int d = tid; d < D; d += kCacheSelThreads) {
+  {
+    const int d = tid % D, part = tid / D;
+    const T* at = q + (static_cast<long>(b) * s.T * H + h * G) * D + d;
     double sum = 0;
-    for (int t = 0; t < count; ++t)
-      for (int g = 0; g < G; ++g)
-        sum += to_float(q[((static_cast<long>(b) * s.T + t) * H + h * G + g) * D + d]);
-    qs[d] = sum;
+#pragma unroll 8
+    for (int r = part; r < count * G; r += kSplit) sum += to_float(at[(static_cast<long>(r / G) * H + r % G) * D]);
+    q_part[part][d] = sum;
   }
-  if (tid == 0) sh_present = 0;
   __syncthreads();
-  for (int j = warp; j < n; j += kCacheSelThreads / 32) {
-    const int page = seq_page(s, b, j);
-    uint32_t key = 0;  // absent
-    if (page >= 0) {
-      const float* ks = k_sum + (static_cast<long>(page) * Hkv + h) * D;
-      double x = 0;
-      for (int d = lane; d < D; d += 32) x += qs[d] * ks[d];
+  const int sub = lane % 8, grp = lane / 8;
+  double qd[kVec][4];
 #pragma unroll
-      for (int o = 16; o; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
-      key = cache_score_key(static_cast<float>(x / min(s.bs, total - j * s.bs)));
-      if (force && (j + 1) * s.bs > start) key = 0xffffffffu;
+  for (int i = 0; i < kVec; ++i)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      double x = 0;
+#pragma unroll
+      for (int p = 0; p < kSplit; ++p) x += q_part[p][i * 32 + sub * 4 + c];
+      qd[i][c] = x;
     }
-    if (lane == 0) {
-      keys[j] = key;
-      if (key) atomicAdd(&sh_present, 1u);
+  const uint32_t to = first_cta_addr(smem_u32(keys));
+  const int lo = static_cast<int>(static_cast<long>(n) * rank / ctas),
+            hi = static_cast<int>(static_cast<long>(n) * (rank + 1) / ctas);
+  for (int j0 = lo; j0 < hi; j0 += kCacheSelWarps * 4 * kUnroll) {
+    int j[kUnroll], page[kUnroll];
+    float4 x[kUnroll][kVec];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      j[u] = j0 + (u * kCacheSelWarps + warp) * 4 + grp;
+      page[u] = j[u] < hi ? seq_page(s, b, j[u]) : -1;
     }
-  }
-  __syncthreads();
-  const uint32_t want = min(static_cast<uint32_t>(topk), sh_present);
-  // the want-th largest key, eight bits at a time
-  if (tid == 0) sh_prefix = 0, sh_need = want;
-  for (int shift = 24; shift >= 0 && want; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    const uint32_t prefix = sh_prefix, need = sh_need;
-    for (int j = tid; j < n; j += kCacheSelThreads)
-      if (shift == 24 || keys[j] >> (shift + 8) == prefix >> (shift + 8)) atomicAdd(&hist[keys[j] >> shift & 255u], 1u);
-    __syncthreads();
-    if (tid == 0) {
-      uint32_t above = 0;
-      int bin = 255;
-      while (bin > 0 && above + hist[bin] < need) above += hist[bin--];
-      sh_prefix = prefix | static_cast<uint32_t>(bin) << shift;
-      sh_need = need - above;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const float4* ks =
+          reinterpret_cast<const float4*>(k_sum + (static_cast<long>(max(page[u], 0)) * Hkv + h) * D) + sub;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) x[u][i] = __ldg(ks + i * 8);
     }
-    __syncthreads();
-  }
-  __syncthreads();
-  // ids in ascending order: all keys above the threshold and the first sh_need equal to it
-  const uint32_t thr = sh_prefix, ties = sh_need;
-  int32_t* out = idx + static_cast<long>(blockIdx.x) * topk;
-  uint32_t above_before = 0, equal_before = 0;
-  for (int j0 = 0; j0 < n && want; j0 += kCacheSelThreads) {
-    const uint32_t key = j0 + tid < n ? keys[j0 + tid] : 0u;
-    const uint32_t above = key > thr, equal = key == thr && key != 0;
-    const uint32_t ma = __ballot_sync(0xffffffffu, above), me = __ballot_sync(0xffffffffu, equal);
-    if (lane == 0) warp_sum[warp] = __popc(ma) | __popc(me) << 16;
-    __syncthreads();
-    uint32_t a = above_before, e = equal_before;
-    for (int w = 0; w < kCacheSelThreads / 32; ++w) {
-      if (w == warp) {
-        const uint32_t below = (1u << lane) - 1u;
-        const uint32_t ea = e + __popc(me & below), pos = a + __popc(ma & below) + min(ea, ties);
-        if (above || (equal && ea < ties)) out[pos] = j0 + tid;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      double dot = 0;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        dot = fma(qd[i][0], static_cast<double>(x[u][i].x), dot);
+        dot = fma(qd[i][1], static_cast<double>(x[u][i].y), dot);
+        dot = fma(qd[i][2], static_cast<double>(x[u][i].z), dot);
+        dot = fma(qd[i][3], static_cast<double>(x[u][i].w), dot);
       }
-      a += warp_sum[w] & 0xffffu;
-      e += warp_sum[w] >> 16;
+#pragma unroll
+      for (int o = 4; o; o /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if (sub == 0 && j[u] < hi) {
+        uint32_t key = 0;  // an absent block: below every score
+        if (page[u] >= 0) {
+          key = cache_score_key(static_cast<float>(dot / min(s.bs, total - j[u] * s.bs)));
+          if (force && (j[u] + 1) * s.bs > start) key = 0xffffffffu;
+        }
+        store_cluster(to + 4u * j[u], key);
+      }
     }
-    above_before = a, equal_before = e;
+  }
+  cluster_sync();
+  if (rank) return;
+
+  // keys[0, n) at or above `least`, over the CTA; the two slots of warp_n take turns, so one barrier a count does
+  int turn = 0;
+  auto count_from = [&](uint32_t least) {
+    int c = 0;
+    for (int j = tid; j < n; j += kCacheSelThreads) c += keys[j] >= least;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0) warp_n[turn][warp] = c;
     __syncthreads();
+    c = 0;
+#pragma unroll
+    for (int w = 0; w < kCacheSelWarps; ++w) c += warp_n[turn][w];
+    turn ^= 1;
+    return c;
+  };
+  const int want = min(topk, count_from(1));
+  // the largest threshold that want keys reach; ties: how many keys equal to it belong
+  uint32_t thr = 0;
+  int reach = 0, ties = 0;
+  if (want) {
+    for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
+      const int c = count_from(thr | bit);
+      if (c >= want) thr |= bit, reach = c;
+      if (c == want) break;
+    }
+    if (reach > want) ties = want - (thr == 0xffffffffu ? 0 : count_from(thr + 1));
+  }
+  const bool some = reach > want;  // only the first `ties` of the equal ones
+  // ids in ascending order: each warp takes a run of blocks
+  int32_t* out = idx + static_cast<long>(row) * topk;
+  const int run = ((n + kCacheSelWarps - 1) / kCacheSelWarps + 31) / 32 * 32;
+  const int first = min(warp * run, n), last = want ? min(first + run, n) : first;
+  int above = 0, equal = 0;
+  for (int j0 = first; j0 < last; j0 += 32) {
+    const uint32_t key = j0 + lane < last ? keys[j0 + lane] : 0u;
+    above += __popc(__ballot_sync(0xffffffffu, key && (some ? key > thr : key >= thr)));
+    equal += __popc(__ballot_sync(0xffffffffu, some && key == thr));
+  }
+  __syncthreads();
+  if (lane == 0) warp_n[0][warp] = above, warp_n[1][warp] = equal;
+  __syncthreads();
+  above = equal = 0;
+  for (int w = 0; w < warp; ++w) above += warp_n[0][w], equal += warp_n[1][w];
+  for (int j0 = first; j0 < last; j0 += 32) {
+    const uint32_t key = j0 + lane < last ? keys[j0 + lane] : 0u, below = (1u << lane) - 1u;
+    const bool up = key && (some ? key > thr : key >= thr), same = some && key == thr;
+    const uint32_t mu = __ballot_sync(0xffffffffu, up), ms = __ballot_sync(0xffffffffu, same);
+    const int e = equal + __popc(ms & below);
+    if (up || (same && e < ties)) out[above + __popc(mu & below) + min(e, ties)] = j0 + lane;
+    above += __popc(mu);
+    equal += __popc(ms);
   }
   for (int j = want + tid; j < topk; j += kCacheSelThreads) out[j] = -1;
 }
