@@ -276,13 +276,14 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const uint8_t* cache, T
 
 // ------------------------------------------------------------------ block selection
 //
-// One cluster of 1 to 8 CTAs per (sequence, key/value head). Its CTAs score a
+// One cluster of 1 to 16 CTAs per (sequence, key/value head). Its CTAs score a
 // slice of the row's blocks each (eight lanes a block, so that a block's sums are
 // one read of D float32 by neighbouring lanes) and store order-preserving keys in
-// the first CTA's shared memory; that CTA finds the topk-th largest key bit by
-// bit, one count of the keys a bit, and writes the ids in ascending order.
+// the first CTA's shared memory; that CTA finds the topk-th largest key by three
+// histograms (short rows: by comparing all with all) and writes the ids in
+// ascending order.
 // The bytes of the sums bound it (B H_kv blocks D 4 bytes) where there are many;
-// a short row is a chain of latencies: lengths, pages, sums, about 20 counts.
+// a short row is a chain of latencies: lengths, pages, sums, three histograms.
 // The dot products run in float64 and are rounded to float32 once, so that which
 // blocks are kept does not depend on an order of summation.
 constexpr int kCacheSelThreads = 256, kCacheSelWarps = kCacheSelThreads / 32;
@@ -325,11 +326,13 @@ __global__ void __launch_bounds__(kCacheSelThreads) cache_topk_kernel(const T* _
                                                                       CacheSeqs s, int H, int Hkv, int topk,
                                                                       int force) {
   constexpr int kVec = D / 32;     // float4s of a lane
-  constexpr int kUnroll = 2;       // blocks of a lane in flight
+  constexpr int kUnroll = 4;       // blocks of a lane in flight
   constexpr int kSplit = kCacheSelThreads / D;
-  extern __shared__ uint32_t keys[];  // [max_blocks], of the first CTA
+  extern __shared__ uint32_t keys[];  // [max_blocks]: pages of this CTA's slice, then (in the first CTA) all keys
   __shared__ double q_part[kSplit][D];
-  __shared__ int warp_n[2][kCacheSelWarps];
+  __shared__ uint2 warp_n[kCacheSelWarps];
+  __shared__ uint32_t hist[2048];
+  __shared__ uint3 found;
   pdl_launch_dependents();
   const uint32_t rank = cluster_rank(), ctas = cluster_size();
   cluster_sync();  // the first CTA's shared memory is there before anyone stores to it
@@ -340,6 +343,9 @@ __global__ void __launch_bounds__(kCacheSelThreads) cache_topk_kernel(const T* _
   seq_step(s, b, start, count);
   const int total = min(start + count, s.max_blocks * s.bs);
   const int n = (total + s.bs - 1) / s.bs;
+  const int lo = static_cast<int>(static_cast<long>(n) * rank / ctas),
+            hi = static_cast<int>(static_cast<long>(n) * (rank + 1) / ctas);
+  const int page0 = lo + tid < hi ? seq_page(s, b, lo + tid) : -1;  // on its way while the queries are summed
   {
     const int d = tid % D, part = tid / D;
     const T* at = q + (static_cast<long>(b) * s.T * H + h * G) * D + d;
@@ -348,6 +354,9 @@ __global__ void __launch_bounds__(kCacheSelThreads) cache_topk_kernel(const T* _
     for (int r = part; r < count * G; r += kSplit) sum += to_float(at[(static_cast<long>(r / G) * H + r % G) * D]);
     q_part[part][d] = sum;
   }
+  if (lo + tid < hi) keys[lo + tid] = static_cast<uint32_t>(page0);
+  for (int j = lo + tid + kCacheSelThreads; j < hi; j += kCacheSelThreads)
+    keys[j] = static_cast<uint32_t>(seq_page(s, b, j));
   __syncthreads();
   const int sub = lane % 8, grp = lane / 8;
   double qd[kVec][4];
@@ -360,16 +369,15 @@ __global__ void __launch_bounds__(kCacheSelThreads) cache_topk_kernel(const T* _
       for (int p = 0; p < kSplit; ++p) x += q_part[p][i * 32 + sub * 4 + c];
       qd[i][c] = x;
     }
+  const double inv_bs = 1.0 / s.bs;
   const uint32_t to = first_cta_addr(smem_u32(keys));
-  const int lo = static_cast<int>(static_cast<long>(n) * rank / ctas),
-            hi = static_cast<int>(static_cast<long>(n) * (rank + 1) / ctas);
   for (int j0 = lo; j0 < hi; j0 += kCacheSelWarps * 4 * kUnroll) {
     int j[kUnroll], page[kUnroll];
     float4 x[kUnroll][kVec];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       j[u] = j0 + (u * kCacheSelWarps + warp) * 4 + grp;
-      page[u] = j[u] < hi ? seq_page(s, b, j[u]) : -1;
+      page[u] = j[u] < hi ? static_cast<int>(keys[j[u]]) : -1;
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -390,10 +398,12 @@ __global__ void __launch_bounds__(kCacheSelThreads) cache_topk_kernel(const T* _
       }
 #pragma unroll
       for (int o = 4; o; o /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if (sub == 0 && j[u] < hi) {
+      if (sub == 0 && j[u] < hi) {  // the block's lanes have all read its page
         uint32_t key = 0;  // an absent block: below every score
         if (page[u] >= 0) {
-          key = cache_score_key(static_cast<float>(dot / min(s.bs, total - j[u] * s.bs)));
+          const int tokens = total - j[u] * s.bs;
+          // a full block's size is a power of two: the product with its inverse is exact
+          key = cache_score_key(static_cast<float>(tokens >= s.bs ? dot * inv_bs : dot / tokens));
           if (force && (j[u] + 1) * s.bs > start) key = 0xffffffffu;
         }
         store_cluster(to + 4u * j[u], key);
@@ -403,56 +413,122 @@ __global__ void __launch_bounds__(kCacheSelThreads) cache_topk_kernel(const T* _
   cluster_sync();
   if (rank) return;
 
-  // keys[0, n) at or above `least`, over the CTA; the two slots of warp_n take turns, so one barrier a count does
-  int turn = 0;
-  auto count_from = [&](uint32_t least) {
-    int c = 0;
-    for (int j = tid; j < n; j += kCacheSelThreads) c += keys[j] >= least;
-    c = __reduce_add_sync(0xffffffffu, c);
-    if (lane == 0) warp_n[turn][warp] = c;
-    __syncthreads();
-    c = 0;
-#pragma unroll
-    for (int w = 0; w < kCacheSelWarps; ++w) c += warp_n[turn][w];
-    turn ^= 1;
-    return c;
-  };
-  const int want = min(topk, count_from(1));
-  // the largest threshold that want keys reach; ties: how many keys equal to it belong
-  uint32_t thr = 0;
-  int reach = 0, ties = 0;
-  if (want) {
-    for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
-      const int c = count_from(thr | bit);
-      if (c >= want) thr |= bit, reach = c;
-      if (c == want) break;
-    }
-    if (reach > want) ties = want - (thr == 0xffffffffu ? 0 : count_from(thr + 1));
-  }
-  const bool some = reach > want;  // only the first `ties` of the equal ones
-  // ids in ascending order: each warp takes a run of blocks
   int32_t* out = idx + static_cast<long>(row) * topk;
-  const int run = ((n + kCacheSelWarps - 1) / kCacheSelWarps + 31) / 32 * 32;
-  const int first = min(warp * run, n), last = want ? min(first + run, n) : first;
-  int above = 0, equal = 0;
-  for (int j0 = first; j0 < last; j0 += 32) {
-    const uint32_t key = j0 + lane < last ? keys[j0 + lane] : 0u;
-    above += __popc(__ballot_sync(0xffffffffu, key && (some ? key > thr : key >= thr)));
-    equal += __popc(__ballot_sync(0xffffffffu, some && key == thr));
-  }
-  __syncthreads();
-  if (lane == 0) warp_n[0][warp] = above, warp_n[1][warp] = equal;
-  __syncthreads();
-  above = equal = 0;
-  for (int w = 0; w < warp; ++w) above += warp_n[0][w], equal += warp_n[1][w];
-  for (int j0 = first; j0 < last; j0 += 32) {
-    const uint32_t key = j0 + lane < last ? keys[j0 + lane] : 0u, below = (1u << lane) - 1u;
-    const bool up = key && (some ? key > thr : key >= thr), same = some && key == thr;
-    const uint32_t mu = __ballot_sync(0xffffffffu, up), ms = __ballot_sync(0xffffffffu, same);
-    const int e = equal + __popc(ms & below);
-    if (up || (same && e < ties)) out[above + __popc(mu & below) + min(e, ties)] = j0 + lane;
-    above += __popc(mu);
-    equal += __popc(ms);
+  const uint32_t below = (1u << lane) - 1u;
+  int want;
+  if (n <= kCacheSelThreads) {
+    // a short row: each key's rank by comparison with all others (absent blocks rank nowhere)
+    const uint32_t key = tid < n ? keys[tid] : 0u;
+    int before = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; j += 4) {
+      const uint4 four = *reinterpret_cast<const uint4*>(keys + j);  // (the allocation is a multiple of 16 bytes)
+      const uint32_t other[4] = {four.x, four.y, four.z, four.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        before += j + i < n && (other[i] > key || (other[i] == key && j + i < tid));
+    }
+    want = min(topk, __syncthreads_count(key != 0));
+    const bool up = key && before < want;
+    const uint32_t mu = __ballot_sync(0xffffffffu, up);
+    if (lane == 0) warp_n[warp] = make_uint2(__popc(mu), 0);
+    __syncthreads();
+    int at = __popc(mu & below);
+    for (int w = 0; w < warp; ++w) at += warp_n[w].x;
+    if (up) out[at] = tid;
+  } else {
+    // the want-th largest key by three histograms of 11, 11 and 10 bits: keys above its interval are in, and `need`
+    // of those in it
+    uint32_t thr = 0, width = 0;  // the interval: thr and its `width` lower bits
+    int need = 0, present = 0;
+#pragma unroll 8
+    for (int j = tid; j < n; j += kCacheSelThreads) present += keys[j] != 0;
+    present = __reduce_add_sync(0xffffffffu, present);
+    if (lane == 0) warp_n[warp].x = present;
+    __syncthreads();
+    present = 0;
+    for (int w = 0; w < kCacheSelWarps; ++w) present += warp_n[w].x;
+    want = need = min(topk, present);
+    if (want) {
+#pragma unroll 1
+      for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const uint32_t bins = pass == 2 ? 1024 : 2048;
+        __syncthreads();
+        for (int i = tid; i < 2048; i += kCacheSelThreads) hist[i] = 0;
+        __syncthreads();
+#pragma unroll 8
+        for (int j = tid; j < n; j += kCacheSelThreads) {
+          const uint32_t key = keys[j];
+          if (key && (pass == 0 || key >> width == thr >> width)) atomicAdd(&hist[key >> shift & (bins - 1)], 1u);
+        }
+        __syncthreads();
+        // from the top: thread t looks after bins 8 (255 - t) .. + 7
+        uint32_t own[8], sum = 0;
+        const int b0 = 8 * (kCacheSelThreads - 1 - tid);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) own[i] = hist[b0 + i], sum += own[i];
+        uint32_t upto = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+          const uint32_t x = __shfl_up_sync(0xffffffffu, upto, d);
+          if (lane >= d) upto += x;
+        }
+        if (lane == 31) warp_n[warp].y = upto;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) upto += warp_n[w].y;
+        if (upto >= static_cast<uint32_t>(need) && upto - sum < static_cast<uint32_t>(need)) {  // one thread
+          uint32_t over = upto - sum;
+#pragma unroll
+          for (int i = 7; i >= 0; --i) {
+            if (over < static_cast<uint32_t>(need) && over + own[i] >= static_cast<uint32_t>(need))
+              found = make_uint3(b0 + i, need - over, own[i]);
+            over += own[i];
+          }
+        }
+        __syncthreads();
+        thr |= found.x << shift;
+        need = found.y;
+        width = shift;
+        if (need == static_cast<int>(found.z)) break;  // the whole interval is in
+      }
+    }
+    // ids in ascending order, 4096 keys at a time: those above the interval, and in it the first ones
+    const bool some = want && need < static_cast<int>(found.z);  // (equal keys then: all 32 bits are known)
+    const uint32_t top = thr >> width;
+    int above = 0, equal = 0;
+    constexpr int kRun = 16;
+    for (int base = 0; base < n && want; base += kRun * kCacheSelThreads) {
+      uint32_t mu[kRun], ms[kRun];
+      int a = 0, e = 0;
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        const int j = base + (warp * kRun + i) * 32 + lane;
+        const uint32_t key = j < n ? keys[j] : 0u, digit = key >> width;
+        mu[i] = __ballot_sync(0xffffffffu, key && (some ? digit > top : digit >= top));
+        ms[i] = __ballot_sync(0xffffffffu, key && some && digit == top);
+        a += __popc(mu[i]);
+        e += __popc(ms[i]);
+      }
+      __syncthreads();
+      if (lane == 0) warp_n[warp] = make_uint2(a, e);
+      __syncthreads();
+      a = above, e = equal;
+      for (int w = 0; w < kCacheSelWarps; ++w) {
+        const uint2 x = warp_n[w];
+        if (w < warp) a += x.x, e += x.y;
+        above += x.x, equal += x.y;
+      }
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        const bool up = mu[i] >> lane & 1, same = ms[i] >> lane & 1;
+        const int es = e + __popc(ms[i] & below);
+        if (up || (same && es < need))
+          out[a + __popc(mu[i] & below) + min(es, need)] = base + (warp * kRun + i) * 32 + lane;
+        a += __popc(mu[i]);
+        e += __popc(ms[i]);
+      }
+    }
   }
   for (int j = want + tid; j < topk; j += kCacheSelThreads) out[j] = -1;
 }
