@@ -1412,7 +1412,7 @@ bsa_status bsa_cache_block_topk(const void* q, const float* k_sum, const int32_t
   if ((s = check_cache_lists(page_table, start, count, idx)) != BSA_OK) return s;
   if ((s = check_device()) != BSA_OK) return s;
   const bsa::CacheSeqs seqs{page_table, start, count, T, num_pages, max_blocks, block_size};
-  const size_t smem = (static_cast<size_t>(max_blocks) + 3) / 4 * 16;  // keys, read four at a time
+  const size_t smem = static_cast<size_t>(max_blocks) * sizeof(uint32_t);
   const cudaError_t e = by_type(dt, D, [&](auto t, auto d) {
     using E = decltype(t);
     const auto kern = bsa::cache_topk_kernel<E, decltype(d)::value>;
@@ -1426,10 +1426,10 @@ bsa_status bsa_cache_block_topk(const void* q, const float* k_sum, const int32_t
       if (a != cudaSuccess) return a;
       if (dev < 64) attr_set[dev] = true;
     }
-    // a cluster for each row: as many CTAs as the device holds at once (two an SM), 64 blocks a CTA at least
+    // a cluster for each row: as many CTAs as the device holds at once (two an SM), 32 blocks a CTA at least
     unsigned ctas = 1;
     while (ctas < 16 && static_cast<long long>(B) * H_kv * ctas * 2 <= 2 * sm_count() &&
-           max_blocks >= static_cast<int>(ctas) * 2 * 64)
+           max_blocks >= static_cast<int>(ctas) * 2 * 32)
       ctas *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(B) * H_kv * ctas);

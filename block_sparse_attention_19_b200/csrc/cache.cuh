@@ -25,6 +25,8 @@
 #include <math_constants.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "bsa_ptx.cuh"
 
 namespace bsa {
@@ -326,12 +328,11 @@ __global__ void __launch_bounds__(kCacheSelThreads) cache_topk_kernel(const T* _
                                                                       CacheSeqs s, int H, int Hkv, int topk,
                                                                       int force) {
   constexpr int kVec = D / 32;     // float4s of a lane
-  constexpr int kUnroll = 4;       // blocks of a lane in flight
   constexpr int kSplit = kCacheSelThreads / D;
   extern __shared__ uint32_t keys[];  // [max_blocks]: pages of this CTA's slice, then (in the first CTA) all keys
   __shared__ double q_part[kSplit][D];
   __shared__ uint2 warp_n[kCacheSelWarps];
-  __shared__ uint32_t hist[2048];
+  __shared__ __align__(16) uint32_t hist[2048];
   __shared__ uint3 found;
   pdl_launch_dependents();
   const uint32_t rank = cluster_rank(), ctas = cluster_size();
@@ -345,7 +346,9 @@ __global__ void __launch_bounds__(kCacheSelThreads) cache_topk_kernel(const T* _
   const int n = (total + s.bs - 1) / s.bs;
   const int lo = static_cast<int>(static_cast<long>(n) * rank / ctas),
             hi = static_cast<int>(static_cast<long>(n) * (rank + 1) / ctas);
-  const int page0 = lo + tid < hi ? seq_page(s, b, lo + tid) : -1;  // on its way while the queries are summed
+  // this slice's first pages are on their way while the queries are summed
+  const int p0 = lo + tid, p1 = p0 + kCacheSelThreads;
+  const int page0 = p0 < hi ? seq_page(s, b, p0) : -1, page1 = p1 < hi ? seq_page(s, b, p1) : -1;
   {
     const int d = tid % D, part = tid / D;
     const T* at = q + (static_cast<long>(b) * s.T * H + h * G) * D + d;
@@ -354,8 +357,9 @@ __global__ void __launch_bounds__(kCacheSelThreads) cache_topk_kernel(const T* _
     for (int r = part; r < count * G; r += kSplit) sum += to_float(at[(static_cast<long>(r / G) * H + r % G) * D]);
     q_part[part][d] = sum;
   }
-  if (lo + tid < hi) keys[lo + tid] = static_cast<uint32_t>(page0);
-  for (int j = lo + tid + kCacheSelThreads; j < hi; j += kCacheSelThreads)
+  if (p0 < hi) keys[p0] = static_cast<uint32_t>(page0);
+  if (p1 < hi) keys[p1] = static_cast<uint32_t>(page1);
+  for (int j = p1 + kCacheSelThreads; j < hi; j += kCacheSelThreads)
     keys[j] = static_cast<uint32_t>(seq_page(s, b, j));
   __syncthreads();
   const int sub = lane % 8, grp = lane / 8;
@@ -371,23 +375,23 @@ __global__ void __launch_bounds__(kCacheSelThreads) cache_topk_kernel(const T* _
     }
   const double inv_bs = 1.0 / s.bs;
   const uint32_t to = first_cta_addr(smem_u32(keys));
-  for (int j0 = lo; j0 < hi; j0 += kCacheSelWarps * 4 * kUnroll) {
-    int j[kUnroll], page[kUnroll];
-    float4 x[kUnroll][kVec];
+  // scores of kN runs of 32 blocks from j0 on, their sums' loads all in flight together
+  auto score = [&](int j0, auto runs) {
+    constexpr int kN = decltype(runs)::value;
+    int page[kN];
+    float4 x[kN][kVec];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      j[u] = j0 + (u * kCacheSelWarps + warp) * 4 + grp;
-      page[u] = j[u] < hi ? static_cast<int>(keys[j[u]]) : -1;
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < kN; ++u) {
+      const int j = j0 + (u * kCacheSelWarps + warp) * 4 + grp;
+      page[u] = j < hi ? static_cast<int>(keys[j]) : -1;
       const float4* ks =
           reinterpret_cast<const float4*>(k_sum + (static_cast<long>(max(page[u], 0)) * Hkv + h) * D) + sub;
 #pragma unroll
       for (int i = 0; i < kVec; ++i) x[u][i] = __ldg(ks + i * 8);
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < kN; ++u) {
+      const int j = j0 + (u * kCacheSelWarps + warp) * 4 + grp;
       double dot = 0;
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
@@ -398,18 +402,25 @@ __global__ void __launch_bounds__(kCacheSelThreads) cache_topk_kernel(const T* _
       }
 #pragma unroll
       for (int o = 4; o; o /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if (sub == 0 && j[u] < hi) {  // the block's lanes have all read its page
-        uint32_t key = 0;  // an absent block: below every score
+      if (sub == 0 && j < hi) {  // the block's lanes have all read its page
+        uint32_t key = 0;        // an absent block: below every score
         if (page[u] >= 0) {
-          const int tokens = total - j[u] * s.bs;
+          const int tokens = total - j * s.bs;
           // a full block's size is a power of two: the product with its inverse is exact
           key = cache_score_key(static_cast<float>(tokens >= s.bs ? dot * inv_bs : dot / tokens));
-          if (force && (j[u] + 1) * s.bs > start) key = 0xffffffffu;
+          if (force && (j + 1) * s.bs > start) key = 0xffffffffu;
         }
-        store_cluster(to + 4u * j[u], key);
+        store_cluster(to + 4u * j, key);
       }
     }
-  }
+  };
+  constexpr int kRunBlocks = 4 * kCacheSelWarps;
+  int j0 = lo;
+  for (; hi - j0 > 2 * kRunBlocks; j0 += 4 * kRunBlocks) score(j0, std::integral_constant<int, 4>{});
+  if (hi - j0 > kRunBlocks)
+    score(j0, std::integral_constant<int, 2>{});
+  else if (hi > j0)
+    score(j0, std::integral_constant<int, 1>{});
   cluster_sync();
   if (rank) return;
 
@@ -420,13 +431,10 @@ __global__ void __launch_bounds__(kCacheSelThreads) cache_topk_kernel(const T* _
     // a short row: each key's rank by comparison with all others (absent blocks rank nowhere)
     const uint32_t key = tid < n ? keys[tid] : 0u;
     int before = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; j += 4) {
-      const uint4 four = *reinterpret_cast<const uint4*>(keys + j);  // (the allocation is a multiple of 16 bytes)
-      const uint32_t other[4] = {four.x, four.y, four.z, four.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        before += j + i < n && (other[i] > key || (other[i] == key && j + i < tid));
+    if (warp * 32 < n) {
+      for (int j = 0; j < warp * 32; ++j) before += keys[j] >= key;
+      for (int j = warp * 32; j < min(n, warp * 32 + 32); ++j) before += keys[j] > key || (keys[j] == key && j < tid);
+      for (int j = warp * 32 + 32; j < n; ++j) before += keys[j] > key;
     }
     want = min(topk, __syncthreads_count(key != 0));
     const bool up = key && before < want;
@@ -455,7 +463,7 @@ __global__ void __launch_bounds__(kCacheSelThreads) cache_topk_kernel(const T* _
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const uint32_t bins = pass == 2 ? 1024 : 2048;
         __syncthreads();
-        for (int i = tid; i < 2048; i += kCacheSelThreads) hist[i] = 0;
+        reinterpret_cast<uint4*>(hist)[tid] = reinterpret_cast<uint4*>(hist)[tid + kCacheSelThreads] = uint4{};
         __syncthreads();
 #pragma unroll 8
         for (int j = tid; j < n; j += kCacheSelThreads) {
@@ -464,10 +472,10 @@ __global__ void __launch_bounds__(kCacheSelThreads) cache_topk_kernel(const T* _
         }
         __syncthreads();
         // from the top: thread t looks after bins 8 (255 - t) .. + 7
-        uint32_t own[8], sum = 0;
         const int b0 = 8 * (kCacheSelThreads - 1 - tid);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) own[i] = hist[b0 + i], sum += own[i];
+        const uint4 o0 = *reinterpret_cast<const uint4*>(hist + b0), o1 = *reinterpret_cast<const uint4*>(hist + b0 + 4);
+        const uint32_t own[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+        const uint32_t sum = o0.x + o0.y + o0.z + o0.w + o1.x + o1.y + o1.z + o1.w;
         uint32_t upto = sum;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -493,11 +501,11 @@ __global__ void __launch_bounds__(kCacheSelThreads) cache_topk_kernel(const T* _
         if (need == static_cast<int>(found.z)) break;  // the whole interval is in
       }
     }
-    // ids in ascending order, 4096 keys at a time: those above the interval, and in it the first ones
+    // ids in ascending order, 1024 keys at a time: those above the interval, and in it the first ones
     const bool some = want && need < static_cast<int>(found.z);  // (equal keys then: all 32 bits are known)
     const uint32_t top = thr >> width;
     int above = 0, equal = 0;
-    constexpr int kRun = 16;
+    constexpr int kRun = 4;
     for (int base = 0; base < n && want; base += kRun * kCacheSelThreads) {
       uint32_t mu[kRun], ms[kRun];
       int a = 0, e = 0;
