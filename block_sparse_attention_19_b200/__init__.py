@@ -595,66 +595,98 @@ def bsa_cache_alloc(num_pages: int, H_kv: int, D: int, block_size: int, device="
             torch.empty((num_pages, H_kv, D), device=device, dtype=torch.float32))
 
 
-def _same_device(*named):
-    """Every tensor contiguous on the first one's CUDA device, which is made the
-    current one of the call by _cache_call."""
+def _cache_call(fn, named, *args):
+    """Calls fn(pointers of the named tensors..., *args, stream) with the first
+    one's device current and its current stream. Every tensor (None: a null
+    pointer) has to be contiguous on that CUDA device. Kept short: a step of
+    generation is a few microseconds of GPU time."""
+    dev = None
+    ptrs = []
     for t, n in named:
-        if t is not None:
-            _dev(t, n)
-            if t.device != named[0][0].device:
-                raise ValueError(f"{n} is on {t.device}, {named[0][1]} on {named[0][0].device}")
+        if t is None:
+            ptrs.append(None)
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{n} must be a CUDA tensor")
+        if not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+        d = t.get_device()
+        if dev is None:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{n} is on cuda:{d}, {named[0][1]} on cuda:{dev}")
+        ptrs.append(t.data_ptr())
+    if dev == torch.cuda.current_device():
+        status = fn(*ptrs, *args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*ptrs, *args, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        _check(status)
+
+
+def _is(t: torch.Tensor, shape: tuple, dtype: torch.dtype, name: str):
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {list(shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}")
 
 
 def _check_seqs(page_table, start, count, B: int):
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [{B}, max_blocks]")
-    _shape(start, (B,), "start")
+    if page_table.dtype is not torch.int32:
+        raise TypeError("page_table must be int32")
+    _is(start, (B,), torch.int32, "start")
     if count is not None:
-        _shape(count, (B,), "count")
-    for t, n in ((page_table, "page_table"), (start, "start"), (count, "count")):
-        if t is not None and t.dtype != torch.int32:
-            raise TypeError(f"{n} must be int32")
+        _is(count, (B,), torch.int32, "count")
 
 
-def _check_cache(cache, H_kv: int, D: int, block_size: int):
-    if cache.dim() != 4 or tuple(cache.shape[1:]) != (H_kv, block_size // 64, 72 * D) or block_size % 64:
-        raise ValueError(f"cache has shape {tuple(cache.shape)}, expected [num_pages, {H_kv}, {block_size} / 64, {72 * D}]")
-    if cache.dtype != torch.uint8:
+def _cache_sizes(cache, block_size: int):
+    """num_pages, H_kv and D of a cache tensor."""
+    if cache.dim() != 4 or cache.shape[3] % 72:
+        raise ValueError(f"cache has shape {tuple(cache.shape)}, expected [num_pages, H_kv, block_size / 64, 72 D]")
+    pages, Hk, tiles, row = cache.shape
+    if block_size % 64 or tiles != block_size // 64:
+        raise ValueError(f"cache has {tiles} tiles a page, block_size {block_size} needs block_size / 64")
+    if cache.dtype is not torch.uint8:
         raise TypeError("cache must be uint8")
+    return pages, Hk, row // 72
 
 
-def _check_k_sum(k_sum, num_pages, H_kv: int, D: int):
-    if k_sum.dim() != 3 or tuple(k_sum.shape[1:]) != (H_kv, D) or num_pages not in (None, k_sum.shape[0]):
-        raise ValueError(f"k_sum has shape {tuple(k_sum.shape)}, expected [num_pages, {H_kv}, {D}]")
-    if k_sum.dtype != torch.float32:
-        raise TypeError("k_sum must be float32")
+def _check_new(k, v, Hk: int, D: int):
+    """B and T of the new tokens' keys and values [B, T, H_kv, D]."""
+    if k.dim() != 4 or k.shape[2] != Hk or k.shape[3] != D:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected [B, T, {Hk}, {D}]")
+    _is(v, k.shape, k.dtype, "v")
+    return k.shape[0], k.shape[1]
 
 
-def _cache_call(fn, t: torch.Tensor, *args):
-    """fn(*args, stream) with t's device current and its current stream."""
-    if t.device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(t)))
-    else:
-        with torch.cuda.device(t.device):
-            _check(fn(*args, _stream(t)))
+def _check_step_q(q, Hk: int, D: int):
+    """B, T and H of the step's queries [B, T, H, D]."""
+    if q.dim() != 4 or q.shape[3] != D or Hk < 1 or q.shape[2] % Hk:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected [B, T, H, {D}] with H a multiple of {Hk}")
+    return q.shape[:3]
+
+
+def _step_out(out, q, count):
+    """The output of a step: rows that no token has are zeros where the call makes it."""
+    if out is None:
+        return (torch.empty_like if count is None else torch.zeros_like)(q)
+    _is(out, q.shape, q.dtype, "out")
+    return out
 
 
 def bsa_cache_write(k, v, cache, k_sum, page_table, start, block_size: int, count=None) -> None:
     """Writes k and v [B, T, H_kv, D] into the cache at the positions start[b] +
     t, t < count[b] (all T without count), and renews k_sum of their pages."""
-    if k.dim() != 4:
-        raise ValueError("k and v must be [B, T, H_kv, D]")
-    _shape(v, k.shape, "v")
-    if v.dtype != k.dtype:
-        raise TypeError("k and v must share one dtype")
-    B, T, Hk, D = k.shape
-    _check_cache(cache, Hk, D, block_size)
-    _check_k_sum(k_sum, cache.shape[0], Hk, D)
+    pages, Hk, D = _cache_sizes(cache, block_size)
+    B, T = _check_new(k, v, Hk, D)
+    _is(k_sum, (pages, Hk, D), torch.float32, "k_sum")
     _check_seqs(page_table, start, count, B)
-    _same_device((k, "k"), (v, "v"), (cache, "cache"), (k_sum, "k_sum"), (page_table, "page_table"), (start, "start"),
-                 (count, "count"))
-    _cache_call(lib.bsa_cache_write, k, _p(k), _p(v), _p(cache), _p(k_sum), _p(page_table), _p(start), _p(count), B, T,
-                Hk, D, block_size, cache.shape[0], page_table.shape[1], _dtype_code(k))
+    _cache_call(lib.bsa_cache_write,
+                ((k, "k"), (v, "v"), (cache, "cache"), (k_sum, "k_sum"), (page_table, "page_table"), (start, "start"),
+                 (count, "count")), B, T, Hk, D, block_size, pages, page_table.shape[1], _dtype_code(k))
 
 
 def bsa_cache_read(cache, page_table, start, T: int, block_size: int, dtype: torch.dtype = torch.bfloat16, count=None,
@@ -662,69 +694,43 @@ def bsa_cache_read(cache, page_table, start, T: int, block_size: int, dtype: tor
     """Keys and values [B, T, H_kv, D] of the positions start[b] + t, in dtype (or
     k_out's). Rows t >= count[b] of k_out and v_out stay as they are; tensors
     that the call makes hold zeros there."""
-    if cache.dim() != 4 or cache.shape[3] % 72:
-        raise ValueError(f"cache has shape {tuple(cache.shape)}, expected [num_pages, H_kv, block_size / 64, 72 D]")
-    B, Hk, D = page_table.shape[0], cache.shape[1], cache.shape[3] // 72
-    _check_cache(cache, Hk, D, block_size)
+    pages, Hk, D = _cache_sizes(cache, block_size)
+    B = page_table.shape[0]
     _check_seqs(page_table, start, count, B)
     new = torch.empty if count is None else torch.zeros
     if k_out is None:
         k_out = new((B, T, Hk, D), device=cache.device, dtype=dtype if v_out is None else v_out.dtype)
     if v_out is None:
         v_out = new((B, T, Hk, D), device=cache.device, dtype=k_out.dtype)
-    _shape(k_out, (B, T, Hk, D), "k_out")
-    _shape(v_out, (B, T, Hk, D), "v_out")
-    if k_out.dtype != v_out.dtype:
-        raise TypeError("k_out and v_out must share one dtype")
-    _same_device((cache, "cache"), (page_table, "page_table"), (start, "start"), (count, "count"), (k_out, "k_out"),
-                 (v_out, "v_out"))
-    _cache_call(lib.bsa_cache_read, cache, _p(cache), _p(page_table), _p(start), _p(count), _p(k_out), _p(v_out), B, T,
-                Hk, D, block_size, cache.shape[0], page_table.shape[1], _dtype_code(k_out))
+    _is(k_out, (B, T, Hk, D), k_out.dtype, "k_out")
+    _is(v_out, (B, T, Hk, D), k_out.dtype, "v_out")
+    _cache_call(lib.bsa_cache_read,
+                ((cache, "cache"), (page_table, "page_table"), (start, "start"), (count, "count"), (k_out, "k_out"),
+                 (v_out, "v_out")), B, T, Hk, D, block_size, pages, page_table.shape[1], _dtype_code(k_out))
     return k_out, v_out
-
-
-def _check_step_q(q, Hk: int, D: int):
-    if q.dim() != 4 or q.shape[3] != D or Hk < 1 or q.shape[2] % Hk:
-        raise ValueError(f"q has shape {tuple(q.shape)}, expected [B, T, H, {D}] with H a multiple of {Hk}")
 
 
 def bsa_cache_block_topk(q, k_sum, page_table, start, topk: int, block_size: int, count=None,
                          idx_out: torch.Tensor | None = None, flags: int = 0) -> torch.Tensor:
     """Blocks [B, H_kv, topk] int32 of the largest scores of the step's queries q
     [B, T, H, D], ascending, padded with -1."""
-    if k_sum.dim() != 3:
-        raise ValueError("k_sum must be [num_pages, H_kv, D]")
-    Hk, D = k_sum.shape[1:]
-    _check_step_q(q, Hk, D)
-    _check_k_sum(k_sum, None, Hk, D)
-    B, T, H, _ = q.shape
+    if k_sum.dim() != 3 or k_sum.dtype is not torch.float32:
+        raise ValueError("k_sum must be [num_pages, H_kv, D] float32")
+    pages, Hk, D = k_sum.shape
+    B, T, H = _check_step_q(q, Hk, D)
     _check_seqs(page_table, start, count, B)
-    if idx_out is not None:
-        _shape(idx_out, (B, Hk, topk), "idx_out")
-        if idx_out.dtype != torch.int32:
-            raise TypeError("idx_out must be int32")
-    _same_device((q, "q"), (k_sum, "k_sum"), (page_table, "page_table"), (start, "start"), (count, "count"),
-                 (idx_out, "idx_out"))
-    idx = idx_out if idx_out is not None else torch.empty((B, Hk, max(topk, 0)), device=q.device, dtype=torch.int32)
-    _cache_call(lib.bsa_cache_block_topk, q, _p(q), _p(k_sum), _p(page_table), _p(start), _p(count), _p(idx), B, T, H,
-                Hk, D, block_size, k_sum.shape[0], page_table.shape[1], topk, _dtype_code(q), flags)
-    return idx
+    if idx_out is None:
+        idx_out = torch.empty((B, Hk, max(topk, 0)), device=q.device, dtype=torch.int32)
+    else:
+        _is(idx_out, (B, Hk, topk), torch.int32, "idx_out")
+    _cache_call(lib.bsa_cache_block_topk,
+                ((q, "q"), (k_sum, "k_sum"), (page_table, "page_table"), (start, "start"), (count, "count"),
+                 (idx_out, "idx_out")), B, T, H, Hk, D, block_size, pages, page_table.shape[1], topk, _dtype_code(q), flags)
+    return idx_out
 
 
 def bsa_cache_attn_workspace_bytes(B: int, T: int, H: int, H_kv: int, D: int) -> int:
     return lib.bsa_cache_attn_workspace_bytes(B, T, H, H_kv, D)
-
-
-def _step_out(out, q, count):
-    """The output of a step: rows that no token has are zeros where the call makes it."""
-    if out is not None:
-        _check_out(out, q)
-        return out
-    return (torch.empty_like if count is None else torch.zeros_like)(q)
-
-
-def _workspace(workspace, need: int, q):
-    return torch.empty(max(need, 1), device=q.device, dtype=torch.uint8) if workspace is None else workspace
 
 
 def bsa_cache_attn(q, cache, page_table, start, block_size: int, idx: torch.Tensor | None = None,
@@ -732,29 +738,31 @@ def bsa_cache_attn(q, cache, page_table, start, block_size: int, idx: torch.Tens
                    out: torch.Tensor | None = None) -> torch.Tensor:
     """Attention of q [B, T, H, D] (token t at position start[b] + t) over the
     cache: over the blocks of idx [B, H_kv, topk], or all of them without."""
-    if cache.dim() != 4 or cache.shape[3] % 72:
-        raise ValueError(f"cache has shape {tuple(cache.shape)}, expected [num_pages, H_kv, block_size / 64, 72 D]")
-    Hk, D = cache.shape[1], cache.shape[3] // 72
-    _check_step_q(q, Hk, D)
-    _check_cache(cache, Hk, D, block_size)
-    B, T, H, _ = q.shape
+    pages, Hk, D = _cache_sizes(cache, block_size)
+    B, T, H = _check_step_q(q, Hk, D)
     _check_seqs(page_table, start, count, B)
+    topk = 0
     if idx is not None:
-        if idx.dim() != 3 or tuple(idx.shape[:2]) != (B, Hk):
-            raise ValueError(f"idx has shape {tuple(idx.shape)}, expected [{B}, {Hk}, topk]")
-        if idx.dtype != torch.int32:
-            raise TypeError("idx must be int32")
-    if out is not None:
-        _check_out(out, q)
-    _same_device((q, "q"), (cache, "cache"), (page_table, "page_table"), (start, "start"), (count, "count"),
-                 (idx, "idx"), (workspace, "workspace"), (out, "out"))
-    workspace = _workspace(workspace, bsa_cache_attn_workspace_bytes(B, T, H, Hk, D), q)
+        topk = idx.shape[-1] if idx.dim() else 0
+        _is(idx, (B, Hk, topk), torch.int32, "idx")
+    if workspace is None and q.is_cuda:
+        workspace = torch.empty(max(lib.bsa_cache_attn_workspace_bytes(B, T, H, Hk, D), 1), device=q.device,
+                                dtype=torch.uint8)
     o = _step_out(out, q, count)
-    _cache_call(lib.bsa_cache_attn, q, _p(q), _p(cache), _p(page_table), _p(start), _p(count), _p(idx), _p(o), B, T, H,
-                Hk, D, block_size, cache.shape[0], page_table.shape[1], 0 if idx is None else idx.shape[2],
-                1.0 / math.sqrt(D) if scale is None else float(scale), _dtype_code(q), _p(workspace),
-                workspace.numel() * workspace.element_size())
+    _cache_call(lib.bsa_cache_attn,
+                ((q, "q"), (cache, "cache"), (page_table, "page_table"), (start, "start"), (count, "count"), (idx, "idx"),
+                 (o, "out")), B, T, H, Hk, D, block_size, pages, page_table.shape[1], topk,
+                D ** -0.5 if scale is None else float(scale), _dtype_code(q), *_room(workspace, q))
     return o
+
+
+def _room(workspace, q):
+    """Pointer and bytes of a workspace on q's device."""
+    if workspace is None:
+        return None, 0
+    if workspace.device != q.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {q.device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def bsa_cache_forward_workspace_bytes(B: int, T: int, H: int, H_kv: int, D: int, topk: int) -> int:
@@ -766,25 +774,19 @@ def bsa_cache_forward(q, k, v, cache, k_sum, page_table, start, block_size: int,
                       flags: int = 0) -> torch.Tensor:
     """One step of generation: writes k and v [B, T, H_kv, D], selects topk blocks
     (0: all) for q [B, T, H, D] and attends over them."""
-    if k.dim() != 4:
-        raise ValueError("k and v must be [B, T, H_kv, D]")
-    _shape(v, k.shape, "v")
-    B, T, Hk, D = k.shape
+    pages, Hk, D = _cache_sizes(cache, block_size)
+    B, T = _check_new(k, v, Hk, D)
     _check_step_q(q, Hk, D)
     H = q.shape[2]
-    _shape(q, (B, T, H, D), "q")
-    if not (q.dtype == k.dtype == v.dtype):
-        raise TypeError("q, k, v must share one dtype")
-    _check_cache(cache, Hk, D, block_size)
-    _check_k_sum(k_sum, cache.shape[0], Hk, D)
+    _is(q, (B, T, H, D), k.dtype, "q")
+    _is(k_sum, (pages, Hk, D), torch.float32, "k_sum")
     _check_seqs(page_table, start, count, B)
-    if out is not None:
-        _check_out(out, q)
-    _same_device((q, "q"), (k, "k"), (v, "v"), (cache, "cache"), (k_sum, "k_sum"), (page_table, "page_table"),
-                 (start, "start"), (count, "count"), (workspace, "workspace"), (out, "out"))
-    workspace = _workspace(workspace, bsa_cache_forward_workspace_bytes(B, T, H, Hk, D, topk), q)
+    if workspace is None and q.is_cuda:
+        workspace = torch.empty(max(lib.bsa_cache_forward_workspace_bytes(B, T, H, Hk, D, topk), 1), device=q.device,
+                                dtype=torch.uint8)
     o = _step_out(out, q, count)
-    _cache_call(lib.bsa_cache_forward, q, _p(q), _p(k), _p(v), _p(cache), _p(k_sum), _p(page_table), _p(start),
-                _p(count), _p(o), B, T, H, Hk, D, block_size, cache.shape[0], page_table.shape[1], topk, _dtype_code(q),
-                flags, _p(workspace), workspace.numel() * workspace.element_size())
+    _cache_call(lib.bsa_cache_forward,
+                ((q, "q"), (k, "k"), (v, "v"), (cache, "cache"), (k_sum, "k_sum"), (page_table, "page_table"),
+                 (start, "start"), (count, "count"), (o, "out")), B, T, H, Hk, D, block_size, pages, page_table.shape[1],
+                topk, _dtype_code(q), flags, *_room(workspace, q))
     return o
