@@ -1381,15 +1381,15 @@ bsa_status bsa_cache_read(const void* cache, const int32_t* page_table, const in
   if ((s = check_tensors({cache, k, v})) != BSA_OK) return s;
   if ((s = check_cache_lists(page_table, start, count, nullptr)) != BSA_OK) return s;
   if ((s = check_device()) != BSA_OK) return s;
-  const long total = static_cast<long>(B) * T * H_kv * (D / 8);
-  const long grid = (total + 255) / 256;
-  if (grid > 0x7fffffffl) return fail(BSA_ERR_UNSUPPORTED, "read grid too large");
+  const long long nslot = (static_cast<long long>(T) + 62) / 64 + 1;  // tiles that T tokens touch
+  const long long grid = nslot * B * H_kv;
+  if (grid > 0x7fffffffll) return fail(BSA_ERR_UNSUPPORTED, "read grid too large");
   const bsa::CacheSeqs seqs{page_table, start, count, T, num_pages, max_blocks, block_size};
   const cudaError_t e = by_type(dt, D, [&](auto t, auto d) {
     using E = decltype(t);
-    return launch_pdl(bsa::cache_read_kernel<E, decltype(d)::value>, static_cast<unsigned>(grid), 256, 0,
+    return launch_pdl(bsa::cache_read_kernel<E, decltype(d)::value>, static_cast<unsigned>(grid), 128, 0,
                       static_cast<cudaStream_t>(stream), static_cast<const uint8_t*>(cache), static_cast<E*>(k),
-                      static_cast<E*>(v), seqs, H_kv, total);
+                      static_cast<E*>(v), seqs, H_kv, static_cast<int>(nslot));
   });
   if ((s = launched(e, "cache_read_kernel launch")) != BSA_OK) return s;
   return ok();

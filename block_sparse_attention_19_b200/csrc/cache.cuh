@@ -85,19 +85,68 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return d;
 }
 
-// Eight consecutive channels of x as float32.
-__device__ __forceinline__ void load_octet(const __nv_bfloat16* x, float (&f)[8]) {
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>(x));
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Eight consecutive channels as they lie in memory.
+template <typename T>
+struct Octet;
+template <>
+struct Octet<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* x) { u = __ldg(reinterpret_cast<const uint4*>(x)); }
+  __device__ __forceinline__ void floats(float (&f)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
+  // The largest and smallest value over this and the seven other lanes of an aligned group of eight, NaN if one is:
+  // on bfloat16 pairs, the smallest negated beside the largest, so that one exchange and one maximum serve both.
+  __device__ __forceinline__ void range(float& mx, float& mn) const {
+    const uint32_t hi = pair_max(pair_max(u.x, u.y), pair_max(u.z, u.w));
+    const uint32_t lo = pair_min(pair_min(u.x, u.y), pair_min(u.z, u.w));
+    uint32_t m = pair_max(__byte_perm(hi, lo, 0x5410) ^ 0x80000000u, __byte_perm(hi, lo, 0x7632) ^ 0x80000000u);
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2) m = pair_max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    mx = __uint_as_float(m << 16);
+    mn = -__uint_as_float(m & 0xffff0000u);
+  }
+  static __device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  static __device__ __forceinline__ uint32_t pair_min(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+};
+template <>
+struct Octet<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* x) {
+    a = __ldg(reinterpret_cast<const float4*>(x)), b = __ldg(reinterpret_cast<const float4*>(x) + 1);
+  }
+  __device__ __forceinline__ void floats(float (&f)[8]) const {
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+  __device__ __forceinline__ void range(float& mx, float& mn) const {
+    mx = max_nan(max_nan(max_nan(a.x, a.y), max_nan(a.z, a.w)), max_nan(max_nan(b.x, b.y), max_nan(b.z, b.w)));
+    mn = min_nan(min_nan(min_nan(a.x, a.y), min_nan(a.z, a.w)), min_nan(min_nan(b.x, b.y), min_nan(b.z, b.w)));
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2) {
+      mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, d));
+    }
+  }
+};
+__device__ __forceinline__ void load_octet(const __nv_bfloat16* x, float (&f)[8]) {
+  Octet<__nv_bfloat16> o;
+  o.load(x);
+  o.floats(f);
 }
 __device__ __forceinline__ void load_octet(const float* x, float (&f)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(x)), b = __ldg(reinterpret_cast<const float4*>(x) + 1);
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  Octet<float> o;
+  o.load(x);
+  o.floats(f);
 }
 __device__ __forceinline__ void store_octet(__nv_bfloat16* x, const float (&f)[8]) {
   *reinterpret_cast<uint4*>(x) =
@@ -118,43 +167,50 @@ __device__ __forceinline__ void unpack_sz(uint32_t sz, float& scale, float& zero
 
 // Quantises the eight channels of this lane; the eight lanes of an aligned
 // group hold the 64 channels that share a scale and a zero. Returns the codes
-// packed in channel order (lowest bits first), replaces f by the values that
-// they stand for, and gives the (scale, zero) pair.
+// packed in channel order (lowest bits first) and gives them as whole floats in
+// `code` (pairs), and the (scale, zero) pair.
 //   z = bf16(min), s = bf16((max - z) * fl(1/15)), code = rint((x - z) * fl(1/s))
 // in float32. A scale below the smallest normal float32 becomes 0 (all codes
 // 0: the group reads back as its zero). A group with a NaN or infinity, or
 // with a range beyond float32, gets NaN for both and reads back as NaN.
-__device__ __forceinline__ uint32_t quantise_octet(float (&f)[8], uint32_t& sz) {
-  float mx = f[0], mn = f[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) mx = max_nan(mx, f[i]), mn = min_nan(mn, f[i]);
-#pragma unroll
-  for (int d = 1; d < 8; d *= 2) {
-    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, d));
-  }
-  const __nv_bfloat16 zb = __float2bfloat16_rn(mn);
-  float z = __bfloat162float(zb);
+template <typename T>
+__device__ __forceinline__ uint32_t quantise_octet(const Octet<T>& x, uint32_t& sz, uint64_t (&code)[4]) {
+  float mx, mn;
+  x.range(mx, mn);
+  const float z = __bfloat162float(__float2bfloat16_rn(mn));
   const float range = __fsub_rn(mx, z);
-  const __nv_bfloat16 sb = __float2bfloat16_rn(__fmul_rn(range, 1.0f / 15.0f));
-  float s = __bfloat162float(sb);
+  float s = __bfloat162float(__float2bfloat16_rn(__fmul_rn(range, 1.0f / 15.0f)));
   if (s < 1.17549435e-38f) s = 0.0f;  // a NaN stays
   const bool finite = fabsf(range) < CUDART_INF_F;
   const float inv = s > 0.0f && finite ? __frcp_rn(s) : 0.0f;
-  if (!finite) s = z = CUDART_NAN_F;
-  sz = (__float_as_uint(s) >> 16) | (__float_as_uint(z) & 0xffff0000u);
+  sz = finite ? (__float_as_uint(s) >> 16) | __float_as_uint(z) : 0x7fff7fffu;
+  float f[8];
+  x.floats(f);
+  // 12582912 = 1.5 * 2^23: adding it rounds to a whole number, half to even, and leaves that number in the low bits
+  constexpr float kRound = 12582912.0f;
+  const uint64_t zz = f2(z, z), rr = f2(kRound, kRound);
   uint32_t w = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    // 12582912 = 1.5 * 2^23: adding it rounds to a whole number, half to even,
-    // and leaves that number in the low bits
-    float t = __fmul_rn(__fsub_rn(f[i], z), inv);
-    t = fminf(fmaxf(t, 0.0f), 15.0f);  // also turns a NaN (not finite: 0 * inf) into 0
-    t = __fadd_rn(t, 12582912.0f);
-    w |= (__float_as_uint(t) & 15u) << (4 * i);
-    f[i] = cache_value(s, z, __fsub_rn(t, 12582912.0f));
+  for (int i = 3; i >= 0; --i) {
+    // the products are single instructions: a packed product and the packed sum after it become one fused
+    // multiply-add, whose codes differ at halves
+    float lo, hi;
+    f2_split(f2_sub(f2(f[2 * i], f[2 * i + 1]), zz), lo, hi);
+    lo = __fmul_rn(lo, inv), hi = __fmul_rn(hi, inv);
+    if constexpr (sizeof(T) == 4) {
+      // a float32 minimum may lie below its bfloat16 zero; of bfloat16 values no quotient leaves [0, 15.04], since
+      // the zero is one of them and the scale is off by at most 2^-8
+      lo = fminf(fmaxf(lo, 0.0f), 15.0f), hi = fminf(fmaxf(hi, 0.0f), 15.0f);
+    }
+    const uint64_t t = f2_add(f2(lo, hi), rr);
+    f2_split(t, lo, hi);
+    // the constant's bits above the number fall out at the top, or are taken off below
+    w = (w << 8) + (__float_as_uint(hi) << 4) + __float_as_uint(lo);
+    code[i] = f2_sub(t, rr);
   }
-  return w;
+  // w = sum of (bits(kRound) + code) << 4 i: the lowest three of those constants reach into 32 bits
+  constexpr uint32_t kBits = 0x4b400000u;
+  return w - (kBits + (kBits << 4) + (kBits << 8));
 }
 
 // ------------------------------------------------------------------ write
@@ -164,17 +220,21 @@ __device__ __forceinline__ uint32_t quantise_octet(float (&f)[8], uint32_t& sz) 
 // last new one, as the cache holds them, so that k_sum depends on the cache's
 // contents alone: not on how the tokens were cut into calls, nor on rows that a
 // later write with a smaller start has replaced. Row r of a tile belongs to a
-// fixed warp and lane group and the partial sums are joined in a fixed order.
+// fixed warp and lane group, which adds up scale code and zero of its rows
+// apart, in their order, and the partial sums are joined in a fixed order.
+// Bound for a prompt: the bytes (2 to 4 in, 9/16 out an element), as long as the
+// quantising stays below about 12 instructions an element: the arithmetic runs
+// on float32 pairs, minima and maxima on bfloat16 pairs.
 template <typename T, int D>
 __global__ void __launch_bounds__(128) cache_write_kernel(const T* __restrict__ k, const T* __restrict__ v,
                                                           uint8_t* cache, float* k_sum, CacheSeqs s, int Hkv,
                                                           int nslot) {
-  constexpr int kOct = D / 8, kRows = 32 / kOct, kStep = 4 * kRows;
+  constexpr int kOct = D / 8, kRows = 32 / kOct, kStep = 4 * kRows, kSteps = kCacheTile / kStep;
   __shared__ float part[4][D];
   pdl_launch_dependents();
   pdl_wait();
   const int h = blockIdx.x % Hkv, slot = blockIdx.x / Hkv % nslot, b = blockIdx.x / Hkv / nslot;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, oct = lane % kOct;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, oct = lane % kOct, sub = lane / kOct;
   int start, count;
   seq_step(s, b, start, count);
   const int block = start / s.bs + slot;
@@ -182,52 +242,109 @@ __global__ void __launch_bounds__(128) cache_write_kernel(const T* __restrict__ 
   const int r0 = max(start - first, 0), r1 = min(start + count - first, s.bs);  // new rows
   const int page = seq_page(s, b, block);
   if (page < 0 || r1 <= r0) return;
-  float acc[8] = {};
+  // row r of the block (r0 <= r < r1) of k and v
+  const long row_of = static_cast<long>(Hkv) * D, at0 = ((static_cast<long>(b) * s.T + first - start) * Hkv + h) * D + oct * 8;
+  uint64_t acc[4] = {};  // sums of scale code, in channel pairs
+  float acc_zero = 0.0f;
+
+  // one row (of tile `base`, the tile's row r): K's and V's octets quantised and stored. kWhole: row r's partner in
+  // its pair is new too
+  auto write_row = [&](uint8_t* base, int r, const Octet<T>& xk, const Octet<T>& xv, bool fresh, auto whole) {
+    uint32_t sz;
+    uint64_t code[4];
+    uint32_t w = quantise_octet(xk, sz, code);
+    const int at = (r * (D / 64) + oct / 8) * 4;
+    if (fresh) {
+      *reinterpret_cast<uint32_t*>(base + r * (D / 2) + k_word(oct, D)) = w;
+      if (oct % 8 == 0) *reinterpret_cast<uint32_t*>(base + cache_ks_offset(D) + at) = sz;
+      float sc, ze;
+      unpack_sz(sz, sc, ze);
+      const uint64_t ss = f2(sc, sc);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = f2_fma(ss, code[i], acc[i]);
+      acc_zero += ze;
+    }
+    w = quantise_octet(xv, sz, code);
+    uint8_t* pair = base + cache_v_offset(D) + (r / 2) * D;
+    if constexpr (decltype(whole)::value) {
+      // the pair's two rows are neighbouring lane groups: each makes one word of both rows' halves
+      const bool odd = r % 2;
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? w : w >> 16, kOct);
+      const uint32_t both = odd ? __byte_perm(other, w, 0x7610) : __byte_perm(w, other, 0x5410);
+      *reinterpret_cast<uint32_t*>(pair + v_word(r / 2, oct, odd, D)) = both;
+    } else if (fresh) {
+      *reinterpret_cast<uint16_t*>(pair + (r % 2) * 2 + v_word(r / 2, oct, 0, D)) = static_cast<uint16_t>(w);
+      *reinterpret_cast<uint16_t*>(pair + (r % 2) * 2 + v_word(r / 2, oct, 1, D)) = static_cast<uint16_t>(w >> 16);
+    }
+    if (fresh && oct % 8 == 0) *reinterpret_cast<uint32_t*>(base + cache_vs_offset(D) + at) = sz;
+  };
+
   for (int tile = 0; tile * kCacheTile < r1; ++tile) {
     uint8_t* base = tile_ptr(cache, page, h, tile, Hkv, s.bs, D);
-    for (int r = warp * kRows + lane / kOct; r < kCacheTile; r += kStep) {
-      const int row = tile * kCacheTile + r;
-      uint32_t* kw = reinterpret_cast<uint32_t*>(base + r * (D / 2) + k_word(oct, D));
-      uint32_t* ks = reinterpret_cast<uint32_t*>(base + cache_ks_offset(D) + (r * (D / 64) + oct / 8) * 4);
-      float f[8] = {};
-      uint32_t sz = 0;
-      const bool fresh = row >= r0 && row < r1;
-      const long at = ((static_cast<long>(b) * s.T + (first + row - start)) * Hkv + h) * D + oct * 8;
-      if (fresh) load_octet(k + at, f);
-      uint32_t w = quantise_octet(f, sz);
-      if (fresh) {
-        *kw = w;
-        if (oct % 8 == 0) *ks = sz;
-      } else if (row < r0) {
-        w = *kw;
+    const int t0 = tile * kCacheTile, mine = warp * kRows + sub;  // this lane group's rows: mine + step kStep
+    if (r0 <= t0 && r1 >= t0 + kCacheTile) {
+      // a tile of new rows only
+      constexpr int kAhead = 4 * sizeof(__nv_bfloat16) / sizeof(T);  // rows in flight
+#pragma unroll 1
+      for (int i0 = 0; i0 < kSteps; i0 += kAhead) {
+        Octet<T> xk[kAhead], xv[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const long at = at0 + (t0 + mine + (i0 + i) * kStep) * row_of;
+          xk[i].load(k + at);
+          xv[i].load(v + at);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) write_row(base, mine + (i0 + i) * kStep, xk[i], xv[i], true, std::true_type{});
+      }
+      continue;
+    }
+    // older rows: their keys' codes and scales, all in flight together
+    uint32_t w[kSteps], sz[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int r = mine + i * kStep;
+      w[i] = sz[i] = 0;
+      if (t0 + r < r0) {
+        w[i] = *reinterpret_cast<const uint32_t*>(base + r * (D / 2) + k_word(oct, D));
+        sz[i] = *reinterpret_cast<const uint32_t*>(base + cache_ks_offset(D) + (r * (D / 64) + oct / 8) * 4);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+      if (t0 + mine + i * kStep < r0) {
         float sc, ze;
-        unpack_sz(*ks, sc, ze);
+        unpack_sz(sz[i], sc, ze);
+        const uint64_t ss = f2(sc, sc);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = cache_value(sc, ze, static_cast<float>((w >> (4 * i)) & 15u));
+        for (int c = 0; c < 4; ++c)
+          acc[c] = f2_fma(ss, f2(static_cast<float>(w[i] >> (8 * c) & 15u), static_cast<float>(w[i] >> (8 * c + 4) & 15u)),
+                          acc[c]);
+        acc_zero += ze;
       }
-      if (row < r1) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += f[i];
-      }
-      if (fresh) load_octet(v + at, f);
-      w = quantise_octet(f, sz);
-      if (fresh) {
-        uint8_t* pair = base + cache_v_offset(D) + (r / 2) * D + (r % 2) * 2;
-        *reinterpret_cast<uint16_t*>(pair + v_word(r / 2, oct, 0, D)) = static_cast<uint16_t>(w);
-        *reinterpret_cast<uint16_t*>(pair + v_word(r / 2, oct, 1, D)) = static_cast<uint16_t>(w >> 16);
-        if (oct % 8 == 0)
-          *reinterpret_cast<uint32_t*>(base + cache_vs_offset(D) + (r * (D / 64) + oct / 8) * 4) = sz;
-      }
+#pragma unroll 1
+    for (int i = 0; i < kSteps; ++i) {
+      const int low = t0 + warp * kRows + i * kStep, row = low + sub;  // the warp's rows here begin at `low`
+      if (low + kRows <= r0 || low >= r1) continue;
+      const bool fresh = row >= r0 && row < r1;
+      Octet<T> xk, xv;
+      const long at = at0 + (fresh ? row : max(r0, low)) * row_of;  // (of a row that is there)
+      xk.load(k + at);
+      xv.load(v + at);
+      write_row(base, row - t0, xk, xv, fresh, std::false_type{});
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    float f[2];
+    f2_split(acc[i], f[0], f[1]);
 #pragma unroll
-    for (int d = kOct; d < 32; d *= 2) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], d);
-  }
-  if (lane < kOct) {
+    for (int c = 0; c < 2; ++c) {
+      f[c] += acc_zero;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) part[warp][oct * 8 + i] = acc[i];
+      for (int d = kOct; d < 32; d *= 2) f[c] += __shfl_xor_sync(0xffffffffu, f[c], d);
+      if (lane < kOct) part[warp][oct * 8 + 2 * i + c] = f[c];
+    }
   }
   __syncthreads();
   if (threadIdx.x < D)
@@ -237,43 +354,67 @@ __global__ void __launch_bounds__(128) cache_write_kernel(const T* __restrict__ 
 
 // ------------------------------------------------------------------ read
 //
-// One thread per eight channels of a token's key and value.
+// One CTA per (sequence, up to 64 rows of one tile, key/value head): a row's
+// eight channels a lane, as the writing lays them. Bound by the bytes (9/16 in, 2
+// to 4 out an element).
+__device__ __forceinline__ void octet_values(uint32_t w, uint32_t sz, float (&f)[8]) {
+  float sc, ze;
+  unpack_sz(sz, sc, ze);
+  // 2^23 + code is the float with the code in its low bits
+  constexpr float kWhole = 8388608.0f;
+  const uint64_t ss = f2(sc, sc), zz = f2(ze, ze), ww = f2(kWhole, kWhole);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t t = f2(__uint_as_float((w >> (8 * i) & 15u) | 0x4b000000u),
+                          __uint_as_float((w >> (8 * i + 4) & 15u) | 0x4b000000u));
+    f2_split(f2_fma(ss, f2_sub(t, ww), zz), f[2 * i], f[2 * i + 1]);
+  }
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256) cache_read_kernel(const uint8_t* cache, T* k, T* v, CacheSeqs s, int Hkv,
-                                                         long total) {
-  constexpr int kOct = D / 8;
+__global__ void __launch_bounds__(128) cache_read_kernel(const uint8_t* __restrict__ cache, T* k, T* v, CacheSeqs s,
+                                                         int Hkv, int nslot) {
+  constexpr int kOct = D / 8, kRows = 32 / kOct, kStep = 4 * kRows, kSteps = kCacheTile / kStep;
   pdl_launch_dependents();
   pdl_wait();
-  const long i = static_cast<long>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= total) return;
-  const int oct = static_cast<int>(i % kOct), h = static_cast<int>(i / kOct % Hkv);
-  const long row = i / kOct / Hkv;  // b * T + t
-  const int b = static_cast<int>(row / s.T), t = static_cast<int>(row % s.T);
+  const int h = blockIdx.x % Hkv, slot = blockIdx.x / Hkv % nslot, b = blockIdx.x / Hkv / nslot;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, oct = lane % kOct, sub = lane / kOct;
   int start, count;
   seq_step(s, b, start, count);
-  if (t >= count) return;
-  const int pos = start + t, page = seq_page(s, b, pos / s.bs), r = pos % kCacheTile;
-  float kf[8] = {}, vf[8] = {};
-  if (page >= 0) {
-    const uint8_t* base =
-        tile_ptr(const_cast<uint8_t*>(cache), page, h, pos % s.bs / kCacheTile, Hkv, s.bs, D);
-    const uint32_t kw = *reinterpret_cast<const uint32_t*>(base + r * (D / 2) + k_word(oct, D));
-    const uint8_t* pair = base + cache_v_offset(D) + (r / 2) * D + (r % 2) * 2;
-    const uint32_t vw = *reinterpret_cast<const uint16_t*>(pair + v_word(r / 2, oct, 0, D)) |
-                        static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(pair + v_word(r / 2, oct, 1, D)))
-                            << 16;
-    const int at = (r * (D / 64) + oct / 8) * 4;
-    float ks, kz, vs, vz;
-    unpack_sz(*reinterpret_cast<const uint32_t*>(base + cache_ks_offset(D) + at), ks, kz);
-    unpack_sz(*reinterpret_cast<const uint32_t*>(base + cache_vs_offset(D) + at), vs, vz);
+  const int first = (start / kCacheTile + slot) * kCacheTile;  // the tile's first token
+  const int r0 = max(start - first, 0), r1 = min(start + count - first, kCacheTile);
+  if (r1 <= r0) return;
+  const int page = seq_page(s, b, first / s.bs);
+  const uint8_t* base = page >= 0 ? tile_ptr(const_cast<uint8_t*>(cache), page, h, first % s.bs / kCacheTile, Hkv, s.bs, D)
+                                  : nullptr;
+  const long at0 = ((static_cast<long>(b) * s.T + first - start) * Hkv + h) * D + oct * 8;
+  uint32_t kw[kSteps], vw[kSteps], ks[kSteps], vs[kSteps];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      kf[j] = cache_value(ks, kz, static_cast<float>((kw >> (4 * j)) & 15u));
-      vf[j] = cache_value(vs, vz, static_cast<float>((vw >> (4 * j)) & 15u));
+  for (int i = 0; i < kSteps; ++i) {
+    // whole pairs are read, also where only one row of them is wanted
+    const int r = warp * kRows + sub + i * kStep, at = (r * (D / 64) + oct / 8) * 4;
+    kw[i] = vw[i] = ks[i] = vs[i] = 0;
+    if (base) {
+      kw[i] = __ldg(reinterpret_cast<const uint32_t*>(base + r * (D / 2) + k_word(oct, D)));
+      vw[i] = __ldg(reinterpret_cast<const uint32_t*>(base + cache_v_offset(D) + (r / 2) * D + v_word(r / 2, oct, r % 2, D)));
+      ks[i] = __ldg(reinterpret_cast<const uint32_t*>(base + cache_ks_offset(D) + at));
+      vs[i] = __ldg(reinterpret_cast<const uint32_t*>(base + cache_vs_offset(D) + at));
     }
   }
-  store_octet(k + i * 8, kf);
-  store_octet(v + i * 8, vf);
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int r = warp * kRows + sub + i * kStep;
+    const bool odd = r % 2;
+    // this lane read the first (even rows) or second four channels of both rows of its pair
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? vw[i] : vw[i] >> 16, kOct);
+    const uint32_t w = odd ? __byte_perm(other, vw[i], 0x7610) : __byte_perm(vw[i], other, 0x5410);
+    if (r < r0 || r >= r1) continue;
+    float f[8];
+    octet_values(kw[i], ks[i], f);
+    store_octet(k + at0 + r * static_cast<long>(Hkv) * D, f);
+    octet_values(w, vs[i], f);
+    store_octet(v + at0 + r * static_cast<long>(Hkv) * D, f);
+  }
 }
 
 // ------------------------------------------------------------------ block selection
