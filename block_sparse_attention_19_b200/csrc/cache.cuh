@@ -97,14 +97,17 @@ struct Octet<__nv_bfloat16> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
-  // The largest and smallest value over this and the seven other lanes of an aligned group of eight, NaN if one is:
-  // on bfloat16 pairs, the smallest negated beside the largest, so that one exchange and one maximum serve both.
-  __device__ __forceinline__ void range(float& mx, float& mn) const {
+  // The largest and smallest value, NaN if one is: on bfloat16 pairs, the smallest negated beside the largest, so that
+  // one exchange and one maximum serve both.
+  using Range = uint32_t;
+  __device__ __forceinline__ Range range() const {
     const uint32_t hi = pair_max(pair_max(u.x, u.y), pair_max(u.z, u.w));
     const uint32_t lo = pair_min(pair_min(u.x, u.y), pair_min(u.z, u.w));
-    uint32_t m = pair_max(__byte_perm(hi, lo, 0x5410) ^ 0x80000000u, __byte_perm(hi, lo, 0x7632) ^ 0x80000000u);
-#pragma unroll
-    for (int d = 1; d < 8; d *= 2) m = pair_max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    return pair_max(__byte_perm(hi, lo, 0x5410) ^ 0x80000000u, __byte_perm(hi, lo, 0x7632) ^ 0x80000000u);
+  }
+  static __device__ __forceinline__ Range join(Range a, Range b) { return pair_max(a, b); }
+  static __device__ __forceinline__ Range other(Range a, int d) { return __shfl_xor_sync(0xffffffffu, a, d); }
+  static __device__ __forceinline__ void limits(Range m, float& mx, float& mn) {
     mx = __uint_as_float(m << 16);
     mn = -__uint_as_float(m & 0xffff0000u);
   }
@@ -128,15 +131,19 @@ struct Octet<float> {
   __device__ __forceinline__ void floats(float (&f)[8]) const {
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
   }
-  __device__ __forceinline__ void range(float& mx, float& mn) const {
-    mx = max_nan(max_nan(max_nan(a.x, a.y), max_nan(a.z, a.w)), max_nan(max_nan(b.x, b.y), max_nan(b.z, b.w)));
-    mn = min_nan(min_nan(min_nan(a.x, a.y), min_nan(a.z, a.w)), min_nan(min_nan(b.x, b.y), min_nan(b.z, b.w)));
-#pragma unroll
-    for (int d = 1; d < 8; d *= 2) {
-      mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-      mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, d));
-    }
+  using Range = float2;  // largest, smallest
+  __device__ __forceinline__ Range range() const {
+    return make_float2(
+        max_nan(max_nan(max_nan(a.x, a.y), max_nan(a.z, a.w)), max_nan(max_nan(b.x, b.y), max_nan(b.z, b.w))),
+        min_nan(min_nan(min_nan(a.x, a.y), min_nan(a.z, a.w)), min_nan(min_nan(b.x, b.y), min_nan(b.z, b.w))));
   }
+  static __device__ __forceinline__ Range join(Range a, Range b) {
+    return make_float2(max_nan(a.x, b.x), min_nan(a.y, b.y));
+  }
+  static __device__ __forceinline__ Range other(Range a, int d) {
+    return make_float2(__shfl_xor_sync(0xffffffffu, a.x, d), __shfl_xor_sync(0xffffffffu, a.y, d));
+  }
+  static __device__ __forceinline__ void limits(Range m, float& mx, float& mn) { mx = m.x, mn = m.y; }
 };
 __device__ __forceinline__ void load_octet(const __nv_bfloat16* x, float (&f)[8]) {
   Octet<__nv_bfloat16> o;
@@ -165,25 +172,27 @@ __device__ __forceinline__ void unpack_sz(uint32_t sz, float& scale, float& zero
   zero = __uint_as_float(sz & 0xffff0000u);
 }
 
-// Quantises the eight channels of this lane; the eight lanes of an aligned
-// group hold the 64 channels that share a scale and a zero. Returns the codes
-// packed in channel order (lowest bits first) and gives them as whole floats in
-// `code` (pairs), and the (scale, zero) pair.
+// Scale and zero of a group of 64 channels with these limits, and what the
+// quantising multiplies by.
 //   z = bf16(min), s = bf16((max - z) * fl(1/15)), code = rint((x - z) * fl(1/s))
 // in float32. A scale below the smallest normal float32 becomes 0 (all codes
 // 0: the group reads back as its zero). A group with a NaN or infinity, or
 // with a range beyond float32, gets NaN for both and reads back as NaN.
-template <typename T>
-__device__ __forceinline__ uint32_t quantise_octet(const Octet<T>& x, uint32_t& sz, uint64_t (&code)[4]) {
-  float mx, mn;
-  x.range(mx, mn);
+__device__ __forceinline__ void group_scale(float mx, float mn, uint32_t& sz, float& inv) {
   const float z = __bfloat162float(__float2bfloat16_rn(mn));
   const float range = __fsub_rn(mx, z);
   float s = __bfloat162float(__float2bfloat16_rn(__fmul_rn(range, 1.0f / 15.0f)));
   if (s < 1.17549435e-38f) s = 0.0f;  // a NaN stays
   const bool finite = fabsf(range) < CUDART_INF_F;
-  const float inv = s > 0.0f && finite ? __frcp_rn(s) : 0.0f;
+  inv = s > 0.0f && finite ? __frcp_rn(s) : 0.0f;
   sz = finite ? (__float_as_uint(s) >> 16) | __float_as_uint(z) : 0x7fff7fffu;
+}
+
+// The codes of the eight channels of this lane, packed in channel order (lowest
+// bits first), and as whole floats in `code` (pairs).
+template <typename T>
+__device__ __forceinline__ uint32_t octet_codes(const Octet<T>& x, uint32_t sz, float inv, uint64_t (&code)[4]) {
+  const float z = __uint_as_float(sz & 0xffff0000u);
   float f[8];
   x.floats(f);
   // 12582912 = 1.5 * 2^23: adding it rounds to a whole number, half to even, and leaves that number in the low bits
@@ -211,6 +220,19 @@ __device__ __forceinline__ uint32_t quantise_octet(const Octet<T>& x, uint32_t& 
   // w = sum of (bits(kRound) + code) << 4 i: the lowest three of those constants reach into 32 bits
   constexpr uint32_t kBits = 0x4b400000u;
   return w - (kBits + (kBits << 4) + (kBits << 8));
+}
+
+// Range, scale and codes of one octet; the eight lanes of an aligned group hold
+// the 64 channels that share a scale.
+template <typename T>
+__device__ __forceinline__ uint32_t quantise_octet(const Octet<T>& x, uint32_t& sz, uint64_t (&code)[4]) {
+  typename Octet<T>::Range m = x.range();
+#pragma unroll
+  for (int d = 1; d < 8; d *= 2) m = Octet<T>::join(m, Octet<T>::other(m, d));
+  float mx, mn, inv;
+  Octet<T>::limits(m, mx, mn);
+  group_scale(mx, mn, sz, inv);
+  return octet_codes(x, sz, inv, code);
 }
 
 // ------------------------------------------------------------------ write
@@ -247,55 +269,67 @@ __global__ void __launch_bounds__(128) cache_write_kernel(const T* __restrict__ 
   uint64_t acc[4] = {};  // sums of scale code, in channel pairs
   float acc_zero = 0.0f;
 
-  // one row (of tile `base`, the tile's row r): K's and V's octets quantised and stored. kWhole: row r's partner in
-  // its pair is new too
-  auto write_row = [&](uint8_t* base, int r, const Octet<T>& xk, const Octet<T>& xv, bool fresh, auto whole) {
-    uint32_t sz;
-    uint64_t code[4];
-    uint32_t w = quantise_octet(xk, sz, code);
-    const int at = (r * (D / 64) + oct / 8) * 4;
-    if (fresh) {
-      *reinterpret_cast<uint32_t*>(base + r * (D / 2) + k_word(oct, D)) = w;
-      if (oct % 8 == 0) *reinterpret_cast<uint32_t*>(base + cache_ks_offset(D) + at) = sz;
-      float sc, ze;
-      unpack_sz(sz, sc, ze);
-      const uint64_t ss = f2(sc, sc);
+  auto add_keys = [&](uint32_t sz, const uint64_t (&code)[4]) {
+    float sc, ze;
+    unpack_sz(sz, sc, ze);
+    const uint64_t ss = f2(sc, sc);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = f2_fma(ss, code[i], acc[i]);
-      acc_zero += ze;
-    }
-    w = quantise_octet(xv, sz, code);
-    uint8_t* pair = base + cache_v_offset(D) + (r / 2) * D;
-    if constexpr (decltype(whole)::value) {
-      // the pair's two rows are neighbouring lane groups: each makes one word of both rows' halves
-      const bool odd = r % 2;
-      const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? w : w >> 16, kOct);
-      const uint32_t both = odd ? __byte_perm(other, w, 0x7610) : __byte_perm(w, other, 0x5410);
-      *reinterpret_cast<uint32_t*>(pair + v_word(r / 2, oct, odd, D)) = both;
-    } else if (fresh) {
-      *reinterpret_cast<uint16_t*>(pair + (r % 2) * 2 + v_word(r / 2, oct, 0, D)) = static_cast<uint16_t>(w);
-      *reinterpret_cast<uint16_t*>(pair + (r % 2) * 2 + v_word(r / 2, oct, 1, D)) = static_cast<uint16_t>(w >> 16);
-    }
-    if (fresh && oct % 8 == 0) *reinterpret_cast<uint32_t*>(base + cache_vs_offset(D) + at) = sz;
+    for (int i = 0; i < 4; ++i) acc[i] = f2_fma(ss, code[i], acc[i]);
+    acc_zero += ze;
   };
 
   for (int tile = 0; tile * kCacheTile < r1; ++tile) {
     uint8_t* base = tile_ptr(cache, page, h, tile, Hkv, s.bs, D);
     const int t0 = tile * kCacheTile, mine = warp * kRows + sub;  // this lane group's rows: mine + step kStep
     if (r0 <= t0 && r1 >= t0 + kCacheTile) {
-      // a tile of new rows only
-      constexpr int kAhead = 4 * sizeof(__nv_bfloat16) / sizeof(T);  // rows in flight
+      // a tile of new rows only: four rows' keys and values at a time, eight octets a lane. Each of a group's eight
+      // lanes ends up with one octet's range (four, two and one exchanges instead of three for each), computes its
+      // scale for all and stores it.
+      using X = Octet<T>;
 #pragma unroll 1
-      for (int i0 = 0; i0 < kSteps; i0 += kAhead) {
-        Octet<T> xk[kAhead], xv[kAhead];
+      for (int i0 = 0; i0 < kSteps; i0 += 4) {
+        X x[8];
+        typename X::Range m[8];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const long at = at0 + (t0 + mine + (i0 + i) * kStep) * row_of;
-          xk[i].load(k + at);
-          xv[i].load(v + at);
+          x[i].load(k + at);
+          x[4 + i].load(v + at);
         }
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) write_row(base, mine + (i0 + i) * kStep, xk[i], xv[i], true, std::true_type{});
+        for (int i = 0; i < 8; ++i) m[i] = x[i].range();
+#pragma unroll
+        for (int d = 4; d; d /= 2) {
+          const bool up = lane & d;
+#pragma unroll
+          for (int i = 0; i < d; ++i)
+            m[i] = X::join(up ? m[i + d] : m[i], X::other(up ? m[i] : m[i + d], d));
+        }
+        float mx, mn, my_inv;
+        uint32_t my_sz;
+        X::limits(m[0], mx, mn);
+        group_scale(mx, mn, my_sz, my_inv);
+        const int my_row = mine + (i0 + lane % 4) * kStep;
+        *reinterpret_cast<uint32_t*>(base + (lane & 4 ? cache_vs_offset(D) : cache_ks_offset(D)) +
+                                     (my_row * (D / 64) + oct / 8) * 4) = my_sz;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = mine + (i0 + i % 4) * kStep, from = (lane & 24) + i;
+          const uint32_t sz = __shfl_sync(0xffffffffu, my_sz, from);
+          const float inv = __shfl_sync(0xffffffffu, my_inv, from);
+          uint64_t code[4];
+          const uint32_t w = octet_codes(x[i], sz, inv, code);
+          if (i < 4) {
+            *reinterpret_cast<uint32_t*>(base + r * (D / 2) + k_word(oct, D)) = w;
+            add_keys(sz, code);
+          } else {
+            // a pair's two rows are neighbouring lane groups: each makes one word of both rows' halves
+            const bool odd = sub % 2;
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? w : w >> 16, kOct);
+            const uint32_t both = odd ? __byte_perm(other, w, 0x7610) : __byte_perm(w, other, 0x5410);
+            *reinterpret_cast<uint32_t*>(base + cache_v_offset(D) + (r / 2) * D + v_word(r / 2, oct, odd, D)) = both;
+          }
+        }
       }
       continue;
     }
@@ -313,14 +347,11 @@ __global__ void __launch_bounds__(128) cache_write_kernel(const T* __restrict__ 
 #pragma unroll
     for (int i = 0; i < kSteps; ++i)
       if (t0 + mine + i * kStep < r0) {
-        float sc, ze;
-        unpack_sz(sz[i], sc, ze);
-        const uint64_t ss = f2(sc, sc);
+        uint64_t code[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          acc[c] = f2_fma(ss, f2(static_cast<float>(w[i] >> (8 * c) & 15u), static_cast<float>(w[i] >> (8 * c + 4) & 15u)),
-                          acc[c]);
-        acc_zero += ze;
+          code[c] = f2(static_cast<float>(w[i] >> (8 * c) & 15u), static_cast<float>(w[i] >> (8 * c + 4) & 15u));
+        add_keys(sz[i], code);
       }
 #pragma unroll 1
     for (int i = 0; i < kSteps; ++i) {
@@ -331,7 +362,22 @@ __global__ void __launch_bounds__(128) cache_write_kernel(const T* __restrict__ 
       const long at = at0 + (fresh ? row : max(r0, low)) * row_of;  // (of a row that is there)
       xk.load(k + at);
       xv.load(v + at);
-      write_row(base, row - t0, xk, xv, fresh, std::false_type{});
+      const int r = row - t0, sc_at = (r * (D / 64) + oct / 8) * 4;
+      uint32_t z;
+      uint64_t code[4];
+      uint32_t c = quantise_octet(xk, z, code);
+      if (fresh) {
+        *reinterpret_cast<uint32_t*>(base + r * (D / 2) + k_word(oct, D)) = c;
+        if (oct % 8 == 0) *reinterpret_cast<uint32_t*>(base + cache_ks_offset(D) + sc_at) = z;
+        add_keys(z, code);
+      }
+      c = quantise_octet(xv, z, code);
+      if (fresh) {
+        uint8_t* to = base + cache_v_offset(D) + (r / 2) * D + (r % 2) * 2;
+        *reinterpret_cast<uint16_t*>(to + v_word(r / 2, oct, 0, D)) = static_cast<uint16_t>(c);
+        *reinterpret_cast<uint16_t*>(to + v_word(r / 2, oct, 1, D)) = static_cast<uint16_t>(c >> 16);
+        if (oct % 8 == 0) *reinterpret_cast<uint32_t*>(base + cache_vs_offset(D) + sc_at) = z;
+      }
     }
   }
 #pragma unroll
