@@ -282,44 +282,48 @@ __global__ void __launch_bounds__(128) cache_write_kernel(const T* __restrict__ 
     uint8_t* base = tile_ptr(cache, page, h, tile, Hkv, s.bs, D);
     const int t0 = tile * kCacheTile, mine = warp * kRows + sub;  // this lane group's rows: mine + step kStep
     if (r0 <= t0 && r1 >= t0 + kCacheTile) {
-      // a tile of new rows only: four rows' keys and values at a time, eight octets a lane. Each of a group's eight
-      // lanes ends up with one octet's range (four, two and one exchanges instead of three for each), computes its
-      // scale for all and stores it.
+      // a tile of new rows only: the keys and values of four (float32: two, for registers) rows at a time, so many
+      // octets a lane. Each of a group's lanes ends up with one octet's range (four, two and one exchanges instead of
+      // three for each), computes its scale for all and stores it.
       using X = Octet<T>;
+      constexpr int kAhead = sizeof(T) == 2 ? 4 : 2, kN = 2 * kAhead;
 #pragma unroll 1
-      for (int i0 = 0; i0 < kSteps; i0 += 4) {
-        X x[8];
-        typename X::Range m[8];
+      for (int i0 = 0; i0 < kSteps; i0 += kAhead) {
+        X x[kN];
+        typename X::Range m[kN];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kAhead; ++i) {
           const long at = at0 + (t0 + mine + (i0 + i) * kStep) * row_of;
           x[i].load(k + at);
-          x[4 + i].load(v + at);
+          x[kAhead + i].load(v + at);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m[i] = x[i].range();
+        for (int i = 0; i < kN; ++i) m[i] = x[i].range();
 #pragma unroll
-        for (int d = 4; d; d /= 2) {
+        for (int d = kAhead; d; d /= 2) {
           const bool up = lane & d;
 #pragma unroll
           for (int i = 0; i < d; ++i)
             m[i] = X::join(up ? m[i + d] : m[i], X::other(up ? m[i] : m[i + d], d));
         }
+#pragma unroll
+        for (int d = kN; d < 8; d *= 2) m[0] = X::join(m[0], X::other(m[0], d));
         float mx, mn, my_inv;
         uint32_t my_sz;
         X::limits(m[0], mx, mn);
         group_scale(mx, mn, my_sz, my_inv);
-        const int my_row = mine + (i0 + lane % 4) * kStep;
-        *reinterpret_cast<uint32_t*>(base + (lane & 4 ? cache_vs_offset(D) : cache_ks_offset(D)) +
-                                     (my_row * (D / 64) + oct / 8) * 4) = my_sz;
+        const int my_row = mine + (i0 + lane % kAhead) * kStep;
+        if (lane % 8 < kN)
+          *reinterpret_cast<uint32_t*>(base + (lane & kAhead ? cache_vs_offset(D) : cache_ks_offset(D)) +
+                                       (my_row * (D / 64) + oct / 8) * 4) = my_sz;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = mine + (i0 + i % 4) * kStep, from = (lane & 24) + i;
+        for (int i = 0; i < kN; ++i) {
+          const int r = mine + (i0 + i % kAhead) * kStep, from = (lane & 24) + i;
           const uint32_t sz = __shfl_sync(0xffffffffu, my_sz, from);
           const float inv = __shfl_sync(0xffffffffu, my_inv, from);
           uint64_t code[4];
           const uint32_t w = octet_codes(x[i], sz, inv, code);
-          if (i < 4) {
+          if (i < kAhead) {
             *reinterpret_cast<uint32_t*>(base + r * (D / 2) + k_word(oct, D)) = w;
             add_keys(sz, code);
           } else {
