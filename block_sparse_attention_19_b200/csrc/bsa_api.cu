@@ -1299,12 +1299,13 @@ bsa_status launched(cudaError_t e, const char* what) {
   return e == cudaSuccess ? BSA_OK : cuda_fail(e, what);
 }
 
-template <typename E, int D, int NT, int FOLD>
-cudaError_t launch_cache_attn(const void* q, const void* cache, const int32_t* idx, void* o, void* ws,
+// Launches the attention (its shape is Shape) and the joining of the units that several CTAs share.
+template <typename E, int D, typename Shape>
+cudaError_t launch_cache_attn(void (*kern)(const E*, const uint8_t*, const int32_t*, E*, float*, bsa::CacheSeqs, int, int,
+                                           int, int, float),
+                              const void* q, const void* cache, const int32_t* idx, void* o, void* ws,
                               const bsa::CacheSeqs& seqs, int B, int H, int Hkv, int topk, float scale_log2,
                               void* stream) {
-  using Shape = bsa::CaShape<D, NT, FOLD>;
-  const auto kern = bsa::cache_attn_kernel<E, D, NT, FOLD>;
   static bool attr_set[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1315,22 +1316,30 @@ cudaError_t launch_cache_attn(const void* q, const void* cache, const int32_t* i
     if (dev < 64) attr_set[dev] = true;
   }
   const int nseq = idx ? 0 : B;
-  // with a long table of sequences one CTA fewer fits an SM's 228 KB (each takes 1 KB more, and up to 2 KB of static memory)
+  // with a long table of sequences one CTA fewer fits an SM's 228 KB (each takes 1 KB more, and static memory)
   const size_t smem = Shape::smem(nseq);
   const unsigned per_sm = std::min<unsigned>(Shape::kCtas, 228 * 1024 / (smem + 3072));
   const unsigned ctas = per_sm * sm_count();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
-      launch_pdl(kern, ctas, bsa::kCaThreads, smem, st, static_cast<const E*>(q),
-                 static_cast<const uint8_t*>(cache), idx, static_cast<E*>(o), static_cast<float*>(ws), seqs, B, H, Hkv,
-                 topk, scale_log2);
+      launch_pdl(kern, ctas, bsa::kCaThreads, smem, st, static_cast<const E*>(q), static_cast<const uint8_t*>(cache), idx,
+                 static_cast<E*>(o), static_cast<float*>(ws), seqs, B, H, Hkv, topk, scale_log2);
   if (e != cudaSuccess) return e;
   // A plain launch: as a programmatic one its waiting CTAs and the next call's early ones share the SMs so that
-  // some of the latter start late (a run of dense calls: 117 against 82 us each).
-  bsa::cache_attn_join_kernel<E, D, NT, FOLD><<<static_cast<unsigned>(B) * seqs.T * H, bsa::kCaJoinWarps * 32,
-                                          (nseq + 1) * sizeof(int), st>>>(
+  // some of the latter start late (a run of dense calls: 85 against 69 us each).
+  bsa::cache_attn_join_kernel<E, D, Shape::kRows><<<static_cast<unsigned>(B) * seqs.T * H, bsa::kCaJoinWarps * 32,
+                                                    (nseq + 1) * sizeof(int), st>>>(
       static_cast<E*>(o), static_cast<const float*>(ws), seqs, B, H, Hkv, idx ? topk : 0, static_cast<int>(ctas));
   return cudaGetLastError();
+}
+
+template <typename E, int D, int FOLD, typename... Args>
+cudaError_t launch_cache_attn_narrow(Args... args) {
+  return launch_cache_attn<E, D, bsa::CaShape<D, 1, FOLD>>(bsa::cache_attn_kernel<E, D, 1, FOLD>, args...);
+}
+template <int D, int NT, typename... Args>
+cudaError_t launch_cache_attn_wide(Args... args) {
+  return launch_cache_attn<__nv_bfloat16, D, bsa::CaWide<D, NT>>(bsa::cache_attn_wide_kernel<D, NT>, args...);
 }
 
 // Calls f with a value of the element type and the head size as a constant.
@@ -1453,7 +1462,8 @@ bsa_status bsa_cache_block_topk(const void* q, const float* k_sum, const int32_t
 size_t bsa_cache_attn_workspace_bytes(int B, int T, int H, int H_kv, int D) {
   if (check_cache_dims(B, T, H, H_kv, D, 64) != BSA_OK) return 0;
   // two parts of a unit's query rows for each CTA; float32 and bfloat16 queries alike
-  const long rows = std::max(8 * bsa::CaShape<128, 1, 1>::kCtas, 16 * bsa::CaShape<128, 2, 1>::kCtas);
+  const long rows = std::max({8 * bsa::CaShape<128, 1, 1>::kCtas, 32 * bsa::CaWide<128, 4>::kCtas,
+                              40 * bsa::CaWide<128, 5>::kCtas});
   return static_cast<size_t>(sm_count()) * rows * 2 * (D + 2) * sizeof(float);
 }
 
@@ -1478,17 +1488,26 @@ bsa_status bsa_cache_attn(const void* q, const void* cache, const int32_t* page_
     using E = decltype(t);
     constexpr int kD = decltype(d)::value;
     const float sl = scale * 1.4426950408889634f;
+    const auto run = [&](auto launch) {
+      return launch(q, cache, idx, o, workspace, seqs, B, H, H_kv, topk, sl, stream);
+    };
     // Query rows of a (sequence, key/value head): up to four are folded (everything between the products once for two
-    // runs of tokens: dense 32768-token batch, four rows, XX us against 69); more than eight go 16 to a unit, whose
-    // tiles are then read and unpacked half as often. float32 queries, whose operands come in two parts, stay at 8.
+    // runs of tokens: dense 32768-token batch, four rows, 65 us against 69), up to eight fill the products' columns
+    // once. More go to the kernel whose warps share a tile, in units of equal size of up to 40 (40 rows, five new
+    // tokens of 8 heads: XX us, 41 in units of 16 rows of the other kernel). float32 queries, whose operands come in
+    // two parts, stay with the first.
     const long long rows = static_cast<long long>(T) * (H / H_kv);
-    if (rows <= 4)
-      return launch_cache_attn<E, kD, 1, 2>(q, cache, idx, o, workspace, seqs, B, H, H_kv, topk, sl, stream);
     if constexpr (sizeof(E) == 2) {
-      if (rows > 8)
-        return launch_cache_attn<E, kD, 2, 1>(q, cache, idx, o, workspace, seqs, B, H, H_kv, topk, sl, stream);
+      if (rows > 8) {
+        const long long units = (rows + 39) / 40, nt = ((rows + units - 1) / units + 7) / 8;
+        if (nt <= 2) return run([](auto... a) { return launch_cache_attn_wide<kD, 2>(a...); });
+        if (nt == 3) return run([](auto... a) { return launch_cache_attn_wide<kD, 3>(a...); });
+        if (nt == 4) return run([](auto... a) { return launch_cache_attn_wide<kD, 4>(a...); });
+        return run([](auto... a) { return launch_cache_attn_wide<kD, 5>(a...); });
+      }
     }
-    return launch_cache_attn<E, kD, 1, 1>(q, cache, idx, o, workspace, seqs, B, H, H_kv, topk, sl, stream);
+    if (rows <= 4) return run([](auto... a) { return launch_cache_attn_narrow<E, kD, 2>(a...); });
+    return run([](auto... a) { return launch_cache_attn_narrow<E, kD, 1>(a...); });
   });
   if ((s = launched(e, "cache_attn_kernel launch")) != BSA_OK) return s;
   return ok();

@@ -45,7 +45,6 @@ struct CaShape {
   static constexpr int kOStride = D + 4;  // floats of a row in the join buffer: 16-byte stores free of conflicts
   static constexpr int kJoinBytes = kCaWarps * kCols * kOStride * 4;
   static constexpr int kStages = 2 * 128 / D;  // tiles of a pair's ring
-  static constexpr int kPartFloats = kRows * (D + 2);
   static size_t smem(int nseq) {
     return 2 * static_cast<size_t>(kStages) * cache_tile_bytes(D) + kJoinBytes + (nseq + 1) * sizeof(int);
   }
@@ -194,9 +193,9 @@ __device__ __forceinline__ CaPlan make_plan(const CacheSeqs& s, int B, int Hkv, 
 // Where a CTA leaves its part of a unit that other CTAs share: slot 0 for the
 // unit that began before the CTA's tiles, slot 1 for the one that begins among
 // them. Floats: references [kRows], weight sums [kRows], sums [kRows][D].
-template <typename Shape>
+template <int kRows, int D>
 __device__ __forceinline__ float* part_of(float* ws, int cta, int slot) {
-  return ws + (static_cast<long>(cta) * 2 + slot) * Shape::kPartFloats;
+  return ws + (static_cast<long>(cta) * 2 + slot) * (kRows * (D + 2));
 }
 
 template <typename T>
@@ -660,7 +659,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT, FOLD>::kCtas))
       }
     __syncthreads();
     const bool whole = first >= begin && first + n <= end;
-    float* part = part_of<Shape>(ws, blockIdx.x, first < begin ? 0 : 1);
+    float* part = part_of<kRows, D>(ws, blockIdx.x, first < begin ? 0 : 1);
     for (int i = threadIdx.x; i < rows * D; i += kCaWarps * 32) {
       const int r = i / D, c = i % D;
       const float top = join_top(join_m[fb], r);
@@ -687,43 +686,492 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT, FOLD>::kCtas))
     for (int i = max(0, loads - kStages); i < loads; ++i) mbar_wait_teardown(&full[i % kStages], i / kStages & 1);
 }
 
+// ------------------------------------------------------------------ many query rows
+//
+// From nine query rows on (bfloat16) the work between the products and the
+// products themselves outweigh the unpacking, and a warp cannot hold the sums of
+// all channels for all rows. So the four warps of a CTA share a tile: each scores
+// 16 of its 64 tokens against all rows, leaves the weights times the values'
+// scales in shared memory in the order of the products' second operand, and after
+// one barrier sums 32 (D = 64: 16) of the channels over all 64 tokens. The rows'
+// references are the CTA's, in shared memory; a tile whose weights would leave
+// float16 raises them and is scored again. Bound: the matrix instructions, 16 NT
+// (D = 128) for 16 tokens at 2.2 cycles of an SM each, 700 cycles a tile at 40 rows
+// against 400 for its bytes.
+template <int D, int NT>
+struct CaWide {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kCtas = NT <= 4 ? 3 : 2;
+  static constexpr int kStages = 4 * 128 / D;
+  static constexpr int kGroups = D / 64, kSteps = D / 16;
+  static constexpr int kQWords = kSteps * NT * 64;            // query operands: [step][nt][lane][2]
+  static constexpr int kPWords = 2 * kGroups * 4 * NT * 64;   // weights: [buffer][group][16 tokens][nt][lane][2]
+  static size_t smem(int nseq) {
+    return static_cast<size_t>(kStages) * cache_tile_bytes(D) + (kQWords + kPWords + nseq + 1) * 4;
+  }
+};
+
+__device__ __forceinline__ uint2 load_pair(uint32_t p) {
+  uint32_t w[2];
+  load_words(p, w);
+  return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ uint64_t load_f2(const float* p) {
+  const float2 f = *reinterpret_cast<const float2*>(p);
+  return f2(f.x, f.y);
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {  // (may become part of a fused multiply-add)
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
+    cache_attn_wide_kernel(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict__ cache,
+                           const int32_t* __restrict__ idx, __nv_bfloat16* o, float* ws, CacheSeqs s, int B, int H,
+                           int Hkv, int topk, float scale_log2) {
+  using W = CaWide<D, NT>;
+  constexpr int kStages = W::kStages, kRows = W::kRows, kTile = cache_tile_bytes(D), kGroups = W::kGroups;
+  constexpr int kWords = D / 32, kMt = D / 64;  // 32-channel words; 16-channel products of a warp
+  constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint32_t* sq = reinterpret_cast<uint32_t*>(smem + kStages * kTile);
+  uint32_t* sp = sq + W::kQWords;
+  int* table = reinterpret_cast<int*>(sp + W::kPWords);
+  __shared__ uint64_t full[kStages];
+  __shared__ int tile_pos[kStages], next_pos[32];
+  __shared__ const uint8_t* next_src[32];
+  __shared__ __align__(16) float s_mul[kRows], s_qsum[kGroups][kRows], s_m[kRows];
+  __shared__ __align__(16) int s_limit[kRows];
+  __shared__ float s_cand[kCaWarps][kRows], s_l[kCaWarps][kRows], s_z[kCaWarps][kGroups][kRows];
+  __shared__ int s_flag[kCaWarps], abort_flag;
+  pdl_launch_dependents();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, G = H / Hkv, g = lane / 4, t4 = lane % 4;
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
+    fence_mbarrier_init();
+  }
+  pdl_wait();
+  const CaPlan plan = make_plan(s, B, Hkv, (s.T * G + kRows - 1) / kRows, idx ? topk : 0, gridDim.x, table);
+  const int begin = min(static_cast<long>(blockIdx.x) * plan.chunk, static_cast<long>(plan.total));
+  const int end = min(begin + plan.chunk, plan.total);
+  volatile int* abort = &abort_flag;
+
+  // warp 0: copies the next tile into its stage; where the next 32 lie is looked up at once, one lane each
+  int load = begin;
+  auto fetch = [&]() {
+    const int n0 = load - begin;
+    if (n0 % 32 == 0) {
+      const int x = load + lane;
+      int pos = -1;
+      const uint8_t* src = nullptr;
+      if (x < end) {
+        int b, unit, first, n;
+        plan.locate(x, b, unit, first, n);
+        const int h = unit / plan.row_tiles, tile = x - first, per = s.bs / kCacheTile;
+        int start, count;
+        seq_step(s, b, start, count);
+        const int block = idx ? idx[(static_cast<long>(b) * Hkv + h) * topk + tile / per] : tile / per;
+        const int page = count ? seq_page(s, b, block) : -1;
+        if (page >= 0) {
+          pos = block * s.bs + tile % per * kCacheTile;
+          src = tile_ptr(const_cast<uint8_t*>(cache), page, h, tile % per, Hkv, s.bs, D);
+          if (pos >= start + count) pos = -1;
+        }
+      }
+      next_pos[lane] = pos;
+      next_src[lane] = src;
+      __syncwarp();
+    }
+    if (lane == 0) {
+      const int st = n0 % kStages, pos = next_pos[n0 % 32];
+      tile_pos[st] = pos;
+      if (pos >= 0) {
+        mbar_arrive_expect_tx(&full[st], kTile);
+        bulk_load(smem + st * kTile, next_src[n0 % 32], kTile, &full[st]);
+      } else {
+        mbar_arrive(&full[st]);
+      }
+    }
+    __syncwarp();
+    ++load;
+  };
+  if (warp == 0)
+    while (load < end && load - begin < kStages - 1) fetch();
+
+  int stage = 0, phase = 0, buf = 0;
+  for (int x = begin; x < end;) {
+    int b, unit, first, n;
+    plan.locate(x, b, unit, first, n);
+    const int stop = min(first + n, end);
+    const int h = unit / plan.row_tiles, row0 = unit % plan.row_tiles * kRows;
+    int start, count;
+    seq_step(s, b, start, count);
+    const int rows = min(kRows, count * G - row0);  // rows with a query (may be <= 0)
+
+    // ---------------- the queries as the score products' second operand (float16, odd channels / 16: see above)
+    for (int nt = warp; nt < NT; nt += kCaWarps) {
+      const int r = nt * 8 + g, row = row0 + r;
+      float f[kWords][8], amax = 0.0f, sum[kGroups] = {};
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {
+        if (r < rows) {
+          load_octet(q + ((static_cast<long>(b) * s.T + row / G) * H + h * G + row % G) * D + w * 32 + t4 * 8, f[w]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[w][i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[w][i])), sum[w / 2] += f[w][i];
+      }
+#pragma unroll
+      for (int d = 1; d < 4; d *= 2) {
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
+      }
+      const int up = min(13 - static_cast<int>((__float_as_uint(amax) >> 23) & 255u) + 127, 126);
+      const float qscale = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[w][i] *= i % 2 ? qscale * 0.0625f : qscale;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          reinterpret_cast<uint2*>(sq)[((w * 2 + k) * NT + nt) * 32 + lane] =
+              make_uint2(pack_f16(f[w][2 * k], f[w][2 * k + 4]), pack_f16(f[w][2 * k + 1], f[w][2 * k + 5]));
+      }
+      if (t4 == 0) {
+        s_mul[r] = __uint_as_float(static_cast<uint32_t>(24 - up + 127) << 23) * scale_log2;
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) s_qsum[j][r] = sum[j] * scale_log2;
+        s_limit[r] = r < rows ? start + row / G + 1 : 0;
+        s_m[r] = -1e30f;
+      }
+    }
+    const int low_limit = start + row0 / G + 1;  // positions below it are seen by all rows
+    __syncthreads();
+
+    uint64_t l[NT], z[kGroups][NT];
+    float acc[kMt][NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      l[nt] = 0;
+#pragma unroll
+      for (int j = 0; j < kGroups; ++j) z[j][nt] = 0;
+#pragma unroll
+      for (int k = 0; k < kMt; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[k][nt][i] = 0.0f;
+    }
+
+    for (; x < stop; ++x) {
+      const int pos = mbar_wait(&full[stage], phase, abort, 803) ? tile_pos[stage] : -1;
+      const uint32_t base = smem_u32(smem) + stage * kTile;
+      const int r0 = warp * 16, p0 = pos + r0 + g;  // this thread's tokens: positions p0 and p0 + 8
+      const bool edge = pos + kCacheTile > low_limit;
+      uint64_t p[NT][2], vz[kGroups][2];
+      auto score = [&](auto masked) -> bool {
+        constexpr bool kEdge = decltype(masked)::value;
+        uint32_t a[kWords][2][4];
+        uint64_t sc[kGroups][2], ze[kGroups][2];
+        {
+          uint32_t kw[2][kWords], sz[2][kGroups];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            load_words(base + (r0 + i * 8) * (D / 2) + lane * (D / 8), kw[i]);
+            load_words(base + cache_ks_offset(D) + (r0 + i * 8 + g) * (D / 16), sz[i]);
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) {
+              float e, f;
+              unpack_sz(sz[i][j], e, f);
+              sc[j][i] = f2(e, e), ze[j][i] = f2(f, f);
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < kWords; ++w)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t u = kw[0][w] >> (8 * k), v = kw[1][w] >> (8 * k);
+              a[w][k][0] = u & kLow, a[w][k][1] = v & kLow, a[w][k][2] = u & kHigh, a[w][k][3] = v & kHigh;
+            }
+        }
+        uint64_t xs[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float dot[kGroups][4];
+#pragma unroll
+          for (int w = 0; w < kWords; ++w)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint2 bq = load_pair(smem_u32(sq) + (((w * 2 + k) * NT + nt) * 32 + lane) * 8);
+              if (w % 2 == 0 && k == 0)
+                mma_f16_first(dot[w / 2], a[w][k][0], a[w][k][1], a[w][k][2], a[w][k][3], bq.x, bq.y);
+              else
+                mma_f16(dot[w / 2], a[w][k][0], a[w][k][1], a[w][k][2], a[w][k][3], bq.x, bq.y);
+            }
+          const int col = nt * 8 + 2 * t4;
+          const uint64_t mul = load_f2(s_mul + col);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint64_t d = f2_mul(sc[0][i], f2(dot[0][2 * i], dot[0][2 * i + 1]));
+            uint64_t e = f2_mul(ze[0][i], load_f2(s_qsum[0] + col));
+            if constexpr (kGroups == 2) {
+              d = f2_fma(sc[1][i], f2(dot[1][2 * i], dot[1][2 * i + 1]), d);
+              e = f2_fma(ze[1][i], load_f2(s_qsum[1] + col), e);
+            }
+            xs[nt][i] = f2_fma(d, mul, e);
+            if constexpr (kEdge) {
+              const int2 lim = *reinterpret_cast<const int2*>(s_limit + col);
+              float lo, hi;
+              f2_split(xs[nt][i], lo, hi);
+              xs[nt][i] = f2(p0 + 8 * i < lim.x ? lo : -CUDART_INF_F, p0 + 8 * i < lim.y ? hi : -CUDART_INF_F);
+            }
+          }
+        }
+        // weights against the references as they stand, times the values' scales, in float16, to shared memory
+        uint32_t vsz[2][kGroups], high = 0;
+        float most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          load_words(base + cache_vs_offset(D) + (r0 + i * 8 + g) * (D / 16), vsz[i]);
+#pragma unroll
+          for (int j = 0; j < kGroups; ++j) {
+            const float f = __uint_as_float(vsz[i][j] & 0xffff0000u);
+            vz[j][i] = f2(f, f);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int col = nt * 8 + 2 * t4;
+          const uint64_t ref = load_f2(s_m + col);
+          uint32_t w16[kGroups][2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float lo, hi;
+            f2_split(f2_sub(xs[nt][i], ref), lo, hi);
+            lo = fast_exp2(lo), hi = fast_exp2(hi);
+            most = fmax3(most, lo, hi);
+            p[nt][i] = f2(lo, hi);
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) {
+              const float vs = __uint_as_float(vsz[i][j] << 16);
+              float wl, wh;
+              f2_split(f2_mul(p[nt][i], f2(vs, vs)), wl, wh);
+              if constexpr (kEdge) {
+                const int2 lim = *reinterpret_cast<const int2*>(s_limit + col);
+                if (p0 + 8 * i >= lim.x) wl = 0.0f;
+                if (p0 + 8 * i >= lim.y) wh = 0.0f;
+              }
+              w16[j][i] = pack_f16(wl, wh);
+              high = max_u16x2(high, w16[j][i]);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < kGroups; ++j)
+            reinterpret_cast<uint2*>(sp)[(((buf * kGroups + j) * 4 + warp) * NT + nt) * 32 + lane] =
+                make_uint2(transpose8x8(w16[j][0]), transpose8x8(w16[j][1]));
+        }
+        const bool flag = __any_sync(0xffffffffu, max_u16x2(high, 0x78007800u) != 0x78007800u || most > 0x1p90f);
+        if (flag) {
+          // the references that would make the largest weight times scale 1
+          float lv[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float vmax = 0x1p-48f;
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) vmax = fmaxf(vmax, __uint_as_float(vsz[i][j] << 16));
+            lv[i] = __log2f(vmax);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float u[2], v[2];
+            f2_split(xs[nt][0], u[0], u[1]);
+            f2_split(xs[nt][1], v[0], v[1]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float top = fmaxf(u[c] + lv[0], v[c] + lv[1]);
+#pragma unroll
+              for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+              if (g == 0) s_cand[warp][nt * 8 + 2 * t4 + c] = top;
+            }
+          }
+        }
+        return flag;
+      };
+      for (int tries = 0;; ++tries) {
+        // (every warp takes every barrier here, whatever it saw of the tile)
+        bool flag = pos >= 0 && (edge ? score(std::true_type{}) : score(std::false_type{}));
+        if (tries) flag = false;  // a NaN: no reference helps
+        if (lane == 0) s_flag[warp] = flag;
+        if (!__syncthreads_or(flag)) break;
+        // raise the references so that the largest weight times scale is 2^12
+        float now[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int col = nt * 8 + 2 * t4 + c;
+            float top = -CUDART_INF_F;
+#pragma unroll
+            for (int w = 0; w < kCaWarps; ++w)
+              if (s_flag[w]) top = fmaxf(top, s_cand[w][col]);
+            const float old = s_m[col], f = fast_exp2(old - (now[nt][c] = fmaxf(old, top - 12.0f)));
+            const uint64_t by = c ? f2(1.0f, f) : f2(f, 1.0f);
+            l[nt] = f2_mul(l[nt], by);
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) z[j][nt] = f2_mul(z[j][nt], by);
+#pragma unroll
+            for (int k = 0; k < kMt; ++k) acc[k][nt][c] *= f, acc[k][nt][2 + c] *= f;
+          }
+        __syncthreads();
+        if (warp == 0 && g == 0) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) s_m[nt * 8 + 2 * t4] = now[nt][0], s_m[nt * 8 + 2 * t4 + 1] = now[nt][1];
+        }
+        __syncthreads();
+      }
+      // every warp is past the tile before this one: its stage can be filled again
+      if (warp == 0 && load < end) fetch();
+      if (pos >= 0) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            l[nt] = f2_add(l[nt], p[nt][i]);
+            // a weight of 0 that stands for "not seen" must not meet a NaN
+            float lo, hi;
+            f2_split(p[nt][i], lo, hi);
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) {
+              if (edge) {
+                const int2 lim = *reinterpret_cast<const int2*>(s_limit + nt * 8 + 2 * t4);
+                float zl, zh, v, unused;
+                f2_split(z[j][nt], zl, zh);
+                f2_split(vz[j][i], v, unused);
+                z[j][nt] = f2(p0 + 8 * i < lim.x ? fmaf(lo, v, zl) : zl, p0 + 8 * i < lim.y ? fmaf(hi, v, zh) : zh);
+              } else {
+                z[j][nt] = f2_fma(p[nt][i], vz[j][i], z[j][nt]);
+              }
+            }
+          }
+        const int word = D == 128 ? warp : warp / 2, j = word / 2;
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+          uint32_t vw[2][1];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            load_words(base + cache_v_offset(D) + (kt * 8 + t4 + 4 * i) * D + (g ^ (2 * t4)) * (D / 8) + word * 4, vw[i]);
+          uint32_t av[kMt][4];
+#pragma unroll
+          for (int k = 0; k < kMt; ++k) {
+            const uint32_t pick = D == 128 ? (k ? 0x4341u : 0x4240u) : (warp % 2 ? 0x4341u : 0x4240u);
+            av[k][1] = __byte_perm(vw[0][0], 0, pick), av[k][0] = av[k][1] & kLow;
+            av[k][3] = __byte_perm(vw[1][0], 0, pick), av[k][2] = av[k][3] & kLow;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 bp = load_pair(smem_u32(sp) + ((((buf * kGroups + j) * 4 + kt) * NT + nt) * 32 + lane) * 8);
+#pragma unroll
+            for (int k = 0; k < kMt; ++k)
+              mma_f16(acc[k][nt], av[k][0], av[k][1], av[k][2], av[k][3], bp.x, bp.y);
+          }
+        }
+      }
+      buf ^= 1;
+      if (++stage == kStages) stage = 0, phase ^= 1;
+    }
+
+    // ---------------- the unit's part of this CTA: the warps' weight sums joined in a fixed order
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float v[1 + kGroups][2];
+      f2_split(l[nt], v[0][0], v[0][1]);
+#pragma unroll
+      for (int j = 0; j < kGroups; ++j) f2_split(z[j][nt], v[1 + j][0], v[1 + j][1]);
+#pragma unroll
+      for (int e = 0; e < 1 + kGroups; ++e)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) v[e][c] += __shfl_xor_sync(0xffffffffu, v[e][c], d);
+          if (g == 0) (e ? s_z[warp][e - 1] : s_l[warp])[nt * 8 + 2 * t4 + c] = v[e][c];
+        }
+    }
+    __syncthreads();
+    const bool whole = first >= begin && first + n <= end;
+    float* part = part_of<kRows, D>(ws, blockIdx.x, first < begin ? 0 : 1);
+    const int word = D == 128 ? warp : warp / 2;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = nt * 8 + 2 * t4 + c;
+        if (r >= rows) continue;
+        float sum = 0.0f, zero = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kCaWarps; ++w) sum += s_l[w][r], zero += s_z[w][word / 2][r];
+        const float by = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
+        const int row = row0 + r;
+        __nv_bfloat16* to = o + ((static_cast<long>(b) * s.T + row / G) * H + h * G + row % G) * D;
+#pragma unroll
+        for (int k = 0; k < kMt; ++k) {
+          const int ch = word * 32 + 4 * g + (D == 128 ? 2 * k : 2 * (warp % 2));
+          const float v0 = fmaf(acc[k][nt][c], 0x1p24f, zero) * by,
+                      v1 = fmaf(acc[k][nt][2 + c] - acc[k][nt][c], 0x1p20f, zero) * by;
+          if (whole)
+            *reinterpret_cast<uint32_t*>(to + ch) = pack_bf16x2(v0, v1);
+          else
+            *reinterpret_cast<float2*>(part + 2 * kRows + r * D + ch) = make_float2(v0, v1);
+        }
+        if (!whole && warp == 0 && g == 0) part[r] = s_m[r], part[kRows + r] = sum;
+      }
+    __syncthreads();
+  }
+  // after a wait that ran out: copies in flight end before the block's shared memory does
+  if (*abort && threadIdx.x == 0)
+    for (int i = max(begin, load - kStages); i < load; ++i)
+      mbar_wait_teardown(&full[(i - begin) % kStages], (i - begin) / kStages & 1);
+}
+
 // Joins the parts of the units that several CTAs share: one CTA per query row,
 // its 8 warps taking the parts in turn and meeting in a fixed order.
 constexpr int kCaJoinWarps = 8;
 
-template <typename T, int D, int NT, int FOLD>
+template <typename T, int D, int kRows>
 __global__ void __launch_bounds__(kCaJoinWarps * 32)
     cache_attn_join_kernel(T* o, const float* ws, CacheSeqs s, int B, int H, int Hkv, int topk, int ctas) {
-  using Shape = CaShape<D, NT, FOLD>;
   constexpr int kPer = D / 32;  // channels of a lane
   extern __shared__ int table[];
   __shared__ float sums[kCaJoinWarps][D], weights[kCaJoinWarps], tops[kCaJoinWarps];
   pdl_launch_dependents();
   pdl_wait();
   const int G = H / Hkv, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int row_tiles = (s.T * G + Shape::kRows - 1) / Shape::kRows;
+  const int row_tiles = (s.T * G + kRows - 1) / kRows;
   const CaPlan plan = make_plan(s, B, Hkv, row_tiles, topk, ctas, table);
   const int row = blockIdx.x % (s.T * G), h = blockIdx.x / (s.T * G) % Hkv, b = blockIdx.x / (s.T * G) / Hkv;
   int start, count;
   seq_step(s, b, start, count);
   if (row / G >= count) return;
-  const int unit = h * row_tiles + row / Shape::kRows, r = row % Shape::kRows;
+  const int unit = h * row_tiles + row / kRows, r = row % kRows;
   const int n = plan.tiles ? plan.tiles : (plan.prefix[b + 1] - plan.prefix[b]) / plan.per_seq;
   const int first = (plan.tiles ? b * plan.per_seq * n : plan.prefix[b]) + unit * n;
   const int c0 = first / plan.chunk, c1 = (first + n - 1) / plan.chunk;
   if (c0 == c1) return;
   float top = -1e30f;
-  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, part_of<Shape>(const_cast<float*>(ws), c, c == c0)[r]);
+  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, part_of<kRows, D>(const_cast<float*>(ws), c, c == c0)[r]);
 #pragma unroll
   for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   float val[kPer] = {}, weight = 0.0f;
 #pragma unroll 4
   for (int c = c0 + warp; c <= c1; c += kCaJoinWarps) {
-    const float* part = part_of<Shape>(const_cast<float*>(ws), c, c == c0);
+    const float* part = part_of<kRows, D>(const_cast<float*>(ws), c, c == c0);
     const float f = fast_exp2(part[r] - top);
-    weight += part[Shape::kRows + r] * f;
+    weight += part[kRows + r] * f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) val[i] = fmaf(part[2 * Shape::kRows + r * D + lane * kPer + i], f, val[i]);
+    for (int i = 0; i < kPer; ++i) val[i] = fmaf(part[2 * kRows + r * D + lane * kPer + i], f, val[i]);
   }
 #pragma unroll
   for (int i = 0; i < kPer; ++i) sums[warp][lane * kPer + i] = val[i];
