@@ -711,10 +711,18 @@ struct CaWide {
   }
 };
 
-__device__ __forceinline__ uint2 load_pair(uint32_t p) {
-  uint32_t w[2];
-  load_words(p, w);
-  return make_uint2(w[0], w[1]);
+// N consecutive 32-bit words, in one load (which the compiler may move between barriers).
+template <int N>
+__device__ __forceinline__ void get_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  } else if constexpr (N == 2) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x, w[1] = u.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
 }
 __device__ __forceinline__ uint64_t load_f2(const float* p) {
   const float2 f = *reinterpret_cast<const float2*>(p);
@@ -869,7 +877,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
 
     for (; x < stop; ++x) {
       const int pos = mbar_wait(&full[stage], phase, abort, 803) ? tile_pos[stage] : -1;
-      const uint32_t base = smem_u32(smem) + stage * kTile;
+      const uint8_t* base = smem + stage * kTile;
       const int r0 = warp * 16, p0 = pos + r0 + g;  // this thread's tokens: positions p0 and p0 + 8
       const bool edge = pos + kCacheTile > low_limit;
       uint64_t p[NT][2], vz[kGroups][2];
@@ -881,8 +889,8 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
           uint32_t kw[2][kWords], sz[2][kGroups];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            load_words(base + (r0 + i * 8) * (D / 2) + lane * (D / 8), kw[i]);
-            load_words(base + cache_ks_offset(D) + (r0 + i * 8 + g) * (D / 16), sz[i]);
+            get_words(base + (r0 + i * 8) * (D / 2) + lane * (D / 8), kw[i]);
+            get_words(base + cache_ks_offset(D) + (r0 + i * 8 + g) * (D / 16), sz[i]);
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
               float e, f;
@@ -898,28 +906,30 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
               a[w][k][0] = u & kLow, a[w][k][1] = v & kLow, a[w][k][2] = u & kHigh, a[w][k][3] = v & kHigh;
             }
         }
+        float dot[kGroups][NT][4];
+#pragma unroll
+        for (int w = 0; w < kWords; ++w)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint2 bq = reinterpret_cast<const uint2*>(sq)[((w * 2 + k) * NT + nt) * 32 + lane];
+              if (w % 2 == 0 && k == 0)
+                mma_f16_first(dot[w / 2][nt], a[w][k][0], a[w][k][1], a[w][k][2], a[w][k][3], bq.x, bq.y);
+              else
+                mma_f16(dot[w / 2][nt], a[w][k][0], a[w][k][1], a[w][k][2], a[w][k][3], bq.x, bq.y);
+            }
         uint64_t xs[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float dot[kGroups][4];
-#pragma unroll
-          for (int w = 0; w < kWords; ++w)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint2 bq = load_pair(smem_u32(sq) + (((w * 2 + k) * NT + nt) * 32 + lane) * 8);
-              if (w % 2 == 0 && k == 0)
-                mma_f16_first(dot[w / 2], a[w][k][0], a[w][k][1], a[w][k][2], a[w][k][3], bq.x, bq.y);
-              else
-                mma_f16(dot[w / 2], a[w][k][0], a[w][k][1], a[w][k][2], a[w][k][3], bq.x, bq.y);
-            }
           const int col = nt * 8 + 2 * t4;
           const uint64_t mul = load_f2(s_mul + col);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            uint64_t d = f2_mul(sc[0][i], f2(dot[0][2 * i], dot[0][2 * i + 1]));
+            uint64_t d = f2_mul(sc[0][i], f2(dot[0][nt][2 * i], dot[0][nt][2 * i + 1]));
             uint64_t e = f2_mul(ze[0][i], load_f2(s_qsum[0] + col));
             if constexpr (kGroups == 2) {
-              d = f2_fma(sc[1][i], f2(dot[1][2 * i], dot[1][2 * i + 1]), d);
+              d = f2_fma(sc[1][i], f2(dot[1][nt][2 * i], dot[1][nt][2 * i + 1]), d);
               e = f2_fma(ze[1][i], load_f2(s_qsum[1] + col), e);
             }
             xs[nt][i] = f2_fma(d, mul, e);
@@ -936,7 +946,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
         float most = 0.0f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          load_words(base + cache_vs_offset(D) + (r0 + i * 8 + g) * (D / 16), vsz[i]);
+          get_words(base + cache_vs_offset(D) + (r0 + i * 8 + g) * (D / 16), vsz[i]);
 #pragma unroll
           for (int j = 0; j < kGroups; ++j) {
             const float f = __uint_as_float(vsz[i][j] & 0xffff0000u);
@@ -1063,7 +1073,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
           uint32_t vw[2][1];
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            load_words(base + cache_v_offset(D) + (kt * 8 + t4 + 4 * i) * D + (g ^ (2 * t4)) * (D / 8) + word * 4, vw[i]);
+            get_words(base + cache_v_offset(D) + (kt * 8 + t4 + 4 * i) * D + (g ^ (2 * t4)) * (D / 8) + word * 4, vw[i]);
           uint32_t av[kMt][4];
 #pragma unroll
           for (int k = 0; k < kMt; ++k) {
@@ -1073,7 +1083,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const uint2 bp = load_pair(smem_u32(sp) + ((((buf * kGroups + j) * 4 + kt) * NT + nt) * 32 + lane) * 8);
+            const uint2 bp = reinterpret_cast<const uint2*>(sp)[(((buf * kGroups + j) * 4 + kt) * NT + nt) * 32 + lane];
 #pragma unroll
             for (int k = 0; k < kMt; ++k)
               mma_f16(acc[k][nt], av[k][0], av[k][1], av[k][2], av[k][3], bp.x, bp.y);
