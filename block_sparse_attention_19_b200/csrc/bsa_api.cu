@@ -1283,11 +1283,11 @@ bsa_status check_tensors(std::initializer_list<const void*> ps) {
   return BSA_OK;
 }
 
-// The attention counts a call's tiles of 64 tokens in 32 bits, and without an
-// index list keeps a table of the sequences in shared memory.
+// The attention counts a call's tiles of 64 tokens in 32 bits and keeps a table
+// of the sequences in shared memory.
 bsa_status check_attn_tiles(int B, int T, int H, int Hkv, int block_size, int max_blocks, int topk) {
-  if (!topk && B > bsa::kCaMaxSeqs)
-    return fail(BSA_ERR_UNSUPPORTED, "B=%d (attention over all blocks takes up to %d sequences)", B, bsa::kCaMaxSeqs);
+  if (B > bsa::kCaMaxSeqs)
+    return fail(BSA_ERR_UNSUPPORTED, "B=%d (the attention takes up to %d sequences)", B, bsa::kCaMaxSeqs);
   const double units = static_cast<double>(B) * Hkv * ((static_cast<long long>(T) * (H / Hkv) + 7) / 8);
   if (units * (topk ? topk : max_blocks) * (block_size / 64) > 2.1e9)
     return fail(BSA_ERR_UNSUPPORTED, "more than 2.1e9 tiles of 64 tokens");
@@ -1313,11 +1313,14 @@ cudaError_t launch_cache_attn(void (*kern)(const E*, const uint8_t*, const int32
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(Shape::smem(bsa::kCaMaxSeqs)));
     if (e != cudaSuccess) return e;
+    const cudaError_t j = cudaFuncSetAttribute(bsa::cache_attn_join_kernel<E, D, Shape::kRows>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(bsa::kCaMaxSeqs * sizeof(int4)));
+    if (j != cudaSuccess) return j;
     if (dev < 64) attr_set[dev] = true;
   }
-  const int nseq = idx ? 0 : B;
-  // with a long table of sequences one CTA fewer fits an SM's 228 KB (each takes 1 KB more, and static memory)
-  const size_t smem = Shape::smem(nseq);
+  // with a long table of sequences fewer CTAs fit an SM's 228 KB (each takes 1 KB more, and static memory)
+  const size_t smem = Shape::smem(B);
   const unsigned per_sm = std::min<unsigned>(Shape::kCtas, 228 * 1024 / (smem + 3072));
   const unsigned ctas = per_sm * sm_count();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1328,7 +1331,7 @@ cudaError_t launch_cache_attn(void (*kern)(const E*, const uint8_t*, const int32
   // A plain launch: as a programmatic one its waiting CTAs and the next call's early ones share the SMs so that
   // some of the latter start late (a run of dense calls: 85 against 69 us each).
   bsa::cache_attn_join_kernel<E, D, Shape::kRows><<<static_cast<unsigned>(B) * seqs.T * H, bsa::kCaJoinWarps * 32,
-                                                    (nseq + 1) * sizeof(int), st>>>(
+                                                    B * sizeof(int4), st>>>(
       static_cast<E*>(o), static_cast<const float*>(ws), seqs, B, H, Hkv, idx ? topk : 0, static_cast<int>(ctas));
   return cudaGetLastError();
 }

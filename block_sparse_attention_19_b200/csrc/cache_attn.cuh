@@ -32,7 +32,7 @@ namespace bsa {
 
 constexpr int kCaWarps = 4;  // in two pairs: a tile goes to a pair, 32 tokens to a warp
 constexpr int kCaThreads = kCaWarps * 32;
-constexpr int kCaMaxSeqs = 4096;                 // sequences whose tile counts fit the table in shared memory
+constexpr int kCaMaxSeqs = 4096;  // sequences whose plan fits in shared memory
 
 // How many query rows a unit has and how they fill the products' 8 NT columns: each once, or (FOLD = 2, up to four
 // rows) twice, the two halves for different tokens.
@@ -46,7 +46,7 @@ struct CaShape {
   static constexpr int kJoinBytes = kCaWarps * kCols * kOStride * 4;
   static constexpr int kStages = 2 * 128 / D;  // tiles of a pair's ring
   static size_t smem(int nseq) {
-    return 2 * static_cast<size_t>(kStages) * cache_tile_bytes(D) + kJoinBytes + (nseq + 1) * sizeof(int);
+    return 2 * static_cast<size_t>(kStages) * cache_tile_bytes(D) + kJoinBytes + nseq * sizeof(int4);
   }
 };
 
@@ -122,72 +122,81 @@ __device__ __forceinline__ uint32_t pack_f16_rest(float lo, float hi, uint32_t p
 // How the tiles of all units are laid in one line and cut into equal pieces, one
 // for each CTA. A unit is (sequence, key/value head, run of kRows query rows).
 struct CaPlan {
-  const int* prefix;  // without idx: tiles before sequence b, [B + 1]
-  int per_seq;        // units of a sequence
-  int row_tiles;      // units of a (sequence, head)
-  int tiles;          // with idx: tiles of every unit
+  const int4* seqs;  // [B]: tiles before the sequence, tiles of each of its units, start, count
+  int per_seq;       // units of a sequence
+  int row_tiles;     // units of a (sequence, head)
   int total, chunk;
   int B;
 
-  __device__ __forceinline__ void locate(int x, int& b, int& unit, int& first, int& n) const {
-    if (tiles) {
-      const int u = x / tiles;
-      b = u / per_seq, unit = u % per_seq, first = u * tiles, n = tiles;
-      return;
-    }
-    int lo = 0, hi = B - 1;  // the last sequence whose tiles begin at or before x
+  // The unit of tile x: its sequence and number there, first tile and tiles; the sequence's start and count.
+  struct Unit {
+    int b, unit, first, n, start, count;
+  };
+  __device__ __forceinline__ Unit locate(int x) const {
+    int lo = 0, hi = B - 1;  // the last sequence whose tiles begin at or before x (one without tiles is never last)
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
-      if (prefix[mid] <= x)
+      if (seqs[mid].x <= x)
         lo = mid;
       else
         hi = mid - 1;
     }
-    b = lo;
-    n = (prefix[b + 1] - prefix[b]) / per_seq;
-    unit = (x - prefix[b]) / n;
-    first = prefix[b] + unit * n;
+    const int4 q = seqs[lo];
+    const int unit = (x - q.x) / q.y;
+    return Unit{lo, unit, q.x + unit * q.y, q.y, q.z, q.w};
   }
+  __device__ __forceinline__ int head(int unit) const { return row_tiles == 1 ? unit : unit / row_tiles; }
+  __device__ __forceinline__ int row0(int unit, int rows) const { return row_tiles == 1 ? 0 : unit % row_tiles * rows; }
 };
 
-// Fills the plan; `table` is shared memory for B + 1 integers (not used with idx).
-// All threads of the block call it; it ends with a barrier.
+// Fills the plan; `table` is shared memory for B int4. All threads of the block call it; it ends with a barrier.
 __device__ __forceinline__ CaPlan make_plan(const CacheSeqs& s, int B, int Hkv, int row_tiles, int topk, int ctas,
-                                            int* table) {
+                                            int4* table) {
+  __shared__ int total;
   CaPlan p;
-  p.prefix = table, p.row_tiles = row_tiles, p.per_seq = Hkv * row_tiles, p.B = B;
-  p.tiles = topk * (s.bs / kCacheTile);
-  if (topk) {
-    p.total = B * p.per_seq * p.tiles;
-    __syncthreads();
-  } else {
-    // warp 0 sums up the sequences' tiles, 32 at a time
-    if (threadIdx.x < 32) {
-      int sum = 0;
-      for (int b0 = 0; b0 < B; b0 += 32) {
-        const int b = b0 + threadIdx.x;
-        int n = 0;
-        if (b < B) {
-          int start, count;
-          seq_step(s, b, start, count);
-          if (count) n = (min(start + count, s.max_blocks * s.bs) + kCacheTile - 1) / kCacheTile * p.per_seq;
-        }
-        int before = n;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-          const int other = __shfl_up_sync(0xffffffffu, before, d);
-          if (threadIdx.x >= d) before += other;
-        }
-        if (b < B) table[b] = sum + before - n;
-        sum += __shfl_sync(0xffffffffu, before, 31);
-      }
-      if (threadIdx.x == 0) table[B] = sum;
-    }
-    __syncthreads();
-    p.total = table[B];
+  p.seqs = table, p.row_tiles = row_tiles, p.per_seq = Hkv * row_tiles, p.B = B;
+  for (int b = threadIdx.x; b < B; b += blockDim.x) {
+    int start, count, n = 0;
+    seq_step(s, b, start, count);
+    if (count) n = topk ? topk * (s.bs / kCacheTile) : (min(start + count, s.max_blocks * s.bs) + kCacheTile - 1) / kCacheTile;
+    table[b] = make_int4(0, n, start, count);
   }
+  if (B > 32) __syncthreads();
+  if (threadIdx.x < 32) {  // warp 0 sums up the sequences' tiles, 32 at a time
+    __syncwarp();
+    int sum = 0;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+      const int b = b0 + threadIdx.x, n = b < B ? table[b].y * p.per_seq : 0;
+      int before = n;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int other = __shfl_up_sync(0xffffffffu, before, d);
+        if (threadIdx.x >= d) before += other;
+      }
+      if (b < B) table[b].x = sum + before - n;
+      sum += __shfl_sync(0xffffffffu, before, 31);
+    }
+    if (threadIdx.x == 0) total = sum;
+  }
+  __syncthreads();
+  p.total = total;
   p.chunk = max(1, (p.total + ctas - 1) / ctas);
   return p;
+}
+
+// Position of tile x's first token and where it lies; -1 where its block is absent or past the sequence's tokens.
+__device__ __forceinline__ int find_tile(const CacheSeqs& s, const CaPlan& plan, const uint8_t* cache,
+                                         const int32_t* idx, int x, int Hkv, int topk, int D, const uint8_t*& src) {
+  const CaPlan::Unit u = plan.locate(x);
+  const int h = plan.head(u.unit), tile = x - u.first, per = s.bs / kCacheTile, shift = per >> 1;  // (per: 1, 2, 4)
+  const int j = tile >> shift;
+  const int block = idx ? idx[(static_cast<long>(u.b) * Hkv + h) * topk + j] : j;
+  const int page = seq_page(s, u.b, block);
+  src = nullptr;
+  if (page < 0) return -1;
+  const int in = tile & (per - 1), pos = block * s.bs + in * kCacheTile;
+  src = tile_ptr(const_cast<uint8_t*>(cache), page, h, in, Hkv, s.bs, D);
+  return pos < u.start + u.count ? pos : -1;
 }
 
 // Where a CTA leaves its part of a unit that other CTAs share: slot 0 for the
@@ -220,7 +229,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT, FOLD>::kCtas))
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
   extern __shared__ __align__(128) uint8_t smem[];
   float* join = reinterpret_cast<float*>(smem + 2 * kStages * kTile);
-  int* table = reinterpret_cast<int*>(smem + 2 * kStages * kTile + Shape::kJoinBytes);
+  int4* table = reinterpret_cast<int4*>(smem + 2 * kStages * kTile + Shape::kJoinBytes);
   __shared__ uint64_t bars[2][2][kStages];
   __shared__ int tile_pos[2][kStages];  // position of the stage's first token; -1: the tile's block is absent
   __shared__ int next_pos[2][32];       // the same of the pair's next 32 tiles, and where they lie
@@ -255,20 +264,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT, FOLD>::kCtas))
       const int x = load + 2 * lane;
       int pos = -1;
       const uint8_t* src = nullptr;
-      if (x < end) {
-        int b, unit, first, n;
-        plan.locate(x, b, unit, first, n);
-        const int h = unit / plan.row_tiles, tile = x - first, per = s.bs / kCacheTile;
-        int start, count;
-        seq_step(s, b, start, count);
-        const int block = idx ? idx[(static_cast<long>(b) * Hkv + h) * topk + tile / per] : tile / per;
-        const int page = count ? seq_page(s, b, block) : -1;
-        if (page >= 0) {
-          pos = block * s.bs + tile % per * kCacheTile;
-          src = tile_ptr(const_cast<uint8_t*>(cache), page, h, tile % per, Hkv, s.bs, D);
-          if (pos >= start + count) pos = -1;
-        }
-      }
+      if (x < end) pos = find_tile(s, plan, cache, idx, x, Hkv, topk, D, src);
       next_pos[pair][lane] = pos;
       next_src[pair][lane] = src;
       __syncwarp();
@@ -288,19 +284,29 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT, FOLD>::kCtas))
     load += 2;
     if (++load_stage == kStages) load_stage = 0;
   };
-  if (leader)
-    while (loads < kStages && load < end) fetch();
-
   const int g = lane / 4, t4 = lane % 4;
   int flushes = 0, phase = 0, stage = 0, mine = begin + pair;  // this pair's next tile and its place
   for (int x = begin; x < end;) {
-    int b, unit, first, n;
-    plan.locate(x, b, unit, first, n);
+    const CaPlan::Unit u = plan.locate(x);
+    const int b = u.b, first = u.first, n = u.n, start = u.start;
     const int stop = min(first + n, end);
-    const int h = unit / plan.row_tiles, row0 = unit % plan.row_tiles * kRows;
-    int start, count;
-    seq_step(s, b, start, count);
-    const int rows = min(kRows, count * G - row0);  // rows with a query (may be <= 0)
+    const int h = plan.head(u.unit), row0 = plan.row0(u.unit, kRows);
+    const int rows = min(kRows, u.count * G - row0);  // rows with a query (may be <= 0)
+    Octet<T> raw[NT][kWords];  // this thread's queries: row nt 8 + g, channels 32 w + 8 t4 + 0..7
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = (nt * 8 + g) % kRows, row = row0 + r;
+      if (r < rows) {
+        const T* at = q + ((static_cast<long>(b) * s.T + row / G) * H + h * G + row % G) * D + t4 * 8;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) raw[nt][w].load(at + w * 32);
+      } else {
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) raw[nt][w] = Octet<T>{};
+      }
+    }
+    if (x == begin && leader)  // the first tiles' addresses and copies, while the queries come
+      while (loads < kStages && load < end) fetch();
 
     // the queries as the products' second operand, and per row what a score is multiplied by
     uint32_t qb[kSplit][kWords][2][NT][2];
@@ -310,17 +316,10 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT, FOLD>::kCtas))
     int low_limit = 0x7fffffff;  // positions below it are seen by all rows
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = (nt * 8 + g) % kRows;
-      float f[kWords][8], amax = 0.0f, sum[kGroups] = {};  // this thread: channels 32 w + 8 t4 + 0..7
-      const int row = row0 + r;
+      float f[kWords][8], amax = 0.0f, sum[kGroups] = {};
 #pragma unroll
       for (int w = 0; w < kWords; ++w) {
-        if (r < rows) {
-          load_octet(q + ((static_cast<long>(b) * s.T + row / G) * H + h * G + row % G) * D + w * 32 + t4 * 8, f[w]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[w][i] = 0.0f;
-        }
+        raw[nt][w].floats(f[w]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[w][i])), sum[w / 2] += f[w][i];
       }
@@ -707,7 +706,7 @@ struct CaWide {
   static constexpr int kQWords = kSteps * NT * 64;            // query operands: [step][nt][lane][2]
   static constexpr int kPWords = 2 * kGroups * 4 * NT * 64;   // weights: [buffer][group][16 tokens][nt][lane][2]
   static size_t smem(int nseq) {
-    return static_cast<size_t>(kStages) * cache_tile_bytes(D) + (kQWords + kPWords + nseq + 1) * 4;
+    return static_cast<size_t>(kStages) * cache_tile_bytes(D) + (kQWords + kPWords + 4 * nseq) * 4;
   }
 };
 
@@ -746,7 +745,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
   extern __shared__ __align__(128) uint8_t smem[];
   uint32_t* sq = reinterpret_cast<uint32_t*>(smem + kStages * kTile);
   uint32_t* sp = sq + W::kQWords;
-  int* table = reinterpret_cast<int*>(sp + W::kPWords);
+  int4* table = reinterpret_cast<int4*>(sp + W::kPWords);
   __shared__ uint64_t full[kStages];
   __shared__ int tile_pos[kStages], next_pos[32];
   __shared__ const uint8_t* next_src[32];
@@ -767,7 +766,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
   const int end = min(begin + plan.chunk, plan.total);
   volatile int* abort = &abort_flag;
 
-  // warp 0: copies the next tile into its stage; where the next 32 lie is looked up at once, one lane each
+  // the last warp: copies the next tile into its stage; where the next 32 lie is looked up at once, one lane each
   int load = begin;
   auto fetch = [&]() {
     const int n0 = load - begin;
@@ -775,20 +774,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
       const int x = load + lane;
       int pos = -1;
       const uint8_t* src = nullptr;
-      if (x < end) {
-        int b, unit, first, n;
-        plan.locate(x, b, unit, first, n);
-        const int h = unit / plan.row_tiles, tile = x - first, per = s.bs / kCacheTile;
-        int start, count;
-        seq_step(s, b, start, count);
-        const int block = idx ? idx[(static_cast<long>(b) * Hkv + h) * topk + tile / per] : tile / per;
-        const int page = count ? seq_page(s, b, block) : -1;
-        if (page >= 0) {
-          pos = block * s.bs + tile % per * kCacheTile;
-          src = tile_ptr(const_cast<uint8_t*>(cache), page, h, tile % per, Hkv, s.bs, D);
-          if (pos >= start + count) pos = -1;
-        }
-      }
+      if (x < end) pos = find_tile(s, plan, cache, idx, x, Hkv, topk, D, src);
       next_pos[lane] = pos;
       next_src[lane] = src;
       __syncwarp();
@@ -806,18 +792,17 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
     __syncwarp();
     ++load;
   };
-  if (warp == 0)
+  const bool loader = warp == kCaWarps - 1;
+  if (loader)
     while (load < end && load - begin < kStages - 1) fetch();
 
   int stage = 0, phase = 0, buf = 0;
   for (int x = begin; x < end;) {
-    int b, unit, first, n;
-    plan.locate(x, b, unit, first, n);
+    const CaPlan::Unit u = plan.locate(x);
+    const int b = u.b, first = u.first, n = u.n, start = u.start;
     const int stop = min(first + n, end);
-    const int h = unit / plan.row_tiles, row0 = unit % plan.row_tiles * kRows;
-    int start, count;
-    seq_step(s, b, start, count);
-    const int rows = min(kRows, count * G - row0);  // rows with a query (may be <= 0)
+    const int h = plan.head(u.unit), row0 = plan.row0(u.unit, kRows);
+    const int rows = min(kRows, u.count * G - row0);  // rows with a query (may be <= 0)
 
     // ---------------- the queries as the score products' second operand (float16, odd channels / 16: see above)
     for (int nt = warp; nt < NT; nt += kCaWarps) {
@@ -1044,7 +1029,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
         __syncthreads();
       }
       // every warp is past the tile before this one: its stage can be filled again
-      if (warp == 0 && load < end) fetch();
+      if (loader && load < end) fetch();
       if (pos >= 0) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -1141,7 +1126,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
     __syncthreads();
   }
   // after a wait that ran out: copies in flight end before the block's shared memory does
-  if (*abort && threadIdx.x == 0)
+  if (*abort && loader && lane == 0)
     for (int i = max(begin, load - kStages); i < load; ++i)
       mbar_wait_teardown(&full[(i - begin) % kStages], (i - begin) / kStages & 1);
 }
@@ -1154,7 +1139,7 @@ template <typename T, int D, int kRows>
 __global__ void __launch_bounds__(kCaJoinWarps * 32)
     cache_attn_join_kernel(T* o, const float* ws, CacheSeqs s, int B, int H, int Hkv, int topk, int ctas) {
   constexpr int kPer = D / 32;  // channels of a lane
-  extern __shared__ int table[];
+  extern __shared__ int4 table[];
   __shared__ float sums[kCaJoinWarps][D], weights[kCaJoinWarps], tops[kCaJoinWarps];
   pdl_launch_dependents();
   pdl_wait();
@@ -1162,35 +1147,53 @@ __global__ void __launch_bounds__(kCaJoinWarps * 32)
   const int row_tiles = (s.T * G + kRows - 1) / kRows;
   const CaPlan plan = make_plan(s, B, Hkv, row_tiles, topk, ctas, table);
   const int row = blockIdx.x % (s.T * G), h = blockIdx.x / (s.T * G) % Hkv, b = blockIdx.x / (s.T * G) / Hkv;
-  int start, count;
-  seq_step(s, b, start, count);
-  if (row / G >= count) return;
-  const int unit = h * row_tiles + row / kRows, r = row % kRows;
-  const int n = plan.tiles ? plan.tiles : (plan.prefix[b + 1] - plan.prefix[b]) / plan.per_seq;
-  const int first = (plan.tiles ? b * plan.per_seq * n : plan.prefix[b]) + unit * n;
-  const int c0 = first / plan.chunk, c1 = (first + n - 1) / plan.chunk;
+  const int4 seq = table[b];
+  if (row / G >= seq.w) return;
+  const int r = row % kRows, first = seq.x + (h * row_tiles + row / kRows) * seq.y;
+  const int c0 = first / plan.chunk, c1 = (first + seq.y - 1) / plan.chunk;
   if (c0 == c1) return;
-  float top = -1e30f;
-  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, part_of<kRows, D>(const_cast<float*>(ws), c, c == c0)[r]);
+  // four parts at a time in flight, each against the largest reference so far
+  constexpr int kAhead = 4;
+  float top = -1e30f, weight = 0.0f, val[kPer] = {};
+  for (int c = c0 + warp; c <= c1; c += kAhead * kCaJoinWarps) {
+    float m[kAhead], l[kAhead], v[kAhead][kPer], now = top;
 #pragma unroll
-  for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  float val[kPer] = {}, weight = 0.0f;
-#pragma unroll 4
-  for (int c = c0 + warp; c <= c1; c += kCaJoinWarps) {
-    const float* part = part_of<kRows, D>(const_cast<float*>(ws), c, c == c0);
-    const float f = fast_exp2(part[r] - top);
-    weight += part[kRows + r] * f;
+    for (int i = 0; i < kAhead; ++i) {
+      const int ci = c + i * kCaJoinWarps;
+      const float* part = part_of<kRows, D>(const_cast<float*>(ws), min(ci, c1), min(ci, c1) == c0);
+      m[i] = ci <= c1 ? part[r] : -CUDART_INF_F;
+      l[i] = part[kRows + r];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) val[i] = fmaf(part[2 * kRows + r * D + lane * kPer + i], f, val[i]);
+      for (int k = 0; k < kPer; ++k) v[i][k] = part[2 * kRows + r * D + lane * kPer + k];
+      now = fmaxf(now, m[i]);
+    }
+    const float f = fast_exp2(top - now);
+    top = now;
+    weight *= f;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) val[k] *= f;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (c + i * kCaJoinWarps > c1) break;  // (a part read twice for nothing may hold a NaN)
+      const float e = fast_exp2(m[i] - top);
+      weight = fmaf(l[i], e, weight);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) val[k] = fmaf(v[i][k], e, val[k]);
+    }
   }
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) sums[warp][lane * kPer + i] = val[i];
-  if (lane == 0) weights[warp] = weight;
+  for (int k = 0; k < kPer; ++k) sums[warp][lane * kPer + k] = val[k];
+  if (lane == 0) weights[warp] = weight, tops[warp] = top;
   __syncthreads();
   if (threadIdx.x < D) {
-    float v = 0.0f, w = 0.0f;
+    float most = tops[0], v = 0.0f, w = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kCaJoinWarps; ++i) v += sums[i][threadIdx.x], w += weights[i];
+    for (int i = 1; i < kCaJoinWarps; ++i) most = fmaxf(most, tops[i]);
+#pragma unroll
+    for (int i = 0; i < kCaJoinWarps; ++i) {
+      const float e = fast_exp2(tops[i] - most);
+      v = fmaf(sums[i][threadIdx.x], e, v), w = fmaf(weights[i], e, w);
+    }
     store_out(o + ((static_cast<long>(b) * s.T + row / G) * H + h * G + row % G) * D + threadIdx.x,
               w == 0.0f ? 0.0f : v / w);
   }
