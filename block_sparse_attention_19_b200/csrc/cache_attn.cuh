@@ -865,7 +865,8 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
       const uint8_t* base = smem + stage * kTile;
       const int r0 = warp * 16, p0 = pos + r0 + g;  // this thread's tokens: positions p0 and p0 + 8
       const bool edge = pos + kCacheTile > low_limit;
-      uint64_t p[NT][2], vz[kGroups][2];
+      uint64_t p[NT][2];
+      uint32_t vsz[2][kGroups];
       auto score = [&](auto masked) -> bool {
         constexpr bool kEdge = decltype(masked)::value;
         uint32_t a[kWords][2][4];
@@ -927,15 +928,16 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
           }
         }
         // weights against the references as they stand, times the values' scales, in float16, to shared memory
-        uint32_t vsz[2][kGroups], high = 0;
+        uint32_t high = 0;
         float most = 0.0f;
+        uint64_t vs[kGroups][2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           get_words(base + cache_vs_offset(D) + (r0 + i * 8 + g) * (D / 16), vsz[i]);
 #pragma unroll
           for (int j = 0; j < kGroups; ++j) {
-            const float f = __uint_as_float(vsz[i][j] & 0xffff0000u);
-            vz[j][i] = f2(f, f);
+            const float f = __uint_as_float(vsz[i][j] << 16);
+            vs[j][i] = f2(f, f);
           }
         }
 #pragma unroll
@@ -952,9 +954,8 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
             p[nt][i] = f2(lo, hi);
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
-              const float vs = __uint_as_float(vsz[i][j] << 16);
               float wl, wh;
-              f2_split(f2_mul(p[nt][i], f2(vs, vs)), wl, wh);
+              f2_split(f2_mul(p[nt][i], vs[j][i]), wl, wh);
               if constexpr (kEdge) {
                 const int2 lim = *reinterpret_cast<const int2*>(s_limit + col);
                 if (p0 + 8 * i >= lim.x) wl = 0.0f;
@@ -1031,27 +1032,33 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
       // every warp is past the tile before this one: its stage can be filled again
       if (loader && load < end) fetch();
       if (pos >= 0) {
+        auto add_up = [&](auto masked) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            l[nt] = f2_add(l[nt], p[nt][i]);
-            // a weight of 0 that stands for "not seen" must not meet a NaN
-            float lo, hi;
-            f2_split(p[nt][i], lo, hi);
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
-              if (edge) {
-                const int2 lim = *reinterpret_cast<const int2*>(s_limit + nt * 8 + 2 * t4);
-                float zl, zh, v, unused;
-                f2_split(z[j][nt], zl, zh);
-                f2_split(vz[j][i], v, unused);
-                z[j][nt] = f2(p0 + 8 * i < lim.x ? fmaf(lo, v, zl) : zl, p0 + 8 * i < lim.y ? fmaf(hi, v, zh) : zh);
-              } else {
-                z[j][nt] = f2_fma(p[nt][i], vz[j][i], z[j][nt]);
+              const float v = __uint_as_float(vsz[i][j] & 0xffff0000u);
+              const uint64_t vv = f2(v, v);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if (j == 0) l[nt] = f2_add(l[nt], p[nt][i]);
+                if constexpr (decltype(masked)::value) {
+                  // a weight of 0 that stands for "not seen" must not meet a NaN
+                  const int2 lim = *reinterpret_cast<const int2*>(s_limit + nt * 8 + 2 * t4);
+                  float lo, hi, zl, zh;
+                  f2_split(p[nt][i], lo, hi);
+                  f2_split(z[j][nt], zl, zh);
+                  z[j][nt] = f2(p0 + 8 * i < lim.x ? fmaf(lo, v, zl) : zl, p0 + 8 * i < lim.y ? fmaf(hi, v, zh) : zh);
+                } else {
+                  z[j][nt] = f2_fma(p[nt][i], vv, z[j][nt]);
+                }
               }
             }
-          }
+        };
+        if (edge)
+          add_up(std::true_type{});
+        else
+          add_up(std::false_type{});
         const int word = D == 128 ? warp : warp / 2, j = word / 2;
 #pragma unroll
         for (int kt = 0; kt < 4; ++kt) {
