@@ -860,15 +860,16 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
         for (int i = 0; i < 4; ++i) acc[k][nt][i] = 0.0f;
     }
 
+    bool fresh = true;
     for (; x < stop; ++x) {
       const int pos = mbar_wait(&full[stage], phase, abort, 803) ? tile_pos[stage] : -1;
       const uint8_t* base = smem + stage * kTile;
       const int r0 = warp * 16, p0 = pos + r0 + g;  // this thread's tokens: positions p0 and p0 + 8
       const bool edge = pos + kCacheTile > low_limit;
-      uint64_t p[NT][2];
+      uint64_t xs[NT][2], p[NT][2], vs[kGroups][2];
       uint32_t vsz[2][kGroups];
-      auto score = [&](auto masked) -> bool {
-        constexpr bool kEdge = decltype(masked)::value;
+      // the scores of this thread's tokens and columns, and its tokens' value scales
+      auto score = [&](auto masked) {
         uint32_t a[kWords][2][4];
         uint64_t sc[kGroups][2], ze[kGroups][2];
         {
@@ -877,11 +878,14 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
           for (int i = 0; i < 2; ++i) {
             get_words(base + (r0 + i * 8) * (D / 2) + lane * (D / 8), kw[i]);
             get_words(base + cache_ks_offset(D) + (r0 + i * 8 + g) * (D / 16), sz[i]);
+            get_words(base + cache_vs_offset(D) + (r0 + i * 8 + g) * (D / 16), vsz[i]);
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
               float e, f;
               unpack_sz(sz[i][j], e, f);
               sc[j][i] = f2(e, e), ze[j][i] = f2(f, f);
+              e = __uint_as_float(vsz[i][j] << 16);
+              vs[j][i] = f2(e, e);
             }
           }
 #pragma unroll
@@ -898,112 +902,112 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
 #pragma unroll
           for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint2 bq = reinterpret_cast<const uint2*>(sq)[((w * 2 + k) * NT + nt) * 32 + lane];
-              if (w % 2 == 0 && k == 0)
-                mma_f16_first(dot[w / 2][nt], a[w][k][0], a[w][k][1], a[w][k][2], a[w][k][3], bq.x, bq.y);
-              else
-                mma_f16(dot[w / 2][nt], a[w][k][0], a[w][k][1], a[w][k][2], a[w][k][3], bq.x, bq.y);
-            }
-        uint64_t xs[NT][2];
+            for (int nt = 0; nt < NT; ++nt)
+              {
+                const uint2 bq = reinterpret_cast<const uint2*>(sq)[((w * 2 + k) * NT + nt) * 32 + lane];
+                if (w % 2 == 0 && k == 0)
+                  mma_f16_first(dot[w / 2][nt], a[w][k][0], a[w][k][1], a[w][k][2], a[w][k][3], bq.x, bq.y);
+                else
+                  mma_f16(dot[w / 2][nt], a[w][k][0], a[w][k][1], a[w][k][2], a[w][k][3], bq.x, bq.y);
+              }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int col = nt * 8 + 2 * t4;
-          const uint64_t mul = load_f2(s_mul + col);
+        for (int nt = 0; nt < NT; ++nt)
+          {
+            const int col = nt * 8 + 2 * t4;
+            const uint64_t mul = load_f2(s_mul + col);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint64_t d = f2_mul(sc[0][i], f2(dot[0][nt][2 * i], dot[0][nt][2 * i + 1]));
-            uint64_t e = f2_mul(ze[0][i], load_f2(s_qsum[0] + col));
-            if constexpr (kGroups == 2) {
-              d = f2_fma(sc[1][i], f2(dot[1][nt][2 * i], dot[1][nt][2 * i + 1]), d);
-              e = f2_fma(ze[1][i], load_f2(s_qsum[1] + col), e);
-            }
-            xs[nt][i] = f2_fma(d, mul, e);
-            if constexpr (kEdge) {
-              const int2 lim = *reinterpret_cast<const int2*>(s_limit + col);
-              float lo, hi;
-              f2_split(xs[nt][i], lo, hi);
-              xs[nt][i] = f2(p0 + 8 * i < lim.x ? lo : -CUDART_INF_F, p0 + 8 * i < lim.y ? hi : -CUDART_INF_F);
+            for (int i = 0; i < 2; ++i) {
+              uint64_t d = f2_mul(sc[0][i], f2(dot[0][nt][2 * i], dot[0][nt][2 * i + 1]));
+              uint64_t e = f2_mul(ze[0][i], load_f2(s_qsum[0] + col));
+              if constexpr (kGroups == 2) {
+                d = f2_fma(sc[1][i], f2(dot[1][nt][2 * i], dot[1][nt][2 * i + 1]), d);
+                e = f2_fma(ze[1][i], load_f2(s_qsum[1] + col), e);
+              }
+              xs[nt][i] = f2_fma(d, mul, e);
+              if constexpr (decltype(masked)::value) {
+                const int2 lim = *reinterpret_cast<const int2*>(s_limit + col);
+                float lo, hi;
+                f2_split(xs[nt][i], lo, hi);
+                xs[nt][i] = f2(p0 + 8 * i < lim.x ? lo : -CUDART_INF_F, p0 + 8 * i < lim.y ? hi : -CUDART_INF_F);
+              }
             }
           }
-        }
-        // weights against the references as they stand, times the values' scales, in float16, to shared memory
+      };
+      // weights against the references as they stand, times the values' scales, in float16, to shared memory. True
+      // where one leaves float16 (from 2^15 on: 0x7800) or is beyond 2^90 (scales near zero).
+      auto weigh = [&](auto masked) -> bool {
         uint32_t high = 0;
         float most = 0.0f;
-        uint64_t vs[kGroups][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          {
+            const int col = nt * 8 + 2 * t4;
+            const uint64_t ref = load_f2(s_m + col);
+            uint32_t w16[kGroups][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float lo, hi;
+              f2_split(f2_sub(xs[nt][i], ref), lo, hi);
+              lo = fast_exp2(lo), hi = fast_exp2(hi);
+              most = fmax3(most, lo, hi);
+              p[nt][i] = f2(lo, hi);
+#pragma unroll
+              for (int j = 0; j < kGroups; ++j) {
+                float wl, wh;
+                f2_split(f2_mul(p[nt][i], vs[j][i]), wl, wh);
+                if constexpr (decltype(masked)::value) {
+                  const int2 lim = *reinterpret_cast<const int2*>(s_limit + col);
+                  if (p0 + 8 * i >= lim.x) wl = 0.0f;
+                  if (p0 + 8 * i >= lim.y) wh = 0.0f;
+                }
+                w16[j][i] = pack_f16(wl, wh);
+                high = max_u16x2(high, w16[j][i]);
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j)
+              reinterpret_cast<uint2*>(sp)[(((buf * kGroups + j) * 4 + warp) * NT + nt) * 32 + lane] =
+                  make_uint2(transpose8x8(w16[j][0]), transpose8x8(w16[j][1]));
+          }
+        return __any_sync(0xffffffffu, max_u16x2(high, 0x78007800u) != 0x78007800u || most > 0x1p90f);
+      };
+      if (pos >= 0) {
+        if (edge)
+          score(std::true_type{});
+        else
+          score(std::false_type{});
+      }
+      // (every warp takes every barrier here, whatever it saw of the tile; a unit's first tile sets the references
+      // before it is weighed)
+      const bool flag = pos >= 0 && (fresh || (edge ? weigh(std::true_type{}) : weigh(std::false_type{})));
+      if (flag) {
+        // the references that would make the largest weight times scale 1
+        float lv[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          get_words(base + cache_vs_offset(D) + (r0 + i * 8 + g) * (D / 16), vsz[i]);
+          float vmax = 0x1p-48f;
 #pragma unroll
-          for (int j = 0; j < kGroups; ++j) {
-            const float f = __uint_as_float(vsz[i][j] << 16);
-            vs[j][i] = f2(f, f);
-          }
+          for (int j = 0; j < kGroups; ++j) vmax = fmaxf(vmax, __uint_as_float(vsz[i][j] << 16));
+          lv[i] = __log2f(vmax);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const int col = nt * 8 + 2 * t4;
-          const uint64_t ref = load_f2(s_m + col);
-          uint32_t w16[kGroups][2];
+          float e[2], f[2];
+          f2_split(xs[nt][0], e[0], e[1]);
+          f2_split(xs[nt][1], f[0], f[1]);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float lo, hi;
-            f2_split(f2_sub(xs[nt][i], ref), lo, hi);
-            lo = fast_exp2(lo), hi = fast_exp2(hi);
-            most = fmax3(most, lo, hi);
-            p[nt][i] = f2(lo, hi);
+          for (int c = 0; c < 2; ++c) {
+            float top = fmaxf(e[c] + lv[0], f[c] + lv[1]);
 #pragma unroll
-            for (int j = 0; j < kGroups; ++j) {
-              float wl, wh;
-              f2_split(f2_mul(p[nt][i], vs[j][i]), wl, wh);
-              if constexpr (kEdge) {
-                const int2 lim = *reinterpret_cast<const int2*>(s_limit + col);
-                if (p0 + 8 * i >= lim.x) wl = 0.0f;
-                if (p0 + 8 * i >= lim.y) wh = 0.0f;
-              }
-              w16[j][i] = pack_f16(wl, wh);
-              high = max_u16x2(high, w16[j][i]);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < kGroups; ++j)
-            reinterpret_cast<uint2*>(sp)[(((buf * kGroups + j) * 4 + warp) * NT + nt) * 32 + lane] =
-                make_uint2(transpose8x8(w16[j][0]), transpose8x8(w16[j][1]));
-        }
-        const bool flag = __any_sync(0xffffffffu, max_u16x2(high, 0x78007800u) != 0x78007800u || most > 0x1p90f);
-        if (flag) {
-          // the references that would make the largest weight times scale 1
-          float lv[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float vmax = 0x1p-48f;
-#pragma unroll
-            for (int j = 0; j < kGroups; ++j) vmax = fmaxf(vmax, __uint_as_float(vsz[i][j] << 16));
-            lv[i] = __log2f(vmax);
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float u[2], v[2];
-            f2_split(xs[nt][0], u[0], u[1]);
-            f2_split(xs[nt][1], v[0], v[1]);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float top = fmaxf(u[c] + lv[0], v[c] + lv[1]);
-#pragma unroll
-              for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-              if (g == 0) s_cand[warp][nt * 8 + 2 * t4 + c] = top;
-            }
+            for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            if (g == 0) s_cand[warp][nt * 8 + 2 * t4 + c] = top;
           }
         }
-        return flag;
-      };
-      for (int tries = 0;; ++tries) {
-        // (every warp takes every barrier here, whatever it saw of the tile)
-        bool flag = pos >= 0 && (edge ? score(std::true_type{}) : score(std::false_type{}));
-        if (tries) flag = false;  // a NaN: no reference helps
-        if (lane == 0) s_flag[warp] = flag;
-        if (!__syncthreads_or(flag)) break;
-        // raise the references so that the largest weight times scale is 2^12
+      }
+      if (lane == 0) s_flag[warp] = flag;
+      if (__syncthreads_or(flag)) {
+        fresh = false;
+        // raise the references so that the largest weight times scale is 2^12, and weigh again (a NaN stays one)
         float now[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -1027,6 +1031,8 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) s_m[nt * 8 + 2 * t4] = now[nt][0], s_m[nt * 8 + 2 * t4 + 1] = now[nt][1];
         }
+        __syncthreads();
+        if (pos >= 0) weigh(std::true_type{});
         __syncthreads();
       }
       // every warp is past the tile before this one: its stage can be filled again
