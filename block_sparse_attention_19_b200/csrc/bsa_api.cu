@@ -1338,7 +1338,7 @@ cudaError_t launch_cache_attn(void (*kern)(const E*, const uint8_t*, const int32
 
 template <typename E, int D, int FOLD, typename... Args>
 cudaError_t launch_cache_attn_narrow(Args... args) {
-  return launch_cache_attn<E, D, bsa::CaShape<D, 1, FOLD>>(bsa::cache_attn_kernel<E, D, 1, FOLD>, args...);
+  return launch_cache_attn<E, D, bsa::CaShape<D, FOLD>>(bsa::cache_attn_kernel<E, D, FOLD>, args...);
 }
 template <int D, int NT, typename... Args>
 cudaError_t launch_cache_attn_wide(Args... args) {
@@ -1465,7 +1465,7 @@ bsa_status bsa_cache_block_topk(const void* q, const float* k_sum, const int32_t
 size_t bsa_cache_attn_workspace_bytes(int B, int T, int H, int H_kv, int D) {
   if (check_cache_dims(B, T, H, H_kv, D, 64) != BSA_OK) return 0;
   // two parts of a unit's query rows for each CTA; float32 and bfloat16 queries alike
-  const long rows = std::max({8 * bsa::CaShape<128, 1, 1>::kCtas, 32 * bsa::CaWide<128, 4>::kCtas,
+  const long rows = std::max({8 * bsa::CaShape<128, 1>::kCtas, 32 * bsa::CaWide<128, 4>::kCtas,
                               40 * bsa::CaWide<128, 5>::kCtas});
   return static_cast<size_t>(sm_count()) * rows * 2 * (D + 2) * sizeof(float);
 }

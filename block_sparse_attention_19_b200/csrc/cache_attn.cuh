@@ -34,14 +34,13 @@ constexpr int kCaWarps = 4;  // in two pairs: a tile goes to a pair, 32 tokens t
 constexpr int kCaThreads = kCaWarps * 32;
 constexpr int kCaMaxSeqs = 4096;  // sequences whose plan fits in shared memory
 
-// How many query rows a unit has and how they fill the products' 8 NT columns: each once, or (FOLD = 2, up to four
+// How many query rows a unit has and how they fill the products' eight columns: each once, or (FOLD = 2, up to four
 // rows) twice, the two halves for different tokens.
-template <int D, int NT, int FOLD>
+template <int D, int FOLD>
 struct CaShape {
-  static_assert(FOLD == 1 || NT == 1);
-  static constexpr int kCols = 8 * NT;
+  static constexpr int kCols = 8;
   static constexpr int kRows = kCols / FOLD;  // query rows of a unit
-  static constexpr int kCtas = NT == 1 ? 4 : 3;  // CTAs of an SM: four (three) warps to each of its quarters
+  static constexpr int kCtas = 4;  // CTAs of an SM: four warps to each of its quarters
   static constexpr int kOStride = D + 4;  // floats of a row in the join buffer: 16-byte stores free of conflicts
   static constexpr int kJoinBytes = kCaWarps * kCols * kOStride * 4;
   static constexpr int kStages = 2 * 128 / D;  // tiles of a pair's ring
@@ -215,17 +214,17 @@ __device__ __forceinline__ void store_out(T* o, float x) {
     *o = x;
 }
 
-template <typename T, int D, int NT, int FOLD>
-__global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT, FOLD>::kCtas))
+template <typename T, int D, int FOLD>
+__global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
     cache_attn_kernel(const T* __restrict__ q, const uint8_t* __restrict__ cache, const int32_t* __restrict__ idx, T* o,
                       float* ws, CacheSeqs s, int B, int H, int Hkv, int topk, float scale_log2) {
-  using Shape = CaShape<D, NT, FOLD>;
+  using Shape = CaShape<D, FOLD>;
   constexpr int kStages = Shape::kStages, kRows = Shape::kRows, kCols = Shape::kCols, kTile = cache_tile_bytes(D);
   constexpr int kWords = D / 32, kGroups = D / 64;
   constexpr int kSplit = sizeof(T) == 4 ? 2 : 1;  // float16 parts of a query element and of a weight
   // runs of 16 tokens computed together; folded, two runs share the columns and everything between the products is
   // computed once for both, each thread looking after the tokens of its half
-  constexpr int kRuns = NT * kSplit == 1 || FOLD == 2 ? 2 : 1, kSoft = kRuns / FOLD;
+  constexpr int kRuns = kSplit == 1 || FOLD == 2 ? 2 : 1, kSoft = kRuns / FOLD;
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
   extern __shared__ __align__(128) uint8_t smem[];
   float* join = reinterpret_cast<float*>(smem + 2 * kStages * kTile);
@@ -292,116 +291,107 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT, FOLD>::kCtas))
     const int stop = min(first + n, end);
     const int h = plan.head(u.unit), row0 = plan.row0(u.unit, kRows);
     const int rows = min(kRows, u.count * G - row0);  // rows with a query (may be <= 0)
-    Octet<T> raw[NT][kWords];  // this thread's queries: row nt 8 + g, channels 32 w + 8 t4 + 0..7
+    Octet<T> raw[kWords];  // this thread's queries: row g, channels 32 w + 8 t4 + 0..7
+    const int r = g % kRows, row = row0 + r;
+    if (r < rows) {
+      const T* at = q + ((static_cast<long>(b) * s.T + row / G) * H + h * G + row % G) * D + t4 * 8;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = (nt * 8 + g) % kRows, row = row0 + r;
-      if (r < rows) {
-        const T* at = q + ((static_cast<long>(b) * s.T + row / G) * H + h * G + row % G) * D + t4 * 8;
+      for (int w = 0; w < kWords; ++w) raw[w].load(at + w * 32);
+    } else {
 #pragma unroll
-        for (int w = 0; w < kWords; ++w) raw[nt][w].load(at + w * 32);
-      } else {
-#pragma unroll
-        for (int w = 0; w < kWords; ++w) raw[nt][w] = Octet<T>{};
-      }
+      for (int w = 0; w < kWords; ++w) raw[w] = Octet<T>{};
     }
     if (x == begin && leader)  // the first tiles' addresses and copies, while the queries come
       while (loads < kStages && load < end) fetch();
 
     // the queries as the products' second operand, and per row what a score is multiplied by
-    uint32_t qb[kSplit][kWords][2][NT][2];
-    uint32_t zb[NT][2];
-    float mul[NT][2], qsum[2][kGroups];  // qsum: folded only, in the place of zb
-    int limit[NT][2];
+    uint32_t qb[kSplit][kWords][2][2];
+    uint32_t zb[2];
+    float mul[2], qsum[2][kGroups];  // qsum: folded only, in the place of zb
+    int limit[2];
     int low_limit = 0x7fffffff;  // positions below it are seen by all rows
+    float f[kWords][8], amax = 0.0f, sum[kGroups] = {};
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float f[kWords][8], amax = 0.0f, sum[kGroups] = {};
+    for (int w = 0; w < kWords; ++w) {
+      raw[w].floats(f[w]);
 #pragma unroll
-      for (int w = 0; w < kWords; ++w) {
-        raw[nt][w].floats(f[w]);
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[w][i])), sum[w / 2] += f[w][i];
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[w][i])), sum[w / 2] += f[w][i];
-      }
+    for (int d = 1; d < 4; d *= 2) {
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
 #pragma unroll
-      for (int d = 1; d < 4; d *= 2) {
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+      for (int j = 0; j < kGroups; ++j) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
+    }
+    // the largest element goes to [2^13, 2^14): float16 holds the eight bits of a bfloat16 element down to 2^-27
+    // (odd channels 2^-23) of it
+    const int up = min(13 - static_cast<int>((__float_as_uint(amax) >> 23) & 255u) + 127, 126);
+    const float qscale = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+    const float back = __uint_as_float(static_cast<uint32_t>(24 - up + 127) << 23) * scale_log2;
 #pragma unroll
-        for (int j = 0; j < kGroups; ++j) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
-      }
-      // the largest element goes to [2^13, 2^14): float16 holds the eight bits of a bfloat16 element down to 2^-27
-      // (odd channels 2^-23) of it
-      const int up = min(13 - static_cast<int>((__float_as_uint(amax) >> 23) & 255u) + 127, 126);
-      const float qscale = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
-      const float back = __uint_as_float(static_cast<uint32_t>(24 - up + 127) << 23) * scale_log2;
+    for (int w = 0; w < kWords; ++w) {
 #pragma unroll
-      for (int w = 0; w < kWords; ++w) {
+      for (int i = 0; i < 8; ++i) f[w][i] *= i % 2 ? qscale * 0.0625f : qscale;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[w][i] *= i % 2 ? qscale * 0.0625f : qscale;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          qb[0][w][k][nt][0] = pack_f16(f[w][2 * k], f[w][2 * k + 4]);
-          qb[0][w][k][nt][1] = pack_f16(f[w][2 * k + 1], f[w][2 * k + 5]);
-          if constexpr (kSplit == 2) {
-            qb[1][w][k][nt][0] = pack_f16_rest(f[w][2 * k], f[w][2 * k + 4], qb[0][w][k][nt][0]);
-            qb[1][w][k][nt][1] = pack_f16_rest(f[w][2 * k + 1], f[w][2 * k + 5], qb[0][w][k][nt][1]);
-          }
+      for (int k = 0; k < 2; ++k) {
+        qb[0][w][k][0] = pack_f16(f[w][2 * k], f[w][2 * k + 4]);
+        qb[0][w][k][1] = pack_f16(f[w][2 * k + 1], f[w][2 * k + 5]);
+        if constexpr (kSplit == 2) {
+          qb[1][w][k][0] = pack_f16_rest(f[w][2 * k], f[w][2 * k + 4], qb[0][w][k][0]);
+          qb[1][w][k][1] = pack_f16_rest(f[w][2 * k + 1], f[w][2 * k + 5], qb[0][w][k][1]);
         }
       }
-      // second operand of zero . (sum of q's channels): a token's (scale, zero) words are the first, group t4 % 2's
-      // in this thread's columns, and the sum meets the zero half in up to four bfloat16 parts
-      {
-        float rest = (kGroups == 2 && t4 % 2 ? sum[kGroups - 1] : sum[0]) * scale_log2;
-        uint32_t parts[4];
+    }
+    // second operand of zero . (sum of q's channels): a token's (scale, zero) words are the first, group t4 % 2's
+    // in this thread's columns, and the sum meets the zero half in up to four bfloat16 parts
+    {
+      float rest = (kGroups == 2 && t4 % 2 ? sum[kGroups - 1] : sum[0]) * scale_log2;
+      uint32_t parts[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __nv_bfloat16 h = __float2bfloat16_rn(rest);
-          parts[i] = static_cast<uint32_t>(__bfloat16_as_ushort(h)) << 16;  // the zero half
-          rest -= __bfloat162float(h);
-        }
-        if (kGroups == 2) {
-          zb[nt][0] = t4 < 2 ? parts[0] : parts[1], zb[nt][1] = t4 < 2 ? parts[2] : parts[3];
-        } else {
-          zb[nt][0] = t4 < 2 ? (t4 ? parts[1] : parts[0]) : (t4 == 2 ? parts[2] : parts[3]);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(rest);
+        parts[i] = static_cast<uint32_t>(__bfloat16_as_ushort(h)) << 16;  // the zero half
+        rest -= __bfloat162float(h);
       }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {  // this thread's scores belong to rows 2 t4 and 2 t4 + 1
-        const int from = (2 * t4 + c) * 4;
-        mul[nt][c] = __shfl_sync(0xffffffffu, back, from);
-        if constexpr (FOLD == 2) {
-#pragma unroll
-          for (int j = 0; j < kGroups; ++j) qsum[c][j] = __shfl_sync(0xffffffffu, sum[j] * scale_log2, from);
-        }
-        const int rr = (nt * 8 + 2 * t4 + c) % kRows;
-        limit[nt][c] = rr < rows ? start + (row0 + rr) / G + 1 : 0;
+      if (kGroups == 2) {
+        zb[0] = t4 < 2 ? parts[0] : parts[1], zb[1] = t4 < 2 ? parts[2] : parts[3];
+      } else {
+        zb[0] = t4 < 2 ? (t4 ? parts[1] : parts[0]) : (t4 == 2 ? parts[2] : parts[3]);
       }
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {  // this thread's scores belong to rows 2 t4 and 2 t4 + 1
+      const int from = (2 * t4 + c) * 4;
+      mul[c] = __shfl_sync(0xffffffffu, back, from);
+      if constexpr (FOLD == 2) {
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) qsum[c][j] = __shfl_sync(0xffffffffu, sum[j] * scale_log2, from);
+      }
+      const int rr = (2 * t4 + c) % kRows;
+      limit[c] = rr < rows ? start + (row0 + rr) / G + 1 : 0;
     }
     low_limit = start + row0 / G + 1;
 
-    float m[NT][2], l[NT][2], z[NT][2][kGroups], acc[kWords][2][NT][4];
+    float m[2], l[2], z[2][kGroups], acc[kWords][2][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int c = 0; c < 2; ++c) {
+      m[c] = -1e30f, l[c] = 0.0f;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        m[nt][c] = -1e30f, l[nt][c] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kGroups; ++j) z[nt][c][j] = 0.0f;
-      }
-#pragma unroll
-      for (int w = 0; w < kWords; ++w)
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[w][k][nt][i] = 0.0f;
+      for (int j = 0; j < kGroups; ++j) z[c][j] = 0.0f;
     }
+#pragma unroll
+    for (int w = 0; w < kWords; ++w)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[w][k][i] = 0.0f;
 
     // kRuns runs of 16 tokens of a tile, from row r0: their scores, weights and sums. kEdge: some row does not see
     // some token.
     auto tokens = [&](uint32_t base, int pos, int r0, auto edge) {
       constexpr bool kEdge = decltype(edge)::value;
       const int half = FOLD == 2 ? t4 / 2 : 0;  // the run that this thread looks after
-      float xs[kSoft][NT][4], dot[kRuns][kGroups][NT][4], zero[kRuns][NT][4];
+      float xs[kSoft][4], dot[kRuns][kGroups][4], zero[kRuns][4];
       uint32_t ksz[kSoft][2][kGroups], vsz[kSoft][2][kGroups];
 #pragma unroll
       for (int u = 0; u < kSoft; ++u)
@@ -419,11 +409,8 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT, FOLD>::kCtas))
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             load_words(base + cache_ks_offset(D) + (r + i * 8 + g) * (D / 16) + (t4 % kGroups) * 4, zw[i]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_bf16_k8_first(zero[e][nt], zw[0][0], zw[1][0], zb[nt][0]);
-            if constexpr (kGroups == 2) mma_bf16_k8(zero[e][nt], zw[0][0], zw[1][0], zb[nt][1]);
-          }
+          mma_bf16_k8_first(zero[e], zw[0][0], zw[1][0], zb[0]);
+          if constexpr (kGroups == 2) mma_bf16_k8(zero[e], zw[0][0], zw[1][0], zb[1]);
         }
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
@@ -432,13 +419,11 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT, FOLD>::kCtas))
             const uint32_t u = kw[0][w] >> (8 * k), v = kw[1][w] >> (8 * k);
             const uint32_t a0 = u & kLow, a1 = v & kLow, a2 = u & kHigh, a3 = v & kHigh;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int sp = 0; sp < kSplit; ++sp)
-                if (w % 2 == 0 && k == 0 && sp == 0)
-                  mma_f16_first(dot[e][w / 2][nt], a0, a1, a2, a3, qb[sp][w][k][nt][0], qb[sp][w][k][nt][1]);
-                else
-                  mma_f16(dot[e][w / 2][nt], a0, a1, a2, a3, qb[sp][w][k][nt][0], qb[sp][w][k][nt][1]);
+            for (int sp = 0; sp < kSplit; ++sp)
+              if (w % 2 == 0 && k == 0 && sp == 0)
+                mma_f16_first(dot[e][w / 2], a0, a1, a2, a3, qb[sp][w][k][0], qb[sp][w][k][1]);
+              else
+                mma_f16(dot[e][w / 2], a0, a1, a2, a3, qb[sp][w][k][0], qb[sp][w][k][1]);
           }
         }
       }
@@ -448,129 +433,115 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT, FOLD>::kCtas))
         for (int i = 0; i < 2; ++i) {
           load_words(base + cache_vs_offset(D) + (r0 + 16 * (u + half) + i * 8 + g) * (D / 16), vsz[u][i]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int c = 0; c < 2; ++c) {
+            const int at = 2 * i + c;
+            float d = 0.0f, a = 0.0f;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int at = 2 * i + c;
-              float d = 0.0f, a = 0.0f;
-#pragma unroll
-              for (int j = 0; j < kGroups; ++j) {
-                const float one = FOLD == 2 && half ? dot[kRuns - 1][j][nt][at] : dot[u][j][nt][at];
-                float sc, ze;
-                unpack_sz(ksz[u][i][j], sc, ze);
-                d = j ? fmaf(sc, one, d) : sc * one;
-                if constexpr (FOLD == 2) a = j ? fmaf(ze, qsum[c][j], a) : ze * qsum[c][j];
-              }
-              if constexpr (FOLD == 1) a = zero[u][nt][at];
-              float v = fmaf(d, mul[nt][c], a);
-              if (kEdge && pos + r0 + 16 * (u + half) + 8 * i + g >= limit[nt][c]) v = -CUDART_INF_F;
-              xs[u][nt][at] = v;
+            for (int j = 0; j < kGroups; ++j) {
+              const float one = FOLD == 2 && half ? dot[kRuns - 1][j][at] : dot[u][j][at];
+              float sc, ze;
+              unpack_sz(ksz[u][i][j], sc, ze);
+              d = j ? fmaf(sc, one, d) : sc * one;
+              if constexpr (FOLD == 2) a = j ? fmaf(ze, qsum[c][j], a) : ze * qsum[c][j];
             }
+            if constexpr (FOLD == 1) a = zero[u][at];
+            float v = fmaf(d, mul[c], a);
+            if (kEdge && pos + r0 + 16 * (u + half) + 8 * i + g >= limit[c]) v = -CUDART_INF_F;
+            xs[u][at] = v;
+          }
         }
       // weights against the references as they stand, times the values' scales, in float16; what a row does not
       // see must not count, not even as 0 * NaN
-      float p[kSoft][NT][4], sum[NT][2];
-      uint32_t w16[kSoft][kGroups][NT][2], high = 0;
+      float p[kSoft][4], sum[2];
+      uint32_t w16[kSoft][kGroups][2], high = 0;
       auto weigh = [&]() {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) sum[nt][c] = l[nt][c];
+        for (int c = 0; c < 2; ++c) sum[c] = l[c];
 #pragma unroll
         for (int e = 0; e < kSoft; ++e)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int i = 0; i < 2; ++i) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int c = 0; c < 2; ++c) {
+              p[e][2 * i + c] = fast_exp2(xs[e][2 * i + c] - m[c]);
+              sum[c] += p[e][2 * i + c];
+            }
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) {
+              const float vs = __uint_as_float(vsz[e][i][j] << 16);
+              float w[2];
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                p[e][nt][2 * i + c] = fast_exp2(xs[e][nt][2 * i + c] - m[nt][c]);
-                sum[nt][c] += p[e][nt][2 * i + c];
+                w[c] = p[e][2 * i + c] * vs;
+                if (kEdge && pos + r0 + 16 * (e + half) + 8 * i + g >= limit[c]) w[c] = 0.0f;
               }
-#pragma unroll
-              for (int j = 0; j < kGroups; ++j) {
-                const float vs = __uint_as_float(vsz[e][i][j] << 16);
-                float w[2];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                  w[c] = p[e][nt][2 * i + c] * vs;
-                  if (kEdge && pos + r0 + 16 * (e + half) + 8 * i + g >= limit[nt][c]) w[c] = 0.0f;
-                }
-                w16[e][j][nt][i] = pack_f16(w[0], w[1]);
-                high = max_u16x2(high, w16[e][j][nt][i]);
-              }
+              w16[e][j][i] = pack_f16(w[0], w[1]);
+              high = max_u16x2(high, w16[e][j][i]);
             }
+          }
       };
       weigh();
-      float most = sum[0][0];
-#pragma unroll
-      for (int i = 1; i < 2 * NT; ++i) most = fmaxf(most, sum[i / 2][i % 2]);
+      const float most = fmaxf(sum[0], sum[1]);
       // Is a weight times scale at 2^15 or above (0x7800), or a sum of weights beyond 2^90 (scales near zero)?
       // Scales are not negative, so the codes of the float16 halves rank as they do.
       if (__any_sync(0xffffffffu, max_u16x2(high, 0x78007800u) != 0x78007800u || most > 0x1p90f)) {
         // raise the references so that the largest weight times scale is 2^12
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int c = 0; c < 2; ++c) {
+          float u = -CUDART_INF_F;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float u = -CUDART_INF_F;
+          for (int e = 0; e < kSoft; ++e)
 #pragma unroll
-            for (int e = 0; e < kSoft; ++e)
+            for (int i = 0; i < 2; ++i) {
+              float vmax = 0x1p-48f;
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                float vmax = 0x1p-48f;
+              for (int j = 0; j < kGroups; ++j) vmax = fmaxf(vmax, __uint_as_float(vsz[e][i][j] << 16));
+              u = fmaxf(u, xs[e][2 * i + c] + __log2f(vmax));
+            }
 #pragma unroll
-                for (int j = 0; j < kGroups; ++j) vmax = fmaxf(vmax, __uint_as_float(vsz[e][i][j] << 16));
-                u = fmaxf(u, xs[e][nt][2 * i + c] + __log2f(vmax));
-              }
+          for (int d = 4; d < 32; d *= 2) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, d));
+          const float now = fmaxf(m[c], u - 12.0f), f = fast_exp2(m[c] - now);
+          m[c] = now;
+          l[c] *= f;
 #pragma unroll
-            for (int d = 4; d < 32; d *= 2) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, d));
-            const float now = fmaxf(m[nt][c], u - 12.0f), f = fast_exp2(m[nt][c] - now);
-            m[nt][c] = now;
-            l[nt][c] *= f;
+          for (int j = 0; j < kGroups; ++j) z[c][j] *= f;
 #pragma unroll
-            for (int j = 0; j < kGroups; ++j) z[nt][c][j] *= f;
+          for (int w = 0; w < kWords; ++w)
 #pragma unroll
-            for (int w = 0; w < kWords; ++w)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) acc[w][k][nt][c] *= f, acc[w][k][nt][2 + c] *= f;
-          }
+            for (int k = 0; k < 2; ++k) acc[w][k][c] *= f, acc[w][k][2 + c] *= f;
+        }
         weigh();
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) l[nt][c] = sum[nt][c];
-      uint32_t pb[kSoft][kSplit][kGroups][NT][2];
+      for (int c = 0; c < 2; ++c) l[c] = sum[c];
+      uint32_t pb[kSoft][kSplit][kGroups][2];
 #pragma unroll
       for (int e = 0; e < kSoft; ++e)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int j = 0; j < kGroups; ++j) {
+            pb[e][0][j][i] = transpose8x8(w16[e][j][i]);
+            float vs, vz, w[2];
+            unpack_sz(vsz[e][i][j], vs, vz);
 #pragma unroll
-            for (int j = 0; j < kGroups; ++j) {
-              pb[e][0][j][nt][i] = transpose8x8(w16[e][j][nt][i]);
-              float vs, vz, w[2];
-              unpack_sz(vsz[e][i][j], vs, vz);
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const bool seen = !kEdge || pos + r0 + 16 * (e + half) + 8 * i + g < limit[nt][c];
-                w[c] = seen ? p[e][nt][2 * i + c] * vs : 0.0f;
-                if (seen) z[nt][c][j] = fmaf(p[e][nt][2 * i + c], vz, z[nt][c][j]);
-              }
-              if constexpr (kSplit == 2)
-                pb[e][1][j][nt][i] = transpose8x8(pack_f16_rest(w[0], w[1], w16[e][j][nt][i]));
+            for (int c = 0; c < 2; ++c) {
+              const bool seen = !kEdge || pos + r0 + 16 * (e + half) + 8 * i + g < limit[c];
+              w[c] = seen ? p[e][2 * i + c] * vs : 0.0f;
+              if (seen) z[c][j] = fmaf(p[e][2 * i + c], vz, z[c][j]);
             }
+            if constexpr (kSplit == 2)
+              pb[e][1][j][i] = transpose8x8(pack_f16_rest(w[0], w[1], w16[e][j][i]));
+          }
 #pragma unroll
       for (int e = 0; e < kRuns; ++e) {
         const int r = r0 + 16 * e;
         // folded: this run's weights are in columns 4 e .. 4 e + 3, the others' must not meet its values
         const uint32_t mine = FOLD == 1 || g / 4 == e ? 0xffffffffu : 0u;
-        uint32_t wb[kSplit][kGroups][NT][2];
+        uint32_t wb[kSplit][kGroups][2];
 #pragma unroll
-        for (int i = 0; i < 2 * kSplit * kGroups * NT; ++i)
-          (&wb[0][0][0][0])[i] = (&pb[FOLD == 2 ? 0 : e][0][0][0][0])[i] & mine;
+        for (int i = 0; i < 2 * kSplit * kGroups; ++i)
+          (&wb[0][0][0])[i] = (&pb[FOLD == 2 ? 0 : e][0][0][0])[i] & mine;
         uint32_t vw[2][kWords];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -583,10 +554,8 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT, FOLD>::kCtas))
             const uint32_t a1 = k ? __byte_perm(vw[0][w], 0, 0x4341) : vw[0][w] & 0x00ff00ffu, a0 = a1 & kLow;
             const uint32_t a3 = k ? __byte_perm(vw[1][w], 0, 0x4341) : vw[1][w] & 0x00ff00ffu, a2 = a3 & kLow;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int sp = 0; sp < kSplit; ++sp)
-                mma_f16(acc[w][k][nt], a0, a1, a2, a3, wb[sp][w / 2][nt][0], wb[sp][w / 2][nt][1]);
+            for (int sp = 0; sp < kSplit; ++sp)
+              mma_f16(acc[w][k], a0, a1, a2, a3, wb[sp][w / 2][0], wb[sp][w / 2][1]);
           }
       }
     };
@@ -626,36 +595,32 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, NT, FOLD>::kCtas))
     };
     const int fb = flushes++ & 1;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int c = 0; c < 2; ++c) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int d = 4; d < 32; d *= 2) {
+        l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
 #pragma unroll
-        for (int d = 4; d < 32; d *= 2) {
-          l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], d);
-#pragma unroll
-          for (int j = 0; j < kGroups; ++j) z[nt][c][j] += __shfl_xor_sync(0xffffffffu, z[nt][c][j], d);
-        }
-        if (g == 0) {
-          join_m[fb][warp][nt * 8 + 2 * t4 + c] = m[nt][c];
-          join_l[fb][warp][nt * 8 + 2 * t4 + c] = l[nt][c];
-        }
+        for (int j = 0; j < kGroups; ++j) z[c][j] += __shfl_xor_sync(0xffffffffu, z[c][j], d);
       }
+      if (g == 0) {
+        join_m[fb][warp][2 * t4 + c] = m[c];
+        join_l[fb][warp][2 * t4 + c] = l[c];
+      }
+    }
     __syncthreads();
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int c = 0; c < 2; ++c) {
+      const int col = 2 * t4 + c;
+      const float f = fast_exp2(m[c] - join_top(join_m[fb], col % kRows));
+      float* to = join + (warp * kCols + col) * Shape::kOStride + 4 * g;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int col = nt * 8 + 2 * t4 + c;
-        const float f = fast_exp2(m[nt][c] - join_top(join_m[fb], col % kRows));
-        float* to = join + (warp * kCols + col) * Shape::kOStride + 4 * g;
-#pragma unroll
-        for (int w = 0; w < kWords; ++w) {
-          const float zz = z[nt][c][w / 2] * f, f0 = f * 0x1p24f, f1 = f * 0x1p20f;
-          *reinterpret_cast<float4*>(to + w * 32) =
-              make_float4(fmaf(acc[w][0][nt][c], f0, zz), fmaf(acc[w][0][nt][2 + c] - acc[w][0][nt][c], f1, zz),
-                          fmaf(acc[w][1][nt][c], f0, zz), fmaf(acc[w][1][nt][2 + c] - acc[w][1][nt][c], f1, zz));
-        }
+      for (int w = 0; w < kWords; ++w) {
+        const float zz = z[c][w / 2] * f, f0 = f * 0x1p24f, f1 = f * 0x1p20f;
+        *reinterpret_cast<float4*>(to + w * 32) =
+            make_float4(fmaf(acc[w][0][c], f0, zz), fmaf(acc[w][0][2 + c] - acc[w][0][c], f1, zz),
+                        fmaf(acc[w][1][c], f0, zz), fmaf(acc[w][1][2 + c] - acc[w][1][c], f1, zz));
       }
+    }
     __syncthreads();
     const bool whole = first >= begin && first + n <= end;
     float* part = part_of<kRows, D>(ws, blockIdx.x, first < begin ? 0 : 1);

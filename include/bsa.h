@@ -425,7 +425,7 @@ bsa_status bsa_forward_noalloc(const void* q, const void* k, const void* v, void
  *     in byte r D / 2 + ((c % 32) / 8) (D / 8) + (c / 32) 4 + (c % 8) / 2, of
  *     its value in byte 32 D + (r / 2) D + (((c % 32) / 4) ^ (2 ((r / 2) % 4)))
  *     (D / 8) + (c / 32) 4 + (r % 2) 2 + (c % 4) / 2, the low four bits for
- *     even c. It stands for zero + scale * code.
+ *     even c. It stands for zero + scale * code; a scale is never negative.
  *   k_sum [num_pages, H_kv, D] float32: sum of each page's keys (as the cache
  *     holds them) over the tokens written.
  *   page_table [B, max_blocks] int32: page of each block of each sequence. An
