@@ -1302,7 +1302,7 @@ bsa_status launched(cudaError_t e, const char* what) {
 // Launches the attention (its shape is Shape) and the joining of the units that several CTAs share.
 template <typename E, int D, typename Shape>
 cudaError_t launch_cache_attn(void (*kern)(const E*, const uint8_t*, const int32_t*, E*, float*, bsa::CacheSeqs, int, int,
-                                           int, int, float),
+                                           int, int, float, int4*),
                               const void* q, const void* cache, const int32_t* idx, void* o, void* ws,
                               const bsa::CacheSeqs& seqs, int B, int H, int Hkv, int topk, float scale_log2,
                               void* stream) {
@@ -1313,26 +1313,24 @@ cudaError_t launch_cache_attn(void (*kern)(const E*, const uint8_t*, const int32
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(Shape::smem(bsa::kCaMaxSeqs)));
     if (e != cudaSuccess) return e;
-    const cudaError_t j = cudaFuncSetAttribute(bsa::cache_attn_join_kernel<E, D, Shape::kRows>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(bsa::kCaMaxSeqs * sizeof(int4)));
-    if (j != cudaSuccess) return j;
     if (dev < 64) attr_set[dev] = true;
   }
   // with a long table of sequences fewer CTAs fit an SM's 228 KB (each takes 1 KB more, and static memory)
   const size_t smem = Shape::smem(B);
   const unsigned per_sm = std::min<unsigned>(Shape::kCtas, 228 * 1024 / (smem + 3072));
   const unsigned ctas = per_sm * sm_count();
+  int4* plan = static_cast<int4*>(ws);  // the plan, then the parts
+  float* parts = reinterpret_cast<float*>(plan + 1 + B);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
       launch_pdl(kern, ctas, bsa::kCaThreads, smem, st, static_cast<const E*>(q), static_cast<const uint8_t*>(cache), idx,
-                 static_cast<E*>(o), static_cast<float*>(ws), seqs, B, H, Hkv, topk, scale_log2);
+                 static_cast<E*>(o), parts, seqs, B, H, Hkv, topk, scale_log2, plan);
   if (e != cudaSuccess) return e;
   // A plain launch: as a programmatic one its waiting CTAs and the next call's early ones share the SMs so that
   // some of the latter start late (a run of dense calls: 85 against 69 us each).
-  bsa::cache_attn_join_kernel<E, D, Shape::kRows><<<static_cast<unsigned>(B) * seqs.T * H, bsa::kCaJoinWarps * 32,
-                                                    B * sizeof(int4), st>>>(
-      static_cast<E*>(o), static_cast<const float*>(ws), seqs, B, H, Hkv, idx ? topk : 0, static_cast<int>(ctas));
+  bsa::cache_attn_join_kernel<E, D, Shape::kRows>
+      <<<static_cast<unsigned>(B) * seqs.T * H, bsa::kCaJoinWarps * 32, 0, st>>>(static_cast<E*>(o), parts, plan, seqs.T,
+                                                                                 H, Hkv);
   return cudaGetLastError();
 }
 
@@ -1464,10 +1462,10 @@ bsa_status bsa_cache_block_topk(const void* q, const float* k_sum, const int32_t
 
 size_t bsa_cache_attn_workspace_bytes(int B, int T, int H, int H_kv, int D) {
   if (check_cache_dims(B, T, H, H_kv, D, 64) != BSA_OK) return 0;
-  // two parts of a unit's query rows for each CTA; float32 and bfloat16 queries alike
+  // the plan; two parts of a unit's query rows for each CTA, float32 and bfloat16 queries alike
   const long rows = std::max({8 * bsa::CaShape<128, 1>::kCtas, 32 * bsa::CaWide<128, 4>::kCtas,
                               40 * bsa::CaWide<128, 5>::kCtas});
-  return static_cast<size_t>(sm_count()) * rows * 2 * (D + 2) * sizeof(float);
+  return (static_cast<size_t>(B) + 1) * sizeof(int4) + static_cast<size_t>(sm_count()) * rows * 2 * (D + 2) * sizeof(float);
 }
 
 bsa_status bsa_cache_attn(const void* q, const void* cache, const int32_t* page_table, const int32_t* start,

@@ -148,9 +148,10 @@ struct CaPlan {
   __device__ __forceinline__ int row0(int unit, int rows) const { return row_tiles == 1 ? 0 : unit % row_tiles * rows; }
 };
 
-// Fills the plan; `table` is shared memory for B int4. All threads of the block call it; it ends with a barrier.
+// Fills the plan; `table` is shared memory for B int4. All threads of the block call it; it ends with a barrier. The
+// first CTA leaves the chunk and the table in `out` for the joining launch.
 __device__ __forceinline__ CaPlan make_plan(const CacheSeqs& s, int B, int Hkv, int row_tiles, int topk, int ctas,
-                                            int4* table) {
+                                            int4* table, int4* out) {
   __shared__ int total;
   CaPlan p;
   p.seqs = table, p.row_tiles = row_tiles, p.per_seq = Hkv * row_tiles, p.B = B;
@@ -180,6 +181,10 @@ __device__ __forceinline__ CaPlan make_plan(const CacheSeqs& s, int B, int Hkv, 
   __syncthreads();
   p.total = total;
   p.chunk = max(1, (p.total + ctas - 1) / ctas);
+  if (blockIdx.x == 0) {
+    for (int b = threadIdx.x; b < B; b += blockDim.x) out[1 + b] = table[b];
+    if (threadIdx.x == 0) out[0] = make_int4(p.chunk, 0, 0, 0);
+  }
   return p;
 }
 
@@ -217,7 +222,7 @@ __device__ __forceinline__ void store_out(T* o, float x) {
 template <typename T, int D, int FOLD>
 __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
     cache_attn_kernel(const T* __restrict__ q, const uint8_t* __restrict__ cache, const int32_t* __restrict__ idx, T* o,
-                      float* ws, CacheSeqs s, int B, int H, int Hkv, int topk, float scale_log2) {
+                      float* ws, CacheSeqs s, int B, int H, int Hkv, int topk, float scale_log2, int4* plan_out) {
   using Shape = CaShape<D, FOLD>;
   constexpr int kStages = Shape::kStages, kRows = Shape::kRows, kCols = Shape::kCols, kTile = cache_tile_bytes(D);
   constexpr int kWords = D / 32, kGroups = D / 64;
@@ -248,7 +253,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
     fence_mbarrier_init();
   }
   pdl_wait();
-  const CaPlan plan = make_plan(s, B, Hkv, (s.T * G + kRows - 1) / kRows, idx ? topk : 0, gridDim.x, table);
+  const CaPlan plan = make_plan(s, B, Hkv, (s.T * G + kRows - 1) / kRows, idx ? topk : 0, gridDim.x, table, plan_out);
   const int begin = min(static_cast<long>(blockIdx.x) * plan.chunk, static_cast<long>(plan.total));
   const int end = min(begin + plan.chunk, plan.total);
   volatile int* abort = &abort_flag;
@@ -702,7 +707,7 @@ template <int D, int NT>
 __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
     cache_attn_wide_kernel(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict__ cache,
                            const int32_t* __restrict__ idx, __nv_bfloat16* o, float* ws, CacheSeqs s, int B, int H,
-                           int Hkv, int topk, float scale_log2) {
+                           int Hkv, int topk, float scale_log2, int4* plan_out) {
   using W = CaWide<D, NT>;
   constexpr int kStages = W::kStages, kRows = W::kRows, kTile = cache_tile_bytes(D), kGroups = W::kGroups;
   constexpr int kWords = D / 32, kMt = D / 64;  // 32-channel words; 16-channel products of a warp
@@ -726,7 +731,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
     fence_mbarrier_init();
   }
   pdl_wait();
-  const CaPlan plan = make_plan(s, B, Hkv, (s.T * G + kRows - 1) / kRows, idx ? topk : 0, gridDim.x, table);
+  const CaPlan plan = make_plan(s, B, Hkv, (s.T * G + kRows - 1) / kRows, idx ? topk : 0, gridDim.x, table, plan_out);
   const int begin = min(static_cast<long>(blockIdx.x) * plan.chunk, static_cast<long>(plan.total));
   const int end = min(begin + plan.chunk, plan.total);
   volatile int* abort = &abort_flag;
@@ -1115,20 +1120,17 @@ constexpr int kCaJoinWarps = 8;
 
 template <typename T, int D, int kRows>
 __global__ void __launch_bounds__(kCaJoinWarps * 32)
-    cache_attn_join_kernel(T* o, const float* ws, CacheSeqs s, int B, int H, int Hkv, int topk, int ctas) {
+    cache_attn_join_kernel(T* o, const float* ws, const int4* plan, int tokens, int H, int Hkv) {
   constexpr int kPer = D / 32;  // channels of a lane
-  extern __shared__ int4 table[];
   __shared__ float sums[kCaJoinWarps][D], weights[kCaJoinWarps], tops[kCaJoinWarps];
-  pdl_launch_dependents();
-  pdl_wait();
   const int G = H / Hkv, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int row_tiles = (s.T * G + kRows - 1) / kRows;
-  const CaPlan plan = make_plan(s, B, Hkv, row_tiles, topk, ctas, table);
-  const int row = blockIdx.x % (s.T * G), h = blockIdx.x / (s.T * G) % Hkv, b = blockIdx.x / (s.T * G) / Hkv;
-  const int4 seq = table[b];
+  const int row_tiles = (tokens * G + kRows - 1) / kRows;
+  const int row = blockIdx.x % (tokens * G), h = blockIdx.x / (tokens * G) % Hkv, b = blockIdx.x / (tokens * G) / Hkv;
+  const int chunk = plan[0].x;
+  const int4 seq = plan[1 + b];
   if (row / G >= seq.w) return;
   const int r = row % kRows, first = seq.x + (h * row_tiles + row / kRows) * seq.y;
-  const int c0 = first / plan.chunk, c1 = (first + seq.y - 1) / plan.chunk;
+  const int c0 = first / chunk, c1 = (first + seq.y - 1) / chunk;
   if (c0 == c1) return;
   // four parts at a time in flight, each against the largest reference so far
   constexpr int kAhead = 4;
@@ -1172,7 +1174,7 @@ __global__ void __launch_bounds__(kCaJoinWarps * 32)
       const float e = fast_exp2(tops[i] - most);
       v = fmaf(sums[i][threadIdx.x], e, v), w = fmaf(weights[i], e, w);
     }
-    store_out(o + ((static_cast<long>(b) * s.T + row / G) * H + h * G + row % G) * D + threadIdx.x,
+    store_out(o + ((static_cast<long>(b) * tokens + row / G) * H + h * G + row % G) * D + threadIdx.x,
               w == 0.0f ? 0.0f : v / w);
   }
 }
