@@ -19,6 +19,9 @@
 //     matrix instructions made the kernel slower: 110 against 89 us at two CTAs an SM.)
 //   values: float16 subnormals, of the byte lo + 16 hi and of lo alone; hi is the
 //     difference of the two sums.
+// float32 queries take the operands code - 8 instead (with zero + 8 scale): sums
+// of both signs stay near the result's own size, and the matrix unit's truncating
+// sums cost them nothing (with code, 1e-4 of the result at 6000 tokens).
 // All of these operands are exact. For float16's range each query row is
 // scaled by a power of two, and the reference M of a row keeps 2^(x - M) v_scale
 // below 2^15.
@@ -94,6 +97,13 @@ __device__ __forceinline__ void load_words(uint32_t p, uint32_t (&w)[N]) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(p));
   else
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(p));
+}
+
+// Two codes in the low bits of 16-bit halves as the float16 numbers code - 8.
+__device__ __forceinline__ uint32_t centred(uint32_t codes) {
+  const uint32_t x = codes | 0x64006400u;  // 1024 + code
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__float2half_rn(1032.0f)));
+  return *reinterpret_cast<const uint32_t*>(&d);
 }
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
@@ -230,6 +240,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
   // runs of 16 tokens computed together; folded, two runs share the columns and everything between the products is
   // computed once for both, each thread looking after the tokens of its half
   constexpr int kRuns = kSplit == 1 || FOLD == 2 ? 2 : 1, kSoft = kRuns / FOLD;
+  constexpr bool kCentre = kSplit == 2;           // operands code - 8 instead of code
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
   extern __shared__ __align__(128) uint8_t smem[];
   float* join = reinterpret_cast<float*>(smem + 2 * kStages * kTile);
@@ -332,11 +343,11 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
     // (odd channels 2^-23) of it
     const int up = min(13 - static_cast<int>((__float_as_uint(amax) >> 23) & 255u) + 127, 126);
     const float qscale = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
-    const float back = __uint_as_float(static_cast<uint32_t>(24 - up + 127) << 23) * scale_log2;
+    const float back = __uint_as_float(static_cast<uint32_t>((kCentre ? 0 : 24) - up + 127) << 23) * scale_log2;
 #pragma unroll
     for (int w = 0; w < kWords; ++w) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[w][i] *= i % 2 ? qscale * 0.0625f : qscale;
+      for (int i = 0; i < 8; ++i) f[w][i] *= i % 2 && !kCentre ? qscale * 0.0625f : qscale;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         qb[0][w][k][0] = pack_f16(f[w][2 * k], f[w][2 * k + 4]);
@@ -355,7 +366,8 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const __nv_bfloat16 h = __float2bfloat16_rn(rest);
-        parts[i] = static_cast<uint32_t>(__bfloat16_as_ushort(h)) << 16;  // the zero half
+        parts[i] = static_cast<uint32_t>(__bfloat16_as_ushort(h)) << 16;  // the zero half, and 8 of it for the scale
+        if constexpr (kCentre) parts[i] |= __bfloat16_as_ushort(__float2bfloat16_rn(8.0f * __bfloat162float(h)));
         rest -= __bfloat162float(h);
       }
       if (kGroups == 2) {
@@ -422,7 +434,8 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const uint32_t u = kw[0][w] >> (8 * k), v = kw[1][w] >> (8 * k);
-            const uint32_t a0 = u & kLow, a1 = v & kLow, a2 = u & kHigh, a3 = v & kHigh;
+            uint32_t a0 = u & kLow, a1 = v & kLow, a2 = u & kHigh, a3 = v & kHigh;
+            if constexpr (kCentre) a0 = centred(a0), a1 = centred(a1), a2 = centred(a2 >> 4), a3 = centred(a3 >> 4);
 #pragma unroll
             for (int sp = 0; sp < kSplit; ++sp)
               if (w % 2 == 0 && k == 0 && sp == 0)
@@ -446,6 +459,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
               const float one = FOLD == 2 && half ? dot[kRuns - 1][j][at] : dot[u][j][at];
               float sc, ze;
               unpack_sz(ksz[u][i][j], sc, ze);
+              if constexpr (kCentre) ze = fmaf(8.0f, sc, ze);
               d = j ? fmaf(sc, one, d) : sc * one;
               if constexpr (FOLD == 2) a = j ? fmaf(ze, qsum[c][j], a) : ze * qsum[c][j];
             }
@@ -529,6 +543,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
             pb[e][0][j][i] = transpose8x8(w16[e][j][i]);
             float vs, vz, w[2];
             unpack_sz(vsz[e][i][j], vs, vz);
+            if constexpr (kCentre) vz = fmaf(8.0f, vs, vz);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const bool seen = !kEdge || pos + r0 + 16 * (e + half) + 8 * i + g < limit[c];
@@ -538,31 +553,48 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
             if constexpr (kSplit == 2)
               pb[e][1][j][i] = transpose8x8(pack_f16_rest(w[0], w[1], w16[e][j][i]));
           }
+      uint32_t wb[kRuns][kSplit][kGroups][2], vw[kRuns][2][kWords];
 #pragma unroll
       for (int e = 0; e < kRuns; ++e) {
-        const int r = r0 + 16 * e;
         // folded: this run's weights are in columns 4 e .. 4 e + 3, the others' must not meet its values
         const uint32_t mine = FOLD == 1 || g / 4 == e ? 0xffffffffu : 0u;
-        uint32_t wb[kSplit][kGroups][2];
 #pragma unroll
         for (int i = 0; i < 2 * kSplit * kGroups; ++i)
-          (&wb[0][0][0])[i] = (&pb[FOLD == 2 ? 0 : e][0][0][0])[i] & mine;
-        uint32_t vw[2][kWords];
+          (&wb[e][0][0][0])[i] = (&pb[FOLD == 2 ? 0 : e][0][0][0])[i] & mine;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          load_words(base + cache_v_offset(D) + (r / 2 + t4 + 4 * i) * D + (g ^ (2 * t4)) * (D / 8), vw[i]);
+          load_words(base + cache_v_offset(D) + ((r0 + 16 * e) / 2 + t4 + 4 * i) * D + (g ^ (2 * t4)) * (D / 8), vw[e][i]);
+      }
+      // These products start from zero and are added in float32: a sum kept in the matrix unit over a long sequence
+      // loses up to half a unit of its last place at every step, always downwards.
 #pragma unroll
-        for (int w = 0; w < kWords; ++w)
+      for (int w = 0; w < kWords; ++w)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            // the byte with channels 2 k and 2 k + 1, and the first one alone
-            const uint32_t a1 = k ? __byte_perm(vw[0][w], 0, 0x4341) : vw[0][w] & 0x00ff00ffu, a0 = a1 & kLow;
-            const uint32_t a3 = k ? __byte_perm(vw[1][w], 0, 0x4341) : vw[1][w] & 0x00ff00ffu, a2 = a3 & kLow;
+        for (int k = 0; k < 2; ++k) {
+          float part[4];
+#pragma unroll
+          for (int e = 0; e < kRuns; ++e) {
+            uint32_t a0, a1, a2, a3;
+            if constexpr (kCentre) {
+              const uint32_t u = vw[e][0][w] >> (8 * k), v = vw[e][1][w] >> (8 * k);
+              a0 = centred(u & kLow), a1 = centred(u >> 4 & kLow), a2 = centred(v & kLow), a3 = centred(v >> 4 & kLow);
+            } else {
+              // the byte with channels 2 k and 2 k + 1, and the first one alone
+              a1 = k ? __byte_perm(vw[e][0][w], 0, 0x4341) : vw[e][0][w] & 0x00ff00ffu, a0 = a1 & kLow;
+              a3 = k ? __byte_perm(vw[e][1][w], 0, 0x4341) : vw[e][1][w] & 0x00ff00ffu, a2 = a3 & kLow;
+            }
 #pragma unroll
             for (int sp = 0; sp < kSplit; ++sp)
-              mma_f16(acc[w][k], a0, a1, a2, a3, wb[sp][w / 2][0], wb[sp][w / 2][1]);
+              if (e == 0 && sp == 0)
+                mma_f16_first(part, a0, a1, a2, a3, wb[e][sp][w / 2][0], wb[e][sp][w / 2][1]);
+              else
+                mma_f16(part, a0, a1, a2, a3, wb[e][sp][w / 2][0], wb[e][sp][w / 2][1]);
           }
-      }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            f2_split(f2_add(f2(acc[w][k][2 * i], acc[w][k][2 * i + 1]), f2(part[2 * i], part[2 * i + 1])),
+                     acc[w][k][2 * i], acc[w][k][2 * i + 1]);
+        }
     };
 
     // a tile goes to one pair of warps, 32 tokens each; the pairs take the CTA's tiles in turn
@@ -620,10 +652,11 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
       float* to = join + (warp * kCols + col) * Shape::kOStride + 4 * g;
 #pragma unroll
       for (int w = 0; w < kWords; ++w) {
-        const float zz = z[c][w / 2] * f, f0 = f * 0x1p24f, f1 = f * 0x1p20f;
-        *reinterpret_cast<float4*>(to + w * 32) =
-            make_float4(fmaf(acc[w][0][c], f0, zz), fmaf(acc[w][0][2 + c] - acc[w][0][c], f1, zz),
-                        fmaf(acc[w][1][c], f0, zz), fmaf(acc[w][1][2 + c] - acc[w][1][c], f1, zz));
+        const float zz = z[c][w / 2] * f, f0 = kCentre ? f : f * 0x1p24f, f1 = kCentre ? f : f * 0x1p20f;
+        float hi[2] = {acc[w][0][2 + c], acc[w][1][2 + c]};
+        if constexpr (!kCentre) hi[0] -= acc[w][0][c], hi[1] -= acc[w][1][c];
+        *reinterpret_cast<float4*>(to + w * 32) = make_float4(fmaf(acc[w][0][c], f0, zz), fmaf(hi[0], f1, zz),
+                                                              fmaf(acc[w][1][c], f0, zz), fmaf(hi[1], f1, zz));
       }
     }
     __syncthreads();
@@ -1036,26 +1069,38 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
         else
           add_up(std::false_type{});
         const int word = D == 128 ? warp : warp / 2, j = word / 2;
+        uint32_t vw[4][2][1];
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-          uint32_t vw[2][1];
+        for (int kt = 0; kt < 4; ++kt)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            get_words(base + cache_v_offset(D) + (kt * 8 + t4 + 4 * i) * D + (g ^ (2 * t4)) * (D / 8) + word * 4, vw[i]);
-          uint32_t av[kMt][4];
+            get_words(base + cache_v_offset(D) + (kt * 8 + t4 + 4 * i) * D + (g ^ (2 * t4)) * (D / 8) + word * 4,
+                      vw[kt][i]);
+        // a tile's products start from zero and are added in float32 (see the other kernel)
 #pragma unroll
-          for (int k = 0; k < kMt; ++k) {
-            const uint32_t pick = D == 128 ? (k ? 0x4341u : 0x4240u) : (warp % 2 ? 0x4341u : 0x4240u);
-            av[k][1] = __byte_perm(vw[0][0], 0, pick), av[k][0] = av[k][1] & kLow;
-            av[k][3] = __byte_perm(vw[1][0], 0, pick), av[k][2] = av[k][3] & kLow;
+        for (int k = 0; k < kMt; ++k) {
+          const uint32_t pick = D == 128 ? (k ? 0x4341u : 0x4240u) : (warp % 2 ? 0x4341u : 0x4240u);
+          float sum[NT][4];
+#pragma unroll
+          for (int kt = 0; kt < 4; ++kt) {
+            const uint32_t a1 = __byte_perm(vw[kt][0][0], 0, pick), a0 = a1 & kLow;
+            const uint32_t a3 = __byte_perm(vw[kt][1][0], 0, pick), a2 = a3 & kLow;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint2 bp =
+                  reinterpret_cast<const uint2*>(sp)[(((buf * kGroups + j) * 4 + kt) * NT + nt) * 32 + lane];
+              if (kt == 0)
+                mma_f16_first(sum[nt], a0, a1, a2, a3, bp.x, bp.y);
+              else
+                mma_f16(sum[nt], a0, a1, a2, a3, bp.x, bp.y);
+            }
           }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint2 bp = reinterpret_cast<const uint2*>(sp)[(((buf * kGroups + j) * 4 + kt) * NT + nt) * 32 + lane];
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < kMt; ++k)
-              mma_f16(acc[k][nt], av[k][0], av[k][1], av[k][2], av[k][3], bp.x, bp.y);
-          }
+            for (int i = 0; i < 2; ++i)
+              f2_split(f2_add(f2(acc[k][nt][2 * i], acc[k][nt][2 * i + 1]), f2(sum[nt][2 * i], sum[nt][2 * i + 1])),
+                       acc[k][nt][2 * i], acc[k][nt][2 * i + 1]);
         }
       }
       buf ^= 1;
