@@ -553,71 +553,106 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
             if constexpr (kSplit == 2)
               pb[e][1][j][i] = transpose8x8(pack_f16_rest(w[0], w[1], w16[e][j][i]));
           }
-      uint32_t wb[kRuns][kSplit][kGroups][2], vw[kRuns][2][kWords];
 #pragma unroll
       for (int e = 0; e < kRuns; ++e) {
         // folded: this run's weights are in columns 4 e .. 4 e + 3, the others' must not meet its values
         const uint32_t mine = FOLD == 1 || g / 4 == e ? 0xffffffffu : 0u;
+        uint32_t wb[kSplit][kGroups][2], vw[2][kWords];
 #pragma unroll
         for (int i = 0; i < 2 * kSplit * kGroups; ++i)
-          (&wb[e][0][0][0])[i] = (&pb[FOLD == 2 ? 0 : e][0][0][0])[i] & mine;
+          (&wb[0][0][0])[i] = (&pb[FOLD == 2 ? 0 : e][0][0][0])[i] & mine;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          load_words(base + cache_v_offset(D) + ((r0 + 16 * e) / 2 + t4 + 4 * i) * D + (g ^ (2 * t4)) * (D / 8), vw[e][i]);
-      }
-      // These products start from zero and are added in float32: a sum kept in the matrix unit over a long sequence
-      // loses up to half a unit of its last place at every step, always downwards.
+          load_words(base + cache_v_offset(D) + ((r0 + 16 * e) / 2 + t4 + 4 * i) * D + (g ^ (2 * t4)) * (D / 8), vw[i]);
 #pragma unroll
-      for (int w = 0; w < kWords; ++w)
+        for (int w = 0; w < kWords; ++w)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float part[4];
-#pragma unroll
-          for (int e = 0; e < kRuns; ++e) {
-            uint32_t a0, a1, a2, a3;
+          for (int k = 0; k < 2; ++k) {
             if constexpr (kCentre) {
-              const uint32_t u = vw[e][0][w] >> (8 * k), v = vw[e][1][w] >> (8 * k);
-              a0 = centred(u & kLow), a1 = centred(u >> 4 & kLow), a2 = centred(v & kLow), a3 = centred(v >> 4 & kLow);
+              // float32: from zero, and added in float32 (see put_aside)
+              const uint32_t u = vw[0][w] >> (8 * k), v = vw[1][w] >> (8 * k);
+              const uint32_t a0 = centred(u & kLow), a1 = centred(u >> 4 & kLow), a2 = centred(v & kLow),
+                             a3 = centred(v >> 4 & kLow);
+              float part[4];
+              mma_f16_first(part, a0, a1, a2, a3, wb[0][w / 2][0], wb[0][w / 2][1]);
+              mma_f16(part, a0, a1, a2, a3, wb[kSplit - 1][w / 2][0], wb[kSplit - 1][w / 2][1]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[w][k][i] += part[i];
             } else {
               // the byte with channels 2 k and 2 k + 1, and the first one alone
-              a1 = k ? __byte_perm(vw[e][0][w], 0, 0x4341) : vw[e][0][w] & 0x00ff00ffu, a0 = a1 & kLow;
-              a3 = k ? __byte_perm(vw[e][1][w], 0, 0x4341) : vw[e][1][w] & 0x00ff00ffu, a2 = a3 & kLow;
+              const uint32_t a1 = k ? __byte_perm(vw[0][w], 0, 0x4341) : vw[0][w] & 0x00ff00ffu, a0 = a1 & kLow;
+              const uint32_t a3 = k ? __byte_perm(vw[1][w], 0, 0x4341) : vw[1][w] & 0x00ff00ffu, a2 = a3 & kLow;
+              mma_f16(acc[w][k], a0, a1, a2, a3, wb[0][w / 2][0], wb[0][w / 2][1]);
             }
-#pragma unroll
-            for (int sp = 0; sp < kSplit; ++sp)
-              if (e == 0 && sp == 0)
-                mma_f16_first(part, a0, a1, a2, a3, wb[e][sp][w / 2][0], wb[e][sp][w / 2][1]);
-              else
-                mma_f16(part, a0, a1, a2, a3, wb[e][sp][w / 2][0], wb[e][sp][w / 2][1]);
           }
+      }
+    };
+
+    // Sums kept in the matrix unit lose up to half a unit of their last place at every step, always downwards (1e-4 of
+    // the result after 6000 tokens, where values of both signs nearly cancel). So every kAside tiles they go to this
+    // thread's places of the join buffer, in float32, at the references of that time.
+    constexpr int kAside = 64;
+    float aside_m[2];
+    bool aside = false;
+    auto sums_of = [&](int c, int w, float f, float zero) {
+      const float f0 = kCentre ? f : f * 0x1p24f, f1 = kCentre ? f : f * 0x1p20f;
+      float hi[2] = {acc[w][0][2 + c], acc[w][1][2 + c]};
+      if constexpr (!kCentre) hi[0] -= acc[w][0][c], hi[1] -= acc[w][1][c];
+      return make_float4(fmaf(acc[w][0][c], f0, zero), fmaf(hi[0], f1, zero), fmaf(acc[w][1][c], f0, zero),
+                         fmaf(hi[1], f1, zero));
+    };
+    // the sums so far at reference m + log2(1 / f), with `zero` for each channel
+    auto put_aside = [&](int c, float f, float old, const float (&zero)[kGroups]) {
+      float4* to = reinterpret_cast<float4*>(join + (warp * kCols + 2 * t4 + c) * Shape::kOStride + 4 * g);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            f2_split(f2_add(f2(acc[w][k][2 * i], acc[w][k][2 * i + 1]), f2(part[2 * i], part[2 * i + 1])),
-                     acc[w][k][2 * i], acc[w][k][2 * i + 1]);
+      for (int w = 0; w < kWords; ++w) {
+        float4 v = sums_of(c, w, f, zero[w / 2]);
+        if (aside) {
+          const float4 u = to[w * 8];
+          v = make_float4(fmaf(u.x, old, v.x), fmaf(u.y, old, v.y), fmaf(u.z, old, v.z), fmaf(u.w, old, v.w));
         }
+        to[w * 8] = v;
+      }
     };
 
     // a tile goes to one pair of warps, 32 tokens each; the pairs take the CTA's tiles in turn
-    for (; mine < stop; mine += 2) {
-      const int pos = mbar_wait(&full[stage], phase, abort, 802) ? tile_pos[pair][stage] : -1;
-      if (pos >= 0) {
-        const uint32_t base = smem_u32(stages) + stage * kTile;
-        const bool edge = pos + kCacheTile > low_limit;
-        for (int run = 0; run < 2; run += kRuns) {
-          const int r0 = (warp % 2) * 32 + run * 16;
-          if (edge)
-            tokens(base, pos, r0, std::true_type{});
-          else
-            tokens(base, pos, r0, std::false_type{});
+    while (mine < stop) {
+      const int until = kCentre ? stop : min(stop, mine + 2 * kAside);
+      for (; mine < until; mine += 2) {
+        const int pos = mbar_wait(&full[stage], phase, abort, 802) ? tile_pos[pair][stage] : -1;
+        if (pos >= 0) {
+          const uint32_t base = smem_u32(stages) + stage * kTile;
+          const bool edge = pos + kCacheTile > low_limit;
+          for (int run = 0; run < 2; run += kRuns) {
+            const int r0 = (warp % 2) * 32 + run * 16;
+            if (edge)
+              tokens(base, pos, r0, std::true_type{});
+            else
+              tokens(base, pos, r0, std::false_type{});
+          }
         }
+        __syncwarp();
+        if (!leader) {
+          if (lane == 0) mbar_arrive(&empty[stage]);
+        } else if (load < end && mbar_wait(&empty[stage], phase, abort, 801)) {
+          fetch();
+        }
+        if (++stage == kStages) stage = 0, phase ^= 1;
       }
-      __syncwarp();
-      if (!leader) {
-        if (lane == 0) mbar_arrive(&empty[stage]);
-      } else if (load < end && mbar_wait(&empty[stage], phase, abort, 801)) {
-        fetch();
+      if (mine >= stop) break;
+      constexpr float kNone[kGroups] = {};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        put_aside(c, 1.0f, aside ? fast_exp2(aside_m[c] - m[c]) : 0.0f, kNone);
+        aside_m[c] = m[c];
       }
-      if (++stage == kStages) stage = 0, phase ^= 1;
+      aside = true;
+#pragma unroll
+      for (int w = 0; w < kWords; ++w)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[w][k][i] = 0.0f;
     }
     x = stop;
 
@@ -647,17 +682,11 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
     __syncthreads();
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const int col = 2 * t4 + c;
-      const float f = fast_exp2(m[c] - join_top(join_m[fb], col % kRows));
-      float* to = join + (warp * kCols + col) * Shape::kOStride + 4 * g;
+      const float top = join_top(join_m[fb], (2 * t4 + c) % kRows), f = fast_exp2(m[c] - top);
+      float zero[kGroups];
 #pragma unroll
-      for (int w = 0; w < kWords; ++w) {
-        const float zz = z[c][w / 2] * f, f0 = kCentre ? f : f * 0x1p24f, f1 = kCentre ? f : f * 0x1p20f;
-        float hi[2] = {acc[w][0][2 + c], acc[w][1][2 + c]};
-        if constexpr (!kCentre) hi[0] -= acc[w][0][c], hi[1] -= acc[w][1][c];
-        *reinterpret_cast<float4*>(to + w * 32) = make_float4(fmaf(acc[w][0][c], f0, zz), fmaf(hi[0], f1, zz),
-                                                              fmaf(acc[w][1][c], f0, zz), fmaf(hi[1], f1, zz));
-      }
+      for (int j = 0; j < kGroups; ++j) zero[j] = z[c][j] * f;
+      put_aside(c, f, aside ? fast_exp2(aside_m[c] - top) : 0.0f, zero);
     }
     __syncthreads();
     const bool whole = first >= begin && first + n <= end;
@@ -682,6 +711,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
         part[2 * kRows + r * D + c] = val;
       }
     }
+    __syncthreads();  // the join buffer is free for the next unit's sums
   }
   // after a wait that ran out: copies in flight end before the block's shared memory does
   if (*abort && leader && lane == 0)
