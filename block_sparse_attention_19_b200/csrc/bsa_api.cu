@@ -1327,7 +1327,7 @@ cudaError_t launch_cache_attn(void (*kern)(const E*, const uint8_t*, const int32
                  static_cast<E*>(o), parts, seqs, B, H, Hkv, topk, scale_log2, plan);
   if (e != cudaSuccess) return e;
   // A plain launch: as a programmatic one its waiting CTAs and the next call's early ones share the SMs so that
-  // some of the latter start late (a run of dense calls: 85 against 69 us each).
+  // some of the latter start late (a run of dense calls: 79 against 59 us each).
   bsa::cache_attn_join_kernel<E, D, Shape::kRows>
       <<<static_cast<unsigned>(B) * seqs.T * H, bsa::kCaJoinWarps * 32, 0, st>>>(static_cast<E*>(o), parts, plan, seqs.T,
                                                                                  H, Hkv);
@@ -1494,9 +1494,9 @@ bsa_status bsa_cache_attn(const void* q, const void* cache, const int32_t* page_
     };
     // Query rows of a (sequence, key/value head): up to four are folded (everything between the products once for two
     // runs of tokens: dense 32768-token batch, four rows, 65 us against 69), up to eight fill the products' columns
-    // once. More go to the kernel whose warps share a tile, in units of equal size of up to 40 (40 rows, five new
-    // tokens of 8 heads: XX us, 41 in units of 16 rows of the other kernel). float32 queries, whose operands come in
-    // two parts, stay with the first.
+    // once. More go to the kernel whose warps share a tile, in units of equal size of up to 40 (40 rows, eight padded
+    // sequences of up to 16384 tokens: 36 us, 41 in units of 16 rows of the other kernel). float32 queries, whose
+    // operands come in two parts, stay with the first.
     const long long rows = static_cast<long long>(T) * (H / H_kv);
     if constexpr (sizeof(E) == 2) {
       if (rows > 8) {
