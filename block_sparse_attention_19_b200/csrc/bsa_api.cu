@@ -1294,6 +1294,28 @@ bsa_status check_attn_tiles(int B, int T, int H, int Hkv, int block_size, int ma
   return BSA_OK;
 }
 
+// Can the device hold a cluster of 16 CTAs of this kernel with 64 KB of shared memory each? Asked once for a device
+// and element type (the two head sizes' kernels need the same).
+template <typename K>
+bool cache_topk_takes_16(K kern, int dev) {
+  static int known[64] = {0};  // 1: yes, 2: no
+  if (dev < 64 && known[dev]) return known[dev] == 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(16);
+  cfg.blockDim = dim3(bsa::kCacheSelThreads);
+  cfg.dynamicSmemBytes = 65536;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 16, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  const bool yes = cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0;
+  if (!yes) cudaGetLastError();
+  if (dev < 64) known[dev] = yes ? 1 : 2;
+  return yes;
+}
+
 bsa_status launched(cudaError_t e, const char* what) {
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? BSA_OK : cuda_fail(e, what);
@@ -1389,6 +1411,7 @@ bsa_status bsa_cache_read(const void* cache, const int32_t* page_table, const in
   bsa_status s;
   if ((s = check_cache(B, T, H_kv, H_kv, D, block_size, num_pages, max_blocks, dt)) != BSA_OK) return s;
   if ((s = check_tensors({cache, k, v})) != BSA_OK) return s;
+  if (k == v || k == cache || v == cache) return fail(BSA_ERR_INVALID_ARG, "k, v and cache must not alias");
   if ((s = check_cache_lists(page_table, start, count, nullptr)) != BSA_OK) return s;
   if ((s = check_device()) != BSA_OK) return s;
   const long long nslot = (static_cast<long long>(T) + 62) / 64 + 1;  // tiles that T tokens touch
@@ -1436,9 +1459,11 @@ bsa_status bsa_cache_block_topk(const void* q, const float* k_sum, const int32_t
       if (a != cudaSuccess) return a;
       if (dev < 64) attr_set[dev] = true;
     }
-    // a cluster for each row: as many CTAs as the device holds at once (two an SM), 32 blocks a CTA at least
+    // A cluster for each row: as many CTAs as the device holds at once (two an SM), 32 blocks a CTA at least; 16, more
+    // than every device has to take, only where it does.
+    const unsigned most = smem <= 65536 && cache_topk_takes_16(kern, dev) ? 16 : 8;
     unsigned ctas = 1;
-    while (ctas < 16 && static_cast<long long>(B) * H_kv * ctas * 2 <= 2 * sm_count() &&
+    while (ctas < most && static_cast<long long>(B) * H_kv * ctas * 2 <= 2 * sm_count() &&
            max_blocks >= static_cast<int>(ctas) * 2 * 32)
       ctas *= 2;
     cudaLaunchConfig_t cfg = {};

@@ -132,11 +132,13 @@ def test_write(bsa, case):
     both.check()
 
 
-def test_write_special_groups(bsa):
+@pytest.mark.parametrize("rows", [20, 64])  # some of a tile, and a tile of new rows only
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_write_special_groups(bsa, dtype, rows):
     """Constant groups, tiny ranges, huge values, and groups that are not finite."""
     rng = np.random.default_rng(5)
     both = Both(bsa, rng, 1, 1, 2, 128, 64)
-    k = randn(rng, 1, 20, 2, 128, dtype="f32")
+    k = randn(rng, 1, rows, 2, 128, dtype="f32")
     k[0, 0] = 7.25
     k[0, 1] = 1e-42
     k[0, 2] *= 1e30
@@ -148,6 +150,8 @@ def test_write_special_groups(bsa):
     k[0, 8] *= 1e-39
     k[0, 9] = k[0, 9] * 1e-3 + 1000
     k[0, 10] = -0.0
+    k[0, 11] = torch.linspace(1.0, 1.0 + 2.0 ** -7, 128, device="cuda")
+    k = k.to(DT[dtype])
     both.write(k, k.flip(1).contiguous(), np.array([0]))
     both.check()
 
@@ -449,6 +453,27 @@ def test_attn_nan_and_infinite_tokens_show_only_where_seen(bsa):
     for pos, bad in ((99, []), (100, [0, 1]), (119, [0, 1]), (120, [0, 1, 2, 3])):
         o = bsa.bsa_cache_attn(q, both.cache, both.tab, dev([pos]), 64)
         assert [h for h in range(4) if torch.isnan(o[0, 0, h]).any()] == bad, pos
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_of_many_rows_with_a_nan_among_the_new_tokens(bsa, D):
+    """The rows before a token that is not finite do not see it; those from it on do."""
+    rng = np.random.default_rng(21)
+    T, H, Hk, n = 12, 8, 2, 200
+    both = Both(bsa, rng, 1, 4, Hk, D, 64)
+    k, v = randn(rng, 1, n, Hk, D), randn(rng, 1, n, Hk, D)
+    v[0, n - 5, 0] = float("nan")
+    k[0, n - 3, 1, 0] = float("inf")
+    both.write(k, v, np.array([0]))
+    q = randn(rng, 1, T, H, D)
+    start = np.array([n - T])
+    o = bsa.bsa_cache_attn(q, both.cache, both.tab, dev(start), 64)
+    bad = torch.isnan(o[0].float()).any(-1).cpu().numpy()
+    assert np.array_equal(bad[:, :4], np.arange(T)[:, None].repeat(4, 1) >= T - 5)
+    assert np.array_equal(bad[:, 4:], np.arange(T)[:, None].repeat(4, 1) >= T - 3)
+    kv = {**both.ref, "kv": np.nan_to_num(both.ref["kv"])}
+    ref, size, logit = C.attn(kv, host(q), both.table, start)
+    check_attn(torch.nan_to_num(o), ref, size, logit, n, D, "bf16", ~bad[None])
 
 
 def test_attn_long_ragged_batch(bsa):

@@ -27,7 +27,7 @@ def _write(bsa, k=A, v=A, cache=A, k_sum=A, table=A, start=A, count=A, B=2, T=3,
                                    blocks, dt, _ptr(0))
 
 
-def _read(bsa, cache=A, table=A, start=A, count=A, k=A, v=A, B=2, T=3, Hk=2, D=64, bs=64, pages=8, blocks=4, dt=1):
+def _read(bsa, cache=A, table=A, start=A, count=A, k=A + 0x100, v=A + 0x200, B=2, T=3, Hk=2, D=64, bs=64, pages=8, blocks=4, dt=1):
     return bsa.lib.bsa_cache_read(*map(_ptr, (cache, table, start, count, k, v)), B, T, Hk, D, bs, pages, blocks, dt,
                                   _ptr(0))
 
@@ -69,13 +69,14 @@ def test_common_refusals(bsa, call, kw, status):
 @pytest.mark.parametrize("call,kw,status", [
     ("write", dict(k=0), 1), ("write", dict(v=A + 8), 3), ("write", dict(cache=0), 1), ("write", dict(k_sum=A + 4), 3),
     ("read", dict(cache=A + 8), 3), ("read", dict(k=0), 1), ("read", dict(v=A + 8), 3),
+    ("read", dict(k=A), 1), ("read", dict(v=A), 1), ("read", dict(k=A + 0x200), 1),
     ("topk", dict(q=0), 1), ("topk", dict(idx=0), 1), ("topk", dict(idx=A + 2), 3), ("topk", dict(topk=0), 1),
     ("topk", dict(H=3), 1), ("topk", dict(flags=4), 2), ("topk", dict(flags=2), 1), ("topk", dict(flags=8), 1),
     ("topk", dict(flags=0x100), 2), ("topk", dict(blocks=49153), 2),
     ("attn", dict(q=0), 1), ("attn", dict(o=A), 1), ("attn", dict(o=A + 8), 3), ("attn", dict(topk=0), 1),
     ("attn", dict(scale=0.0), 1), ("attn", dict(scale=float("nan")), 1), ("attn", dict(scale=float("inf")), 1),
     ("attn", dict(H=5), 1), ("attn", dict(ws=0), 4), ("attn", dict(wsb=8), 4), ("attn", dict(ws=A + 8), 3),
-    ("attn", dict(idx=A + 1), 3),
+    ("attn", dict(idx=A + 1), 3), ("attn", dict(B=4097), 2), ("forward", dict(B=4097), 2),
     ("forward", dict(q=0), 1), ("forward", dict(k=0), 1), ("forward", dict(o=A), 1), ("forward", dict(topk=-1), 1),
     ("forward", dict(flags=4), 2), ("forward", dict(flags=2), 1), ("forward", dict(ws=0), 4),
     ("forward", dict(wsb=64), 4), ("forward", dict(ws=A + 16), 3), ("forward", dict(blocks=49153), 2),
