@@ -41,6 +41,7 @@ BSA_FLAG_FORCE_DIAG, BSA_FLAG_MAX_POOL and BSA_GLOBAL_HEAD_PERIOD(p).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -595,28 +596,34 @@ def bsa_cache_alloc(num_pages: int, H_kv: int, D: int, block_size: int, device="
             torch.empty((num_pages, H_kv, D), device=device, dtype=torch.float32))
 
 
-def _cache_call(fn, named, *args):
-    """Calls fn(pointers of the named tensors..., *args, stream) with the first
-    one's device current and its current stream. Every tensor (None: a null
-    pointer) has to be contiguous on that CUDA device. Kept short: a step of
-    generation is a few microseconds of GPU time."""
-    dev = None
-    ptrs = []
+def _refuse(named, dev: int):
+    """Says which of a call's tensors is not a contiguous one on the first one's CUDA device."""
     for t, n in named:
         if t is None:
-            ptrs.append(None)
             continue
         if not t.is_cuda:
             raise ValueError(f"{n} must be a CUDA tensor")
         if not t.is_contiguous():
             raise ValueError(f"{n} must be contiguous")
-        d = t.get_device()
-        if dev is None:
-            dev = d
-        elif d != dev:
-            raise ValueError(f"{n} is on cuda:{d}, {named[0][1]} on cuda:{dev}")
-        ptrs.append(t.data_ptr())
-    if dev == torch.cuda.current_device():
+        if t.get_device() != dev:
+            raise ValueError(f"{n} is on {t.device}, {named[0][1]} on cuda:{dev}")
+
+
+def _cache_call(fn, named, *args):
+    """Calls fn(pointers of the named tensors..., *args, stream) with the first
+    one's device current and its current stream. Every tensor (None: a null
+    pointer) has to be contiguous on that CUDA device. Kept short: a step of
+    generation is a few microseconds of GPU time."""
+    dev = named[0][0].get_device()
+    ptrs = []
+    for t, _ in named:
+        if t is None:
+            ptrs.append(None)
+        elif dev >= 0 and t.get_device() == dev and t.is_contiguous():
+            ptrs.append(t.data_ptr())
+        else:
+            _refuse(named, dev)
+    if dev == torch._C._cuda_getDevice():
         status = fn(*ptrs, *args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
@@ -729,6 +736,7 @@ def bsa_cache_block_topk(q, k_sum, page_table, start, topk: int, block_size: int
     return idx_out
 
 
+@functools.lru_cache(maxsize=256)
 def bsa_cache_attn_workspace_bytes(B: int, T: int, H: int, H_kv: int, D: int) -> int:
     return lib.bsa_cache_attn_workspace_bytes(B, T, H, H_kv, D)
 
@@ -746,7 +754,7 @@ def bsa_cache_attn(q, cache, page_table, start, block_size: int, idx: torch.Tens
         topk = idx.shape[-1] if idx.dim() else 0
         _is(idx, (B, Hk, topk), torch.int32, "idx")
     if workspace is None and q.is_cuda:
-        workspace = torch.empty(max(lib.bsa_cache_attn_workspace_bytes(B, T, H, Hk, D), 1), device=q.device,
+        workspace = torch.empty(max(bsa_cache_attn_workspace_bytes(B, T, H, Hk, D), 1), device=q.device,
                                 dtype=torch.uint8)
     o = _step_out(out, q, count)
     _cache_call(lib.bsa_cache_attn,
@@ -765,6 +773,7 @@ def _room(workspace, q):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+@functools.lru_cache(maxsize=256)
 def bsa_cache_forward_workspace_bytes(B: int, T: int, H: int, H_kv: int, D: int, topk: int) -> int:
     return lib.bsa_cache_forward_workspace_bytes(B, T, H, H_kv, D, topk)
 
@@ -782,7 +791,7 @@ def bsa_cache_forward(q, k, v, cache, k_sum, page_table, start, block_size: int,
     _is(k_sum, (pages, Hk, D), torch.float32, "k_sum")
     _check_seqs(page_table, start, count, B)
     if workspace is None and q.is_cuda:
-        workspace = torch.empty(max(lib.bsa_cache_forward_workspace_bytes(B, T, H, Hk, D, topk), 1), device=q.device,
+        workspace = torch.empty(max(bsa_cache_forward_workspace_bytes(B, T, H, Hk, D, topk), 1), device=q.device,
                                 dtype=torch.uint8)
     o = _step_out(out, q, count)
     _cache_call(lib.bsa_cache_forward,
