@@ -979,10 +979,9 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
           }
       };
       // weights against the references as they stand, times the values' scales, in float16, to shared memory. True
-      // where one leaves float16 (from 2^15 on: 0x7800) or is beyond 2^90 (scales near zero).
+      // where one times its token's larger scale is above 2^15, or one is beyond 2^90 (scales near zero).
       auto weigh = [&](auto masked) -> bool {
-        uint32_t high = 0;
-        float most = 0.0f;
+        float most[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
           {
@@ -994,7 +993,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
               float lo, hi;
               f2_split(f2_sub(xs[nt][i], ref), lo, hi);
               lo = fast_exp2(lo), hi = fast_exp2(hi);
-              most = fmax3(most, lo, hi);
+              most[i] = fmax3(most[i], lo, hi);
               p[nt][i] = f2(lo, hi);
 #pragma unroll
               for (int j = 0; j < kGroups; ++j) {
@@ -1006,7 +1005,6 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
                   if (p0 + 8 * i >= lim.y) wh = 0.0f;
                 }
                 w16[j][i] = pack_f16(wl, wh);
-                high = max_u16x2(high, w16[j][i]);
               }
             }
 #pragma unroll
@@ -1014,7 +1012,14 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
               reinterpret_cast<uint2*>(sp)[(((buf * kGroups + j) * 4 + warp) * NT + nt) * 32 + lane] =
                   make_uint2(transpose8x8(w16[j][0]), transpose8x8(w16[j][1]));
           }
-        return __any_sync(0xffffffffu, max_u16x2(high, 0x78007800u) != 0x78007800u || most > 0x1p90f);
+        bool over = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float vmax = __uint_as_float(vsz[i][0] << 16);
+          if constexpr (kGroups == 2) vmax = fmaxf(vmax, __uint_as_float(vsz[i][1] << 16));
+          over = over || most[i] * vmax > 32768.0f || most[i] > 0x1p90f;
+        }
+        return __any_sync(0xffffffffu, over);
       };
       if (pos >= 0) {
         if (edge)
@@ -1111,39 +1116,40 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
         else
           add_up(std::false_type{});
         const int word = D == 128 ? warp : warp / 2, j = word / 2;
-        uint32_t vw[4][2][1];
+        // a tile's products start from zero and are added in float32 (see the other kernel)
+        float sum[kMt][NT][4];
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt)
+        for (int kt = 0; kt < 4; ++kt) {
+          uint32_t vw[2][1], av[kMt][4];
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            get_words(base + cache_v_offset(D) + (kt * 8 + t4 + 4 * i) * D + (g ^ (2 * t4)) * (D / 8) + word * 4,
-                      vw[kt][i]);
-        // a tile's products start from zero and are added in float32 (see the other kernel)
+            get_words(base + cache_v_offset(D) + (kt * 8 + t4 + 4 * i) * D + (g ^ (2 * t4)) * (D / 8) + word * 4, vw[i]);
 #pragma unroll
-        for (int k = 0; k < kMt; ++k) {
-          const uint32_t pick = D == 128 ? (k ? 0x4341u : 0x4240u) : (warp % 2 ? 0x4341u : 0x4240u);
-          float sum[NT][4];
-#pragma unroll
-          for (int kt = 0; kt < 4; ++kt) {
-            const uint32_t a1 = __byte_perm(vw[kt][0][0], 0, pick), a0 = a1 & kLow;
-            const uint32_t a3 = __byte_perm(vw[kt][1][0], 0, pick), a2 = a3 & kLow;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint2 bp =
-                  reinterpret_cast<const uint2*>(sp)[(((buf * kGroups + j) * 4 + kt) * NT + nt) * 32 + lane];
-              if (kt == 0)
-                mma_f16_first(sum[nt], a0, a1, a2, a3, bp.x, bp.y);
-              else
-                mma_f16(sum[nt], a0, a1, a2, a3, bp.x, bp.y);
-            }
+          for (int k = 0; k < kMt; ++k) {
+            const uint32_t pick = D == 128 ? (k ? 0x4341u : 0x4240u) : (warp % 2 ? 0x4341u : 0x4240u);
+            av[k][1] = __byte_perm(vw[0][0], 0, pick), av[k][0] = av[k][1] & kLow;
+            av[k][3] = __byte_perm(vw[1][0], 0, pick), av[k][2] = av[k][3] & kLow;
           }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 bp = reinterpret_cast<const uint2*>(sp)[(((buf * kGroups + j) * 4 + kt) * NT + nt) * 32 + lane];
+#pragma unroll
+            for (int k = 0; k < kMt; ++k)
+              if (kt == 0)
+                mma_f16_first(sum[k][nt], av[k][0], av[k][1], av[k][2], av[k][3], bp.x, bp.y);
+              else
+                mma_f16(sum[k][nt], av[k][0], av[k][1], av[k][2], av[k][3], bp.x, bp.y);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kMt; ++k)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-              f2_split(f2_add(f2(acc[k][nt][2 * i], acc[k][nt][2 * i + 1]), f2(sum[nt][2 * i], sum[nt][2 * i + 1])),
+              f2_split(f2_add(f2(acc[k][nt][2 * i], acc[k][nt][2 * i + 1]),
+                              f2(sum[k][nt][2 * i], sum[k][nt][2 * i + 1])),
                        acc[k][nt][2 * i], acc[k][nt][2 * i + 1]);
-        }
       }
       buf ^= 1;
       if (++stage == kStages) stage = 0, phase ^= 1;
