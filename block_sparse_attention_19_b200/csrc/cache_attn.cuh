@@ -45,6 +45,7 @@ namespace bsa {
 constexpr int kCaWarps = 4;  // in two pairs: a tile goes to a pair, 32 tokens to a warp
 constexpr int kCaThreads = kCaWarps * 32;
 constexpr int kCaMaxSeqs = 4096;  // sequences whose plan fits in shared memory
+constexpr float kCaNone = -0x1.fffffep127f;  // reference of a row that has seen nothing: no finite score is below it
 
 // How many query rows a unit has and how they fill the products' eight columns: each once, or (FOLD = 2, up to four
 // rows) twice, the two halves for different tokens.
@@ -135,6 +136,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ uint32_t pack_f16_rest(float lo, float hi, uint32_t packed) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&packed));
   return pack_f16(lo - f.x, hi - f.y);
+}
+
+// 2^e scale_log2, what a row's products with codes are multiplied by. A row with an element of 2^117 or more, an
+// infinity too, has NaN instead: 2^e does not hold its scale any more, and its scores would be wrong, not infinite.
+__device__ __forceinline__ float score_factor(float amax, int e, float scale_log2) {
+  const float f = __uint_as_float(static_cast<uint32_t>(min(e, 127) + 127) << 23) * scale_log2;
+  return amax < 0x1p117f ? f : CUDART_NAN_F;
 }
 
 // How the tiles of all units are laid in one line and cut into equal pieces, one
@@ -352,7 +360,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
     // (odd channels 2^-23) of it
     const int up = min(13 - static_cast<int>((__float_as_uint(amax) >> 23) & 255u) + 127, 126);
     const float qscale = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
-    const float back = __uint_as_float(static_cast<uint32_t>((kCentre ? 0 : 24) - up + 127) << 23) * scale_log2;
+    const float back = score_factor(amax, (kCentre ? 0 : 24) - up, scale_log2);
 #pragma unroll
     for (int w = 0; w < kWords; ++w) {
 #pragma unroll
@@ -401,7 +409,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
     float m[2], l[2], z[2][kGroups], acc[kWords][2][4];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      m[c] = -1e30f, l[c] = 0.0f;
+      m[c] = kCaNone, l[c] = 0.0f;
 #pragma unroll
       for (int j = 0; j < kGroups; ++j) z[c][j] = 0.0f;
     }
@@ -882,11 +890,11 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
               make_uint2(pack_f16(f[w][2 * k], f[w][2 * k + 4]), pack_f16(f[w][2 * k + 1], f[w][2 * k + 5]));
       }
       if (t4 == 0) {
-        s_mul[r] = __uint_as_float(static_cast<uint32_t>(24 - up + 127) << 23) * scale_log2;
+        s_mul[r] = score_factor(amax, 24 - up, scale_log2);
 #pragma unroll
         for (int j = 0; j < kGroups; ++j) s_qsum[j][r] = sum[j] * scale_log2;
         s_limit[r] = r < rows ? start + row / G + 1 : 0;
-        s_m[r] = -1e30f;
+        s_m[r] = kCaNone;
       }
     }
     const int low_limit = start + row0 / G + 1;  // positions below it are seen by all rows
@@ -1227,7 +1235,7 @@ __global__ void __launch_bounds__(kCaJoinWarps * 32)
   if (c0 == c1) return;
   // four parts at a time in flight, each against the largest reference so far
   constexpr int kAhead = 4;
-  float top = -1e30f, weight = 0.0f, val[kPer] = {};
+  float top = kCaNone, weight = 0.0f, val[kPer] = {};
   for (int c = c0 + warp; c <= c1; c += kAhead * kCaJoinWarps) {
     float m[kAhead], l[kAhead], v[kAhead][kPer], now = top;
 #pragma unroll

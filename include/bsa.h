@@ -500,7 +500,9 @@ size_t bsa_cache_attn_workspace_bytes(int B, int T, int H, int H_kv, int D);
  * weights times the values' scales are rounded to float16 for the tensor cores
  * (relative 2^-11), float32 queries' parts are split in two. workspace: device
  * memory of bsa_cache_attn_workspace_bytes() bytes, 16-byte aligned, not used
- * by an overlapping call. B <= 4096. Deterministic. */
+ * by an overlapping call. B <= 4096. Deterministic. A query row with a NaN, an
+ * infinity or an element of 2^117 or more in size gives NaN (zeros where it
+ * sees no token). */
 bsa_status bsa_cache_attn(const void* q, const void* cache, const int32_t* page_table, const int32_t* start,
                           const int32_t* count, const int32_t* idx, void* o, int B, int T, int H, int H_kv, int D,
                           int block_size, int num_pages, int max_blocks, int topk, float scale, bsa_dtype dt,

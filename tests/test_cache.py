@@ -476,6 +476,51 @@ def test_attn_of_many_rows_with_a_nan_among_the_new_tokens(bsa, D):
     check_attn(torch.nan_to_num(o), ref, size, logit, n, D, "bf16", ~bad[None])
 
 
+FORMS = [("bf16", 1, 1), ("bf16", 4, 2), ("bf16", 4, 3), ("bf16", 8, 5), ("f32", 4, 1), ("f32", 4, 2)]  # type, G, T
+
+
+@pytest.mark.parametrize("dtype,G,T", FORMS, ids=lambda x: str(x))
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_queries_that_are_not_finite(bsa, D, dtype, G, T):
+    """A row with an infinity, a NaN or an element of 2^117 and above gives NaN, also where all its scores would be
+    -inf; the others know nothing of it, and neither does a row that sees no token."""
+    rng = np.random.default_rng(23)
+    Hk, n = 5, 150
+    both = Both(bsa, rng, 1, 3, Hk, D, 64)
+    k, v = randn(rng, 1, n, Hk, D, offset=-8.0), randn(rng, 1, n, Hk, D)
+    both.write(k, v, np.array([0]))
+    q = randn(rng, 1, T, Hk * G, D, dtype=dtype)
+    clean, start = q.clone(), np.array([n - T])
+    bad = np.zeros((1, T, Hk * G), bool)
+    for i, x in enumerate((float("inf"), -float("inf"), float("nan"), 2.0 ** 117)):
+        q[0, T - 1, i * G, 7 * i] = x
+        bad[0, T - 1, i * G] = True
+    o = bsa.bsa_cache_attn(q, both.cache, both.tab, dev(start), 64)
+    assert torch.isnan(o[torch.as_tensor(bad, device="cuda")]).all()
+    ref, size, logit = C.attn(both.ref, host(clean), both.table, start)
+    check_attn(torch.nan_to_num(o), ref, size, logit, n, D, dtype, ~bad)
+    idx = torch.full((1, Hk, 1), -1, dtype=torch.int32, device="cuda")
+    assert not bsa.bsa_cache_attn(q, both.cache, both.tab, dev(start), 64, idx=idx).any()
+
+
+@pytest.mark.parametrize("dtype,G,T", FORMS, ids=lambda x: str(x))
+def test_attn_scores_far_below_zero(bsa, dtype, G, T):
+    """Scores of -2^113 (i + 1): all weight is on token 0. Weight 1 in float16 (2^-11 at most), the output's rounding
+    (2^-9) and float32 sums stay below 2^-8 of |zero| + 15 scale."""
+    rng = np.random.default_rng(24)
+    D, Hk, n = 64, 2, 200
+    both = Both(bsa, rng, 1, 4, Hk, D, 64)
+    k = torch.arange(1, n + 1, device="cuda", dtype=torch.float32).view(1, n, 1, 1).expand(1, n, Hk, D) * -2.0 ** 50
+    v = randn(rng, 1, n, Hk, D)
+    both.write(k.bfloat16().contiguous(), v, np.array([0]))
+    q = torch.full((1, T, Hk * G, D), 2.0 ** 60, device="cuda", dtype=DT[dtype])
+    o = bsa.bsa_cache_attn(q, both.cache, both.tab, dev([n - T]), 64)
+    _, held = bsa.bsa_cache_read(both.cache, both.tab, dev([0]), n, 64, dtype=torch.float32)
+    want = held[0, 0].repeat_interleave(G, 0).expand(T, -1, -1)
+    size = 2 * held[0, 0].abs().amax(-1).repeat_interleave(G, 0).view(1, -1, 1)
+    assert ((o[0].float() - want).abs() <= 2.0 ** -8 * size).all()
+
+
 def test_attn_long_ragged_batch(bsa):
     """Many sequences of very different lengths against the float64 formula on what is read back."""
     g = torch.Generator(device="cuda").manual_seed(3)
