@@ -45,6 +45,12 @@ namespace bsa {
 constexpr int kCaWarps = 4;  // in two pairs: a tile goes to a pair, 32 tokens to a warp
 constexpr int kCaThreads = kCaWarps * 32;
 constexpr int kCaMaxSeqs = 4096;  // sequences whose plan fits in shared memory
+// Where a raised reference puts log2 of the largest weight times scale. Later ones may reach 2^15 before the next raise,
+// and a raise weighs a tile twice: from 8 on 2^7 times the largest so far is left, with scores of deviation 2 most rows'
+// last raise (many rows: 33.2 us, 36.2 from 12 on). What float16's smallest number costs is 2^-33 of the largest, below the
+// float32 sums' rounding. float32 queries keep the finer 12.
+template <typename T>
+constexpr float kCaRaise = sizeof(T) == 4 ? 12.0f : 8.0f;
 constexpr float kCaNone = -0x1.fffffep127f;  // reference of a row that has seen nothing: no finite score is below it
 
 // How many query rows a unit has and how they fill the products' eight columns: each once, or (FOLD = 2, up to four
@@ -521,7 +527,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
       // Is a weight times scale at 2^15 or above (0x7800), or a sum of weights beyond 2^90 (scales near zero)?
       // Scales are not negative, so the codes of the float16 halves rank as they do.
       if (__any_sync(0xffffffffu, max_u16x2(high, 0x78007800u) != 0x78007800u || most > 0x1p90f)) {
-        // raise the references so that the largest weight times scale is 2^12
+        // raise the references so that the largest weight times scale is 2^kCaRaise
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float u = -CUDART_INF_F;
@@ -536,7 +542,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
             }
 #pragma unroll
           for (int d = 4; d < 32; d *= 2) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, d));
-          const float now = fmaxf(m[c], u - 12.0f), f = fast_exp2(m[c] - now);
+          const float now = fmaxf(m[c], u - kCaRaise<T>), f = fast_exp2(m[c] - now);
           m[c] = now;
           l[c] *= f;
 #pragma unroll
@@ -1065,7 +1071,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
       if (lane == 0) s_flag[warp] = flag;
       if (__syncthreads_or(flag)) {
         fresh = false;
-        // raise the references so that the largest weight times scale is 2^12, and weigh again (a NaN stays one)
+        // raise the references so that the largest weight times scale is 2^kCaRaise, and weigh again (a NaN stays one)
         float now[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -1076,7 +1082,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
 #pragma unroll
             for (int w = 0; w < kCaWarps; ++w)
               if (s_flag[w]) top = fmaxf(top, s_cand[w][col]);
-            const float old = s_m[col], f = fast_exp2(old - (now[nt][c] = fmaxf(old, top - 12.0f)));
+            const float old = s_m[col], f = fast_exp2(old - (now[nt][c] = fmaxf(old, top - kCaRaise<__nv_bfloat16>)));
             const uint64_t by = c ? f2(1.0f, f) : f2(f, 1.0f);
             l[nt] = f2_mul(l[nt], by);
 #pragma unroll

@@ -498,7 +498,8 @@ size_t bsa_cache_attn_workspace_bytes(int B, int T, int H, int H_kv, int D);
  * cache: write them first. q, o: [B, T, H, D]; o must not be q. Scores, the
  * softmax's sums and the output sums are float32; bfloat16 queries' softmax
  * weights times the values' scales are rounded to float16 for the tensor cores
- * (relative 2^-11), float32 queries' parts are split in two. workspace: device
+ * (relative 2^-11, and 2^-33 of the row's largest weight times scale over all
+ * channels), float32 queries' parts are split in two. workspace: device
  * memory of bsa_cache_attn_workspace_bytes() bytes, 16-byte aligned, not used
  * by an overlapping call. B <= 4096. Deterministic. A query row with a NaN, an
  * infinity or an element of 2^117 or more in size gives NaN (zeros where it
