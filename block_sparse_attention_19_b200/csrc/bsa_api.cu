@@ -1289,7 +1289,8 @@ bsa_status check_attn_tiles(int B, int T, int H, int Hkv, int block_size, int ma
   if (B > bsa::kCaMaxSeqs)
     return fail(BSA_ERR_UNSUPPORTED, "B=%d (the attention takes up to %d sequences)", B, bsa::kCaMaxSeqs);
   const double units = static_cast<double>(B) * Hkv * ((static_cast<long long>(T) * (H / Hkv) + 7) / 8);
-  if (units * (topk ? topk : max_blocks) * (block_size / 64) > 2.1e9)
+  // (a unit weighs a few tiles more than it has)
+  if (units * ((topk ? topk : max_blocks) * (block_size / 64.0) + bsa::kCaMaxExtra) > 2.1e9)
     return fail(BSA_ERR_UNSUPPORTED, "more than 2.1e9 tiles of 64 tokens");
   return BSA_OK;
 }

@@ -44,6 +44,7 @@ namespace bsa {
 
 constexpr int kCaWarps = 4;  // in two pairs: a tile goes to a pair, 32 tokens to a warp
 constexpr int kCaThreads = kCaWarps * 32;
+constexpr int kCaMaxExtra = 6;  // (see CaPlan)
 constexpr int kCaMaxSeqs = 4096;  // sequences whose plan fits in shared memory
 // Where a raised reference puts log2 of the largest weight times scale. Later ones may reach 2^15 before the next raise,
 // and a raise weighs a tile twice: from 8 on 2^7 times the largest so far is left, with scores of deviation 2 most rows'
@@ -60,6 +61,7 @@ struct CaShape {
   static constexpr int kCols = 8;
   static constexpr int kRows = kCols / FOLD;  // query rows of a unit
   static constexpr int kCtas = 4;  // CTAs of an SM: four warps to each of its quarters
+  static constexpr int kExtra = 6;  // (see CaPlan)
   static constexpr int kOStride = D + 4;  // floats of a row in the join buffer: 16-byte stores free of conflicts
   static constexpr int kJoinBytes = kCaWarps * kCols * kOStride * 4;
   static constexpr int kStages = 2 * 128 / D;  // tiles of a pair's ring
@@ -153,12 +155,44 @@ __device__ __forceinline__ float score_factor(float amax, int e, float scale_log
 
 // How the tiles of all units are laid in one line and cut into equal pieces, one
 // for each CTA. A unit is (sequence, key/value head, run of kRows query rows).
+//
+// Beginning a unit (its queries, its first tile's references, the sums of the one
+// before) takes a CTA as long as `extra` tiles, so the pieces are equal in tiles
+// and beginnings together: a unit weighs its tiles and `extra` more, which come
+// before them. (Ragged batch of 48: 16.6 us with six, 17.7 with two, 18.3 with none;
+// 40 rows: 28.0 with four, 29.0 with two, 33.1 with none.)
 struct CaPlan {
-  const int4* seqs;  // [B]: tiles before the sequence, tiles of each of its units, start, count
+  const int4* seqs;  // [B]: tiles before the sequence, weight before it, start, count
   int per_seq;       // units of a sequence
   int row_tiles;     // units of a (sequence, head)
-  int total, chunk;
-  int B;
+  // x: tiles of a unit where blocks are selected (otherwise 0), y: tokens of a full table. In shared memory, since
+  // registers are short in the loop over tiles (dense 32768-token batch: 64.5 us, 59.8 without them).
+  const volatile int2* limits;
+  int total, weight;  // tiles and weight of all units
+  int chunk;          // weight of a CTA
+  int extra, B;
+
+  // tiles of each unit of a sequence with these values
+  static __device__ __forceinline__ int tiles(int start, int count, int fixed, int most) {
+    return count == 0 ? 0 : fixed ? fixed : (min(start + count, most) + kCacheTile - 1) / kCacheTile;
+  }
+
+  // The first tile of CTA i.
+  __device__ __forceinline__ int cut(int i) const {
+    const int at = i * chunk;
+    if (at >= weight) return total;
+    int lo = 0, hi = B - 1;  // as in locate
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (seqs[mid].y <= at)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const int4 q = seqs[lo];
+    const int n = tiles(q.z, q.w, limits->x, limits->y), unit = (at - q.y) / (n + extra), in = (at - q.y) % (n + extra);
+    return q.x + unit * n + max(in - extra, 0);
+  }
 
   // The unit of tile x: its sequence and number there, first tile and tiles; the sequence's start and count.
   struct Unit {
@@ -174,49 +208,60 @@ struct CaPlan {
         hi = mid - 1;
     }
     const int4 q = seqs[lo];
-    const int unit = (x - q.x) / q.y;
-    return Unit{lo, unit, q.x + unit * q.y, q.y, q.z, q.w};
+    const int n = tiles(q.z, q.w, limits->x, limits->y), unit = (x - q.x) / n;
+    return Unit{lo, unit, q.x + unit * n, n, q.z, q.w};
   }
   __device__ __forceinline__ int head(int unit) const { return row_tiles == 1 ? unit : unit / row_tiles; }
   __device__ __forceinline__ int row0(int unit, int rows) const { return row_tiles == 1 ? 0 : unit % row_tiles * rows; }
 };
 
-// Fills the plan; `table` is shared memory for B int4. All threads of the block call it; it ends with a barrier. The
-// first CTA leaves the chunk and the table in `out` for the joining launch.
-__device__ __forceinline__ CaPlan make_plan(const CacheSeqs& s, int B, int Hkv, int row_tiles, int topk, int ctas,
-                                            int4* table, int4* out) {
-  __shared__ int total;
+// Fills the plan and finds the CTA's piece [begin, end); `table` is shared memory for B int4. All threads of the block
+// call it; it ends with a barrier. The first CTA leaves what the joining launch needs in `out`.
+__device__ __forceinline__ CaPlan make_plan(const CacheSeqs& s, int B, int Hkv, int row_tiles, int topk, int extra,
+                                            int4* table, int4* out, int& begin, int& end) {
+  __shared__ int total, weight;
+  __shared__ int2 limits;
   CaPlan p;
-  p.seqs = table, p.row_tiles = row_tiles, p.per_seq = Hkv * row_tiles, p.B = B;
+  p.seqs = table, p.row_tiles = row_tiles, p.per_seq = Hkv * row_tiles, p.extra = extra, p.B = B;
+  const int fixed = topk * (s.bs / kCacheTile), most = s.max_blocks * s.bs;
+  if (threadIdx.x == 0) limits = make_int2(fixed, most);
+  p.limits = &limits;
   for (int b = threadIdx.x; b < B; b += blockDim.x) {
-    int start, count, n = 0;
+    int start, count;
     seq_step(s, b, start, count);
-    if (count) n = topk ? topk * (s.bs / kCacheTile) : (min(start + count, s.max_blocks * s.bs) + kCacheTile - 1) / kCacheTile;
-    table[b] = make_int4(0, n, start, count);
+    table[b] = make_int4(0, 0, start, count);
   }
   if (B > 32) __syncthreads();
   if (threadIdx.x < 32) {  // warp 0 sums up the sequences' tiles, 32 at a time
     __syncwarp();
-    int sum = 0;
+    int sum = 0, begun = 0;  // tiles, and sequences with some
     for (int b0 = 0; b0 < B; b0 += 32) {
-      const int b = b0 + threadIdx.x, n = b < B ? table[b].y * p.per_seq : 0;
+      const int b = b0 + threadIdx.x;
+      const int4 q = b < B ? table[b] : make_int4(0, 0, 0, 0);
+      const int n = CaPlan::tiles(q.z, q.w, fixed, most) * p.per_seq;
       int before = n;
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
         const int other = __shfl_up_sync(0xffffffffu, before, d);
         if (threadIdx.x >= d) before += other;
       }
-      if (b < B) table[b].x = sum + before - n;
+      const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
+      const int x = sum + before - n;
+      if (b < B)
+        table[b] = make_int4(x, x + (begun + __popc(some & ((1u << threadIdx.x) - 1))) * p.per_seq * extra, q.z, q.w);
       sum += __shfl_sync(0xffffffffu, before, 31);
+      begun += __popc(some);
     }
-    if (threadIdx.x == 0) total = sum;
+    if (threadIdx.x == 0) total = sum, weight = sum + begun * p.per_seq * extra;
   }
   __syncthreads();
-  p.total = total;
-  p.chunk = max(1, (p.total + ctas - 1) / ctas);
+  p.total = total, p.weight = weight;
+  p.chunk = max(1, (p.weight + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+  const int x = p.cut(blockIdx.x + threadIdx.x % 2);  // even threads the first tile, odd ones the next CTA's
+  begin = __shfl_sync(0xffffffffu, x, 0), end = __shfl_sync(0xffffffffu, x, 1);
   if (blockIdx.x == 0) {
     for (int b = threadIdx.x; b < B; b += blockDim.x) out[1 + b] = table[b];
-    if (threadIdx.x == 0) out[0] = make_int4(p.chunk, 0, 0, 0);
+    if (threadIdx.x == 0) out[0] = make_int4(p.chunk, extra, fixed, most);
   }
   return p;
 }
@@ -287,9 +332,9 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
     fence_mbarrier_init();
   }
   pdl_wait();
-  const CaPlan plan = make_plan(s, B, Hkv, (s.T * G + kRows - 1) / kRows, idx ? topk : 0, gridDim.x, table, plan_out);
-  const int begin = min(static_cast<long>(blockIdx.x) * plan.chunk, static_cast<long>(plan.total));
-  const int end = min(begin + plan.chunk, plan.total);
+  int begin, end;
+  const CaPlan plan = make_plan(s, B, Hkv, (s.T * G + kRows - 1) / kRows, idx ? topk : 0, Shape::kExtra, table, plan_out,
+                                begin, end);
   volatile int* abort = &abort_flag;
   uint8_t* stages = smem + pair * kStages * kTile;
   uint64_t *full = bars[pair][0], *empty = bars[pair][1];
@@ -760,6 +805,7 @@ template <int D, int NT>
 struct CaWide {
   static constexpr int kRows = 8 * NT;
   static constexpr int kCtas = NT <= 4 ? 3 : 2;
+  static constexpr int kExtra = 4;  // (see CaPlan)
   static constexpr int kStages = 4 * 128 / D;
   static constexpr int kGroups = D / 64, kSteps = D / 16;
   static constexpr int kQWords = kSteps * NT * 64;            // query operands: [step][nt][lane][2]
@@ -820,9 +866,9 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
     fence_mbarrier_init();
   }
   pdl_wait();
-  const CaPlan plan = make_plan(s, B, Hkv, (s.T * G + kRows - 1) / kRows, idx ? topk : 0, gridDim.x, table, plan_out);
-  const int begin = min(static_cast<long>(blockIdx.x) * plan.chunk, static_cast<long>(plan.total));
-  const int end = min(begin + plan.chunk, plan.total);
+  int begin, end;
+  const CaPlan plan = make_plan(s, B, Hkv, (s.T * G + kRows - 1) / kRows, idx ? topk : 0, W::kExtra, table, plan_out,
+                                begin, end);
   volatile int* abort = &abort_flag;
 
   // the last warp: copies the next tile into its stage; where the next 32 lie is looked up at once, one lane each
@@ -1233,11 +1279,11 @@ __global__ void __launch_bounds__(kCaJoinWarps * 32)
   const int G = H / Hkv, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int row_tiles = (tokens * G + kRows - 1) / kRows;
   const int row = blockIdx.x % (tokens * G), h = blockIdx.x / (tokens * G) % Hkv, b = blockIdx.x / (tokens * G) / Hkv;
-  const int chunk = plan[0].x;
-  const int4 seq = plan[1 + b];
+  const int4 head = plan[0], seq = plan[1 + b];  // (see make_plan)
   if (row / G >= seq.w) return;
-  const int r = row % kRows, first = seq.x + (h * row_tiles + row / kRows) * seq.y;
-  const int c0 = first / chunk, c1 = (first + seq.y - 1) / chunk;
+  const int chunk = head.x, extra = head.y, n = CaPlan::tiles(seq.z, seq.w, head.z, head.w);
+  const int r = row % kRows, first = seq.y + (h * row_tiles + row / kRows) * (n + extra) + extra;  // the first tile's place
+  const int c0 = first / chunk, c1 = (first + n - 1) / chunk;
   if (c0 == c1) return;
   // four parts at a time in flight, each against the largest reference so far
   constexpr int kAhead = 4;
