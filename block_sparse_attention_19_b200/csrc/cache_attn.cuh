@@ -910,17 +910,27 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
     const int rows = min(kRows, u.count * G - row0);  // rows with a query (may be <= 0)
 
     // ---------------- the queries as the score products' second operand (float16, odd channels / 16: see above)
-    for (int nt = warp; nt < NT; nt += kCaWarps) {
+    constexpr int kPer = (NT + kCaWarps - 1) / kCaWarps;
+    Octet<__nv_bfloat16> raw[kPer][kWords];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int r = (warp + e * kCaWarps) * 8 + g, row = row0 + r;
+#pragma unroll
+      for (int w = 0; w < kWords; ++w)
+        if (r < rows)
+          raw[e][w].load(q + ((static_cast<long>(b) * s.T + row / G) * H + h * G + row % G) * D + w * 32 + t4 * 8);
+        else
+          raw[e][w] = Octet<__nv_bfloat16>{};
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int nt = warp + e * kCaWarps;
+      if (nt >= NT) break;
       const int r = nt * 8 + g, row = row0 + r;
       float f[kWords][8], amax = 0.0f, sum[kGroups] = {};
 #pragma unroll
       for (int w = 0; w < kWords; ++w) {
-        if (r < rows) {
-          load_octet(q + ((static_cast<long>(b) * s.T + row / G) * H + h * G + row % G) * D + w * 32 + t4 * 8, f[w]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[w][i] = 0.0f;
-        }
+        raw[e][w].floats(f[w]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[w][i])), sum[w / 2] += f[w][i];
       }
