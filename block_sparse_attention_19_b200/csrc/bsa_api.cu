@@ -1519,9 +1519,9 @@ bsa_status bsa_cache_attn(const void* q, const void* cache, const int32_t* page_
       return launch(q, cache, idx, o, workspace, seqs, B, H, H_kv, topk, sl, stream);
     };
     // Query rows of a (sequence, key/value head): up to four are folded (everything between the products once for two
-    // runs of tokens: dense 32768-token batch, four rows, 65 us against 69), up to eight fill the products' columns
+    // runs of tokens: dense 32768-token batch, four rows, 59 us against 63.5), up to eight fill the products' columns
     // once. More go to the kernel whose warps share a tile, in units of equal size of up to 40 (40 rows, eight padded
-    // sequences of up to 16384 tokens: 36 us, 41 in units of 16 rows of the other kernel). float32 queries, whose
+    // sequences of up to 16384 tokens: 27 us, 28 in units of 8 rows of the other kernel). float32 queries, whose
     // operands come in two parts, stay with the first.
     const long long rows = static_cast<long long>(T) * (H / H_kv);
     if constexpr (sizeof(E) == 2) {

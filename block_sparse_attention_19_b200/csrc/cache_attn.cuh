@@ -29,8 +29,8 @@
 // All units' tiles lie in one line, cut into equal pieces for CTAs that are all
 // resident at once; a unit that several CTAs share leaves one part for each, which a
 // second launch joins. Measured on one B200 (6.55 TB/s copied): 16 sequences of
-// 32768 tokens, 4 heads, four query rows each: 61.6 us for 302 MB, 4.9 TB/s; 15% of
-// the blocks of up to 131072 tokens: 37 us; one sequence of 397 tokens: 8 us, of
+// 32768 tokens, 4 heads, four query rows each: 59 us for 302 MB, 5.1 TB/s; 15% of
+// the blocks of up to 131072 tokens: 35 us; one sequence of 397 tokens: 8 us, of
 // which 2 are the joining launch. In the long run a tile costs its bytes' time;
 // the rest is a chain that every call has: lengths, plan, page, first tile (4 us),
 // the last tiles' sums (1.3 us), the joining (2 to 4.5 us).
@@ -797,9 +797,10 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
 // references are the CTA's, in shared memory; a tile whose weights would leave
 // float16 raises them and is weighed again. Bound: the matrix instructions, 16 NT
 // (D = 128) for 16 tokens at 2.2 cycles of an SM each, 700 cycles a tile at 40 rows
-// against 400 for its bytes; measured, 2150: eight warps an SM do not hide the
-// chain of products, exponentials, barrier and products (issue 40%, matrix unit
-// 30%, shared memory 45% busy). Two teams of four warps with half the rows each
+// against 400 for its bytes; measured, 1850: eight warps an SM do not hide the
+// chain of products, exponentials, barrier and products (profiled at 2150, before
+// references left more room: issue 40%, matrix unit 30%, shared memory 45% busy;
+// three CTAs an SM, with spills, 86 -> 110 us for 32768 tokens). Two teams of four warps with half the rows each
 // took 1.4 times as long, since both unpack every tile.
 template <int D, int NT>
 struct CaWide {
