@@ -753,6 +753,8 @@ def bsa_cache_attn(q, cache, page_table, start, block_size: int, idx: torch.Tens
     if idx is not None:
         topk = idx.shape[-1] if idx.dim() else 0
         _is(idx, (B, Hk, topk), torch.int32, "idx")
+        if topk < 1:  # an empty tensor's pointer is null, which the library takes for "all blocks"
+            raise ValueError(f"idx has shape {tuple(idx.shape)}, topk must be positive")
     if workspace is None and q.is_cuda:
         workspace = torch.empty(max(bsa_cache_attn_workspace_bytes(B, T, H, Hk, D), 1), device=q.device,
                                 dtype=torch.uint8)

@@ -148,3 +148,13 @@ def test_binding_refuses_before_the_device(bsa):
             f()
     with pytest.raises(ValueError):
         bsa.bsa_cache_alloc(8, 2, 96, 64, device="cpu")
+
+
+@pytest.mark.parametrize("shape", [(2, 2, 0), (2, 0), ()])
+def test_binding_refuses_an_empty_selection(bsa, shape):
+    """idx without a block is not "all blocks", although its pointer is null."""
+    q = torch.zeros(2, 1, 4, 64, dtype=torch.bfloat16)
+    cache, _ = bsa.bsa_cache_alloc(8, 2, 64, 64, device="cpu")
+    table, start = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="idx"):
+        bsa.bsa_cache_attn(q, cache, table, start, 64, idx=torch.zeros(shape, dtype=torch.int32))
