@@ -641,7 +641,7 @@ def _is(t: torch.Tensor, shape: tuple, dtype: torch.dtype, name: str):
 
 def _check_seqs(page_table, start, count, B: int):
     if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [{B}, max_blocks]")
+        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [{B or 'B'}, max_blocks]")
     if page_table.dtype is not torch.int32:
         raise TypeError("page_table must be int32")
     _is(start, (B,), torch.int32, "start")
@@ -702,7 +702,7 @@ def bsa_cache_read(cache, page_table, start, T: int, block_size: int, dtype: tor
     k_out's). Rows t >= count[b] of k_out and v_out stay as they are; tensors
     that the call makes hold zeros there."""
     pages, Hk, D = _cache_sizes(cache, block_size)
-    B = page_table.shape[0]
+    B = page_table.shape[0] if page_table.dim() else 0
     _check_seqs(page_table, start, count, B)
     new = torch.empty if count is None else torch.zeros
     if k_out is None:

@@ -158,3 +158,17 @@ def test_binding_refuses_an_empty_selection(bsa, shape):
     table, start = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError, match="idx"):
         bsa.bsa_cache_attn(q, cache, table, start, 64, idx=torch.zeros(shape, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("shape", [(), (2,), (2, 4, 1)])
+def test_binding_refuses_page_tables_of_other_dimensions(bsa, shape):
+    x = torch.zeros(2, 1, 2, 64, dtype=torch.bfloat16)
+    cache, k_sum = bsa.bsa_cache_alloc(8, 2, 64, 64, device="cpu")
+    table, start = torch.zeros(shape, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: bsa.bsa_cache_write(x, x, cache, k_sum, table, start, 64),
+                 lambda: bsa.bsa_cache_read(cache, table, start, 1, 64),
+                 lambda: bsa.bsa_cache_block_topk(x, k_sum, table, start, 1, 64),
+                 lambda: bsa.bsa_cache_attn(x, cache, table, start, 64),
+                 lambda: bsa.bsa_cache_forward(x, x, x, cache, k_sum, table, start, 64)):
+        with pytest.raises(ValueError, match="page_table"):
+            call()
