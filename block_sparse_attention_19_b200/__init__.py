@@ -676,10 +676,12 @@ def _check_step_q(q, Hk: int, D: int):
     return q.shape[:3]
 
 
-def _step_out(out, q, count):
-    """The output of a step: rows that no token has are zeros where the call makes it."""
+def _step_out(out, q):
+    """The output of a step: rows that no token has (a padded batch's, and all of
+    a sequence whose start is negative, also without count) are zeros where the
+    call makes it."""
     if out is None:
-        return (torch.empty_like if count is None else torch.zeros_like)(q)
+        return torch.zeros_like(q)
     _is(out, q.shape, q.dtype, "out")
     return out
 
@@ -699,16 +701,16 @@ def bsa_cache_write(k, v, cache, k_sum, page_table, start, block_size: int, coun
 def bsa_cache_read(cache, page_table, start, T: int, block_size: int, dtype: torch.dtype = torch.bfloat16, count=None,
                    k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None):
     """Keys and values [B, T, H_kv, D] of the positions start[b] + t, in dtype (or
-    k_out's). Rows t >= count[b] of k_out and v_out stay as they are; tensors
-    that the call makes hold zeros there."""
+    k_out's). Rows t >= count[b] of k_out and v_out (all rows of a sequence whose
+    start is negative) stay as they are; tensors that the call makes hold zeros
+    there."""
     pages, Hk, D = _cache_sizes(cache, block_size)
     B = page_table.shape[0] if page_table.dim() else 0
     _check_seqs(page_table, start, count, B)
-    new = torch.empty if count is None else torch.zeros
     if k_out is None:
-        k_out = new((B, T, Hk, D), device=cache.device, dtype=dtype if v_out is None else v_out.dtype)
+        k_out = torch.zeros((B, T, Hk, D), device=cache.device, dtype=dtype if v_out is None else v_out.dtype)
     if v_out is None:
-        v_out = new((B, T, Hk, D), device=cache.device, dtype=k_out.dtype)
+        v_out = torch.zeros((B, T, Hk, D), device=cache.device, dtype=k_out.dtype)
     _is(k_out, (B, T, Hk, D), k_out.dtype, "k_out")
     _is(v_out, (B, T, Hk, D), k_out.dtype, "v_out")
     _cache_call(lib.bsa_cache_read,
@@ -745,7 +747,9 @@ def bsa_cache_attn(q, cache, page_table, start, block_size: int, idx: torch.Tens
                    scale: float | None = None, count=None, workspace: torch.Tensor | None = None,
                    out: torch.Tensor | None = None) -> torch.Tensor:
     """Attention of q [B, T, H, D] (token t at position start[b] + t) over the
-    cache: over the blocks of idx [B, H_kv, topk], or all of them without."""
+    cache: over the blocks of idx [B, H_kv, topk], or all of them without. Rows
+    that no token has stay as they are in out, and are zeros where the call makes
+    the output (which out saves)."""
     pages, Hk, D = _cache_sizes(cache, block_size)
     B, T, H = _check_step_q(q, Hk, D)
     _check_seqs(page_table, start, count, B)
@@ -758,7 +762,7 @@ def bsa_cache_attn(q, cache, page_table, start, block_size: int, idx: torch.Tens
     if workspace is None and q.is_cuda:
         workspace = torch.empty(max(bsa_cache_attn_workspace_bytes(B, T, H, Hk, D), 1), device=q.device,
                                 dtype=torch.uint8)
-    o = _step_out(out, q, count)
+    o = _step_out(out, q)
     _cache_call(lib.bsa_cache_attn,
                 ((q, "q"), (cache, "cache"), (page_table, "page_table"), (start, "start"), (count, "count"), (idx, "idx"),
                  (o, "out")), B, T, H, Hk, D, block_size, pages, page_table.shape[1], topk,
@@ -795,7 +799,7 @@ def bsa_cache_forward(q, k, v, cache, k_sum, page_table, start, block_size: int,
     if workspace is None and q.is_cuda:
         workspace = torch.empty(max(bsa_cache_forward_workspace_bytes(B, T, H, Hk, D, topk), 1), device=q.device,
                                 dtype=torch.uint8)
-    o = _step_out(out, q, count)
+    o = _step_out(out, q)
     _cache_call(lib.bsa_cache_forward,
                 ((q, "q"), (k, "k"), (v, "v"), (cache, "cache"), (k_sum, "k_sum"), (page_table, "page_table"),
                  (start, "start"), (count, "count"), (o, "out")), B, T, H, Hk, D, block_size, pages, page_table.shape[1],

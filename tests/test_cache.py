@@ -676,3 +676,28 @@ def test_cache_past_32_bit_offsets(bsa):
     assert torch.equal(o, bsa.bsa_cache_attn(q, near[0], low, dev([299]), bs))
     a = bsa.bsa_cache_block_topk(q, k_sum, table, dev([299]), 1, bs)
     assert torch.equal(a, bsa.bsa_cache_block_topk(q, near[1], low, dev([299]), 1, bs))
+
+
+@pytest.mark.parametrize("count", [None, [1, 2]])
+def test_rows_without_a_token_are_zeros_where_the_call_makes_the_tensor(bsa, count):
+    """A negative start makes a sequence empty, with count or without: its rows are no leftovers of other tensors."""
+    rng = np.random.default_rng(25)
+    B, T, H, Hk, D, bs = 2, 2, 4, 2, 64, 64
+    both = Both(bsa, rng, B, 2, Hk, D, bs)
+    x, q = randn(rng, B, T, Hk, D), randn(rng, B, T, H, D)
+    start, cnt = dev([-1, 0]), None if count is None else dev(count)
+
+    def litter():
+        """Freed memory of the sizes to come, full of NaN."""
+        for n in (H, Hk, Hk):
+            torch.full((B, T, n, D), float("nan"), device="cuda", dtype=torch.bfloat16)
+
+    litter()
+    o = bsa.bsa_cache_forward(q, x, x, both.cache, both.k_sum, both.tab, start, bs, count=cnt)
+    assert not o[0].any() and bool(o[1].any())
+    litter()
+    o = bsa.bsa_cache_attn(q, both.cache, both.tab, start, bs, count=cnt)
+    assert not o[0].any() and bool(o[1].any())
+    litter()
+    k, v = bsa.bsa_cache_read(both.cache, both.tab, start, T, bs, count=cnt)
+    assert not k[0].any() and not v[0].any() and bool(k[1].any())
