@@ -739,7 +739,14 @@ def bsa_cache_block_topk(q, k_sum, page_table, start, topk: int, block_size: int
 
 
 @functools.lru_cache(maxsize=256)
+def _workspace_bytes(dev: int, fn, *sizes) -> int:
+    """What fn(*sizes) gives with the CUDA device dev current: the sizes depend on its number of SMs."""
+    with torch.cuda.device(dev):
+        return fn(*sizes)
+
+
 def bsa_cache_attn_workspace_bytes(B: int, T: int, H: int, H_kv: int, D: int) -> int:
+    """Bytes of the workspace on the current device."""
     return lib.bsa_cache_attn_workspace_bytes(B, T, H, H_kv, D)
 
 
@@ -760,8 +767,8 @@ def bsa_cache_attn(q, cache, page_table, start, block_size: int, idx: torch.Tens
         if topk < 1:  # an empty tensor's pointer is null, which the library takes for "all blocks"
             raise ValueError(f"idx has shape {tuple(idx.shape)}, topk must be positive")
     if workspace is None and q.is_cuda:
-        workspace = torch.empty(max(bsa_cache_attn_workspace_bytes(B, T, H, Hk, D), 1), device=q.device,
-                                dtype=torch.uint8)
+        workspace = torch.empty(max(_workspace_bytes(q.get_device(), lib.bsa_cache_attn_workspace_bytes, B, T, H, Hk, D), 1),
+                                device=q.device, dtype=torch.uint8)
     o = _step_out(out, q)
     _cache_call(lib.bsa_cache_attn,
                 ((q, "q"), (cache, "cache"), (page_table, "page_table"), (start, "start"), (count, "count"), (idx, "idx"),
@@ -779,8 +786,8 @@ def _room(workspace, q):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-@functools.lru_cache(maxsize=256)
 def bsa_cache_forward_workspace_bytes(B: int, T: int, H: int, H_kv: int, D: int, topk: int) -> int:
+    """Bytes of the workspace on the current device."""
     return lib.bsa_cache_forward_workspace_bytes(B, T, H, H_kv, D, topk)
 
 
@@ -797,8 +804,9 @@ def bsa_cache_forward(q, k, v, cache, k_sum, page_table, start, block_size: int,
     _is(k_sum, (pages, Hk, D), torch.float32, "k_sum")
     _check_seqs(page_table, start, count, B)
     if workspace is None and q.is_cuda:
-        workspace = torch.empty(max(bsa_cache_forward_workspace_bytes(B, T, H, Hk, D, topk), 1), device=q.device,
-                                dtype=torch.uint8)
+        workspace = torch.empty(
+            max(_workspace_bytes(q.get_device(), lib.bsa_cache_forward_workspace_bytes, B, T, H, Hk, D, topk), 1),
+            device=q.device, dtype=torch.uint8)
     o = _step_out(out, q)
     _cache_call(lib.bsa_cache_forward,
                 ((q, "q"), (k, "k"), (v, "v"), (cache, "cache"), (k_sum, "k_sum"), (page_table, "page_table"),

@@ -485,7 +485,8 @@ bsa_status bsa_cache_block_topk(const void* q, const float* k_sum, const int32_t
                                 int block_size, int num_pages, int max_blocks, int topk, bsa_dtype dt,
                                 unsigned flags, void* stream);
 
-/* Workspace bytes of bsa_cache_attn; 0 if the arguments are invalid. */
+/* Workspace bytes of bsa_cache_attn on the current device (the size follows its
+ * number of SMs); 0 if the arguments are invalid. */
 size_t bsa_cache_attn_workspace_bytes(int B, int T, int H, int H_kv, int D);
 
 /* Attention over the cache: the query of token t sees the tokens at positions
@@ -510,8 +511,8 @@ bsa_status bsa_cache_attn(const void* q, const void* cache, const int32_t* page_
                           void* workspace, size_t workspace_bytes, void* stream);
 
 /* Workspace bytes of bsa_cache_forward: the index list [B, H_kv, topk] and the
- * attention's workspace, each section 256-byte aligned; 0 if the arguments are
- * invalid. */
+ * attention's workspace (on the current device), each section 256-byte aligned;
+ * 0 if the arguments are invalid. */
 size_t bsa_cache_forward_workspace_bytes(int B, int T, int H, int H_kv, int D, int topk);
 
 /* One step of generation: bsa_cache_write of k and v, bsa_cache_block_topk

@@ -172,3 +172,37 @@ def test_binding_refuses_page_tables_of_other_dimensions(bsa, shape):
                  lambda: bsa.bsa_cache_forward(x, x, x, cache, k_sum, table, start, 64)):
         with pytest.raises(ValueError, match="page_table"):
             call()
+
+
+def test_workspace_sizes_belong_to_a_device(bsa, monkeypatch):
+    """A size that was asked for on one device is not given for another with more SMs."""
+    sms, current = {0: 100, 1: 148}, [0]
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.dev
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    class Lib:
+        @staticmethod
+        def bsa_cache_attn_workspace_bytes(*sizes):
+            return sms[current[0]] * sum(sizes)
+
+        @staticmethod
+        def bsa_cache_forward_workspace_bytes(*sizes):
+            return sms[current[0]] * sum(sizes) + 1
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(bsa, "lib", Lib)
+    for dev in (0, 1, 0):
+        current[0] = dev
+        assert bsa.bsa_cache_attn_workspace_bytes(1, 1, 4, 2, 64) == 72 * sms[dev]
+        assert bsa.bsa_cache_forward_workspace_bytes(1, 1, 4, 2, 64, 3) == 75 * sms[dev] + 1
+    current[0] = 0
+    for dev in (0, 1, 0):  # what the calls allocate: the tensors' device counts, not the current one
+        assert bsa._workspace_bytes(dev, Lib.bsa_cache_attn_workspace_bytes, 1, 1, 4, 2, 64) == 72 * sms[dev]
