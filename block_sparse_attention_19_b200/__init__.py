@@ -739,10 +739,10 @@ def bsa_cache_block_topk(q, k_sum, page_table, start, topk: int, block_size: int
 
 
 @functools.lru_cache(maxsize=256)
-def _workspace_bytes(dev: int, fn, *sizes) -> int:
-    """What fn(*sizes) gives with the CUDA device dev current: the sizes depend on its number of SMs."""
+def _workspace_bytes(dev: int, name: str, *sizes) -> int:
+    """What the library's function gives with the CUDA device dev current: it depends on its number of SMs."""
     with torch.cuda.device(dev):
-        return fn(*sizes)
+        return getattr(lib, name)(*sizes)
 
 
 def bsa_cache_attn_workspace_bytes(B: int, T: int, H: int, H_kv: int, D: int) -> int:
@@ -767,7 +767,7 @@ def bsa_cache_attn(q, cache, page_table, start, block_size: int, idx: torch.Tens
         if topk < 1:  # an empty tensor's pointer is null, which the library takes for "all blocks"
             raise ValueError(f"idx has shape {tuple(idx.shape)}, topk must be positive")
     if workspace is None and q.is_cuda:
-        workspace = torch.empty(max(_workspace_bytes(q.get_device(), lib.bsa_cache_attn_workspace_bytes, B, T, H, Hk, D), 1),
+        workspace = torch.empty(max(_workspace_bytes(q.get_device(), "bsa_cache_attn_workspace_bytes", B, T, H, Hk, D), 1),
                                 device=q.device, dtype=torch.uint8)
     o = _step_out(out, q)
     _cache_call(lib.bsa_cache_attn,
@@ -805,7 +805,7 @@ def bsa_cache_forward(q, k, v, cache, k_sum, page_table, start, block_size: int,
     _check_seqs(page_table, start, count, B)
     if workspace is None and q.is_cuda:
         workspace = torch.empty(
-            max(_workspace_bytes(q.get_device(), lib.bsa_cache_forward_workspace_bytes, B, T, H, Hk, D, topk), 1),
+            max(_workspace_bytes(q.get_device(), "bsa_cache_forward_workspace_bytes", B, T, H, Hk, D, topk), 1),
             device=q.device, dtype=torch.uint8)
     o = _step_out(out, q)
     _cache_call(lib.bsa_cache_forward,

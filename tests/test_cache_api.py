@@ -198,6 +198,9 @@ def test_workspace_sizes_belong_to_a_device(bsa, monkeypatch):
             return sms[current[0]] * sum(sizes) + 1
 
     monkeypatch.setattr(torch.cuda, "device", Device)
+    for name, sizes in (("bsa_cache_attn_workspace_bytes", (2, 1, 4, 2, 64)),
+                        ("bsa_cache_forward_workspace_bytes", (2, 1, 4, 2, 64, 3))):
+        assert bsa._workspace_bytes(0, name, *sizes) == getattr(bsa, name)(*sizes) > 0
     monkeypatch.setattr(bsa, "lib", Lib)
     for dev in (0, 1, 0):
         current[0] = dev
@@ -205,4 +208,4 @@ def test_workspace_sizes_belong_to_a_device(bsa, monkeypatch):
         assert bsa.bsa_cache_forward_workspace_bytes(1, 1, 4, 2, 64, 3) == 75 * sms[dev] + 1
     current[0] = 0
     for dev in (0, 1, 0):  # what the calls allocate: the tensors' device counts, not the current one
-        assert bsa._workspace_bytes(dev, Lib.bsa_cache_attn_workspace_bytes, 1, 1, 4, 2, 64) == 72 * sms[dev]
+        assert bsa._workspace_bytes(dev, "bsa_cache_attn_workspace_bytes", 1, 1, 4, 2, 64) == 72 * sms[dev]
