@@ -487,8 +487,9 @@ __global__ void __launch_bounds__(128) cache_read_kernel(const uint8_t* __restri
 // blocks are kept does not depend on an order of summation.
 constexpr int kCacheSelThreads = 256, kCacheSelWarps = kCacheSelThreads / 32;
 
+constexpr uint32_t kForcedKey = 0xffffffffu;  // a forced block ranks above every score, a NaN among the scores first
 __device__ __forceinline__ uint32_t cache_score_key(float x) {
-  if (x != x) return 0xffffffffu;  // a NaN ranks first
+  if (x != x) return kForcedKey - 1;
   const uint32_t u = __float_as_uint(x + 0.0f);  // -0 as +0
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
@@ -605,7 +606,7 @@ __global__ void __launch_bounds__(kCacheSelThreads) cache_topk_kernel(const T* _
           const int tokens = total - j * s.bs;
           // a full block's size is a power of two: the product with its inverse is exact
           key = cache_score_key(static_cast<float>(tokens >= s.bs ? dot * inv_bs : dot / tokens));
-          if (force && (j + 1) * s.bs > start) key = 0xffffffffu;
+          if (force && (j + 1) * s.bs > start) key = kForcedKey;
         }
         store_cluster(to + 4u * j, key);
       }

@@ -106,7 +106,8 @@ def read(cache, table, start, T, count=None, k_out=None, v_out=None):
 
 def block_topk(q, k_sum, table, start, topk, bs, count=None, force_diag=False):
     """idx [B, H_kv, topk], and the scores of the present blocks (float64 rounded
-    to float32) as lists of dicts [b][h]."""
+    to float32) as lists of dicts [b][h]. The order: forced blocks, NaN scores,
+    scores from the largest on; the lower block first where these are equal."""
     B, T, H, D = q.shape
     pages, Hk = k_sum.shape[:2]
     idx = np.full((B, Hk, topk), -1, np.int32)
@@ -117,14 +118,15 @@ def block_topk(q, k_sum, table, start, topk, bs, count=None, force_diag=False):
         scores.append([])
         for h in range(Hk):
             qs = q[b, :n, h * (H // Hk):(h + 1) * (H // Hk)].sum((0, 1))
-            sc = {}
+            sc, forced = {}, set()
             for j in range(-(-total // bs)):
                 p = _page(table, pages, b, j)
                 if p >= 0:
                     sc[j] = np.float32((qs @ k_sum[p, h]) / min(bs, total - j * bs))
                     if force_diag and (j + 1) * bs > s:
-                        sc[j] = np.float32(np.inf)
-            best = sorted(sc, key=lambda j: (-sc[j], j))[:topk]
+                        forced.add(j)
+            rank = {j: (0, 0.0, j) if j in forced else (1, 0.0, j) if np.isnan(x) else (2, -x, j) for j, x in sc.items()}
+            best = sorted(sc, key=rank.get)[:topk]
             idx[b, h, :len(best)] = sorted(best)
             scores[b].append(sc)
     return idx, scores

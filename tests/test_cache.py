@@ -701,3 +701,20 @@ def test_rows_without_a_token_are_zeros_where_the_call_makes_the_tensor(bsa, cou
     litter()
     k, v = bsa.bsa_cache_read(both.cache, both.tab, start, T, bs, count=cnt)
     assert not k[0].any() and not v[0].any() and bool(k[1].any())
+
+
+@pytest.mark.parametrize("P", [12, 300])
+def test_block_topk_forced_blocks_rank_above_scores_that_are_not_finite(bsa, P):
+    """Older blocks with NaN or infinite sums do not push out the blocks of the new tokens."""
+    Hk, D, bs, T = 2, 64, 64, 3
+    k_sum = torch.randn(P, Hk, D, device="cuda", generator=torch.Generator(device="cuda").manual_seed(7))
+    k_sum[1:8:2], k_sum[2], k_sum[6] = float("nan"), float("inf"), -float("inf")
+    table, start = np.arange(P)[None], np.array([(P - 1) * bs - 1])  # new tokens in the last two blocks
+    q = torch.ones(1, T, Hk, D, device="cuda")
+    for topk in (1, 2, 3, 6, 7, P - 1, P):
+        for flags in (0, bsa.BSA_FLAG_CAUSAL | bsa.BSA_FLAG_FORCE_DIAG):
+            with np.errstate(invalid="ignore"):
+                want, _ = C.block_topk(host(q), host(k_sum), table, start, topk, bs, force_diag=bool(flags))
+            got = bsa.bsa_cache_block_topk(q, k_sum, dev(table), dev(start), topk, bs, flags=flags)
+            assert np.array_equal(got.cpu().numpy(), want), (topk, flags)
+            assert not flags or set(range(P - 2, P)[:topk]) <= set(got[0, 0].tolist())

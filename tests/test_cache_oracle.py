@@ -106,3 +106,15 @@ def test_block_topk_against_numpy():
     assert idx[1].tolist() == [[0, -1, -1, -1]] * 2  # 43 tokens: one block
     forced, _ = C.block_topk(q, k_sum, table, np.array([510, 40]), 2, bs, force_diag=True)
     assert forced[0].tolist() == [[7, 8]] * 2  # tokens 510..512 lie in blocks 7 and 8
+
+
+def test_block_topk_order_of_forced_and_special_scores():
+    """Forced blocks, then NaN, then +inf, then the rest; equal ones by their number."""
+    k_sum = np.ones((8, 1, 64))
+    k_sum[1], k_sum[3], k_sum[4], k_sum[6] = np.inf, np.nan, np.nan, -np.inf
+    table, q = np.arange(8)[None], np.ones((1, 1, 1, 64))
+    for topk, plain, forced in ((1, [3], [7]), (2, [3, 4], [3, 7]), (3, [1, 3, 4], [3, 4, 7]), (4, [0, 1, 3, 4], [1, 3, 4, 7]),
+                                (7, [0, 1, 2, 3, 4, 5, 7], [0, 1, 2, 3, 4, 5, 7])):
+        for force, want in ((False, plain), (True, forced)):
+            idx, _ = C.block_topk(q, k_sum, table, np.array([511]), topk, 64, force_diag=force)
+            assert idx.tolist() == [[want]], (topk, force)
