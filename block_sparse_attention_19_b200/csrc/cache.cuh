@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kCacheSelThreads) cache_topk_kernel(const T* _
           const int tokens = total - j * s.bs;
           // a full block's size is a power of two: the product with its inverse is exact
           key = cache_score_key(static_cast<float>(tokens >= s.bs ? dot * inv_bs : dot / tokens));
-          if (force && (j + 1) * s.bs > start) key = kForcedKey;
+          if (force && count > 0 && (j + 1) * s.bs > start) key = kForcedKey;
         }
         store_cluster(to + 4u * j, key);
       }

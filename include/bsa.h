@@ -479,8 +479,9 @@ bsa_status bsa_cache_read(const void* cache, const int32_t* page_table, const in
  * lower j (-0 ties with +0, NaN ranks first), ascending, padded with -1.
  * flags: 0 or BSA_FLAG_CAUSAL (the cache is causal: no effect), and
  * BSA_FLAG_CAUSAL | BSA_FLAG_FORCE_DIAG ranks the blocks that hold the step's
- * new tokens above all others, NaN scores included (the lower block first where
- * topk holds not all of them). max_blocks <= 49152. One launch. */
+ * new tokens (none where count[b] is 0) above all others, NaN scores included
+ * (the lower block first where topk holds not all of them). max_blocks <=
+ * 49152. One launch. */
 bsa_status bsa_cache_block_topk(const void* q, const float* k_sum, const int32_t* page_table, const int32_t* start,
                                 const int32_t* count, int32_t* idx, int B, int T, int H, int H_kv, int D,
                                 int block_size, int num_pages, int max_blocks, int topk, bsa_dtype dt,

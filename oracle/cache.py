@@ -123,7 +123,7 @@ def block_topk(q, k_sum, table, start, topk, bs, count=None, force_diag=False):
                 p = _page(table, pages, b, j)
                 if p >= 0:
                     sc[j] = np.float32((qs @ k_sum[p, h]) / min(bs, total - j * bs))
-                    if force_diag and (j + 1) * bs > s:
+                    if force_diag and n and (j + 1) * bs > s:
                         forced.add(j)
             rank = {j: (0, 0.0, j) if j in forced else (1, 0.0, j) if np.isnan(x) else (2, -x, j) for j, x in sc.items()}
             best = sorted(sc, key=rank.get)[:topk]

@@ -718,3 +718,16 @@ def test_block_topk_forced_blocks_rank_above_scores_that_are_not_finite(bsa, P):
             got = bsa.bsa_cache_block_topk(q, k_sum, dev(table), dev(start), topk, bs, flags=flags)
             assert np.array_equal(got.cpu().numpy(), want), (topk, flags)
             assert not flags or set(range(P - 2, P)[:topk]) <= set(got[0, 0].tolist())
+
+
+@pytest.mark.parametrize("P", [4, 400])
+def test_block_topk_forces_nothing_without_new_tokens(bsa, P):
+    Hk, D, bs, B = 2, 64, 64, 3
+    k_sum = torch.ones(B * P, Hk, D, device="cuda")
+    table, q = np.arange(B * P).reshape(B, P), torch.ones(B, 2, Hk, D, device="cuda")
+    start, count = np.array([(P - 1) * bs + 8, (P - 1) * bs, (P - 1) * bs + 8]), np.array([0, 0, 2])
+    want, _ = C.block_topk(host(q), host(k_sum), table, start, 2, bs, count, force_diag=True)
+    got = bsa.bsa_cache_block_topk(q, k_sum, dev(table), dev(start), 2, bs, count=dev(count),
+                                   flags=bsa.BSA_FLAG_CAUSAL | bsa.BSA_FLAG_FORCE_DIAG)
+    assert np.array_equal(got.cpu().numpy(), want)
+    assert got[0].tolist() == [[0, 1]] * Hk and got[2].tolist() == [[0, P - 1]] * Hk

@@ -118,3 +118,10 @@ def test_block_topk_order_of_forced_and_special_scores():
         for force, want in ((False, plain), (True, forced)):
             idx, _ = C.block_topk(q, k_sum, table, np.array([511]), topk, 64, force_diag=force)
             assert idx.tolist() == [[want]], (topk, force)
+
+
+def test_block_topk_forces_nothing_without_new_tokens():
+    """A sequence of a padded batch that brings no token has scores of 0 throughout: its first blocks."""
+    table, q = np.arange(4)[None], np.ones((1, 1, 1, 64))
+    idx, _ = C.block_topk(q, np.ones((4, 1, 64)), table, np.array([200]), 2, 64, np.array([0]), force_diag=True)
+    assert idx.tolist() == [[[0, 1]]]
