@@ -1501,7 +1501,9 @@ bsa_status bsa_cache_attn(const void* q, const void* cache, const int32_t* page_
   bsa_status s;
   if ((s = check_cache(B, T, H, H_kv, D, block_size, num_pages, max_blocks, dt)) != BSA_OK) return s;
   if (idx && topk < 1) return fail(BSA_ERR_INVALID_ARG, "topk=%d must be positive", topk);
-  if (!std::isfinite(scale) || scale <= 0.0f) return fail(BSA_ERR_INVALID_ARG, "scale must be positive and finite");
+  const float sl = scale * 1.4426950408889634f;  // scores are exponents of 2
+  if (!std::isfinite(sl) || scale <= 0.0f)
+    return fail(BSA_ERR_INVALID_ARG, "scale=%g must be positive, and scale log2(e) within float32", scale);
   if ((s = check_attn_tiles(B, T, H, H_kv, block_size, max_blocks, idx ? topk : 0)) != BSA_OK) return s;
   if ((s = check_tensors({q, cache, o})) != BSA_OK) return s;
   if (o == q) return fail(BSA_ERR_INVALID_ARG, "o must not alias q");
@@ -1514,7 +1516,6 @@ bsa_status bsa_cache_attn(const void* q, const void* cache, const int32_t* page_
   const cudaError_t e = by_type(dt, D, [&](auto t, auto d) {
     using E = decltype(t);
     constexpr int kD = decltype(d)::value;
-    const float sl = scale * 1.4426950408889634f;
     const auto run = [&](auto launch) {
       return launch(q, cache, idx, o, workspace, seqs, B, H, H_kv, topk, sl, stream);
     };

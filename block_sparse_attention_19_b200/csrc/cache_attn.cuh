@@ -147,10 +147,12 @@ __device__ __forceinline__ uint32_t pack_f16_rest(float lo, float hi, uint32_t p
 }
 
 // 2^e scale_log2, what a row's products with codes are multiplied by. A row with an element of 2^117 or more, an
-// infinity too, has NaN instead: 2^e does not hold its scale any more, and its scores would be wrong, not infinite.
+// infinity too, has NaN instead: 2^e does not hold its scale any more, and its scores would be wrong, not infinite. So
+// has one for which that factor, or the sum of its channels times scale_log2 (up to 2^7 amax scale_log2), leaves
+// float32 with a large scale: products below zero would all be -inf, and a row that sees tokens would read as zeros.
 __device__ __forceinline__ float score_factor(float amax, int e, float scale_log2) {
   const float f = __uint_as_float(static_cast<uint32_t>(min(e, 127) + 127) << 23) * scale_log2;
-  return amax < 0x1p117f ? f : CUDART_NAN_F;
+  return amax < 0x1p117f && f < CUDART_INF_F && amax * scale_log2 < 0x1p120f ? f : CUDART_NAN_F;
 }
 
 // How the tiles of all units are laid in one line and cut into equal pieces, one

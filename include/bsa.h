@@ -506,7 +506,9 @@ size_t bsa_cache_attn_workspace_bytes(int B, int T, int H, int H_kv, int D);
  * memory of bsa_cache_attn_workspace_bytes() bytes, 16-byte aligned, not used
  * by an overlapping call. B <= 4096. Deterministic. A query row with a NaN, an
  * infinity or an element of 2^117 or more in size gives NaN (zeros where it
- * sees no token). */
+ * sees no token); with a scale above 1/2 so may one with an element of
+ * 2^116 / scale or more. scale: positive, times log2(e) within float32. A score
+ * beyond float32 counts as the infinity of its sign. */
 bsa_status bsa_cache_attn(const void* q, const void* cache, const int32_t* page_table, const int32_t* start,
                           const int32_t* count, const int32_t* idx, void* o, int B, int T, int H, int H_kv, int D,
                           int block_size, int num_pages, int max_blocks, int topk, float scale, bsa_dtype dt,

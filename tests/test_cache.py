@@ -731,3 +731,23 @@ def test_block_topk_forces_nothing_without_new_tokens(bsa, P):
                                    flags=bsa.BSA_FLAG_CAUSAL | bsa.BSA_FLAG_FORCE_DIAG)
     assert np.array_equal(got.cpu().numpy(), want)
     assert got[0].tolist() == [[0, 1]] * Hk and got[2].tolist() == [[0, P - 1]] * Hk
+
+
+@pytest.mark.parametrize("dtype,G,T", FORMS, ids=lambda x: str(x))
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_large_queries_times_a_large_scale(bsa, D, dtype, G, T):
+    """A row whose element times scale leaves what a score can be made of gives NaN, never the zeros of a row that sees
+    nothing, however its scores' signs fall; half the rows are ordinary ones and know nothing of it."""
+    rng = np.random.default_rng(26)
+    Hk, n, scale = 2, 150, 2.0 ** 12
+    both = Both(bsa, rng, 1, 3, Hk, D, 64)
+    k, v = randn(rng, 1, n, Hk, D, offset=-8.0), randn(rng, 1, n, Hk, D)
+    both.write(k, v, np.array([0]))
+    q = randn(rng, 1, T, Hk * G, D, dtype=dtype, scale=2.0 ** -14)
+    start, bad = np.array([n - T]), np.zeros((1, T, Hk * G), bool)
+    q[0, T - 1, :G] = 2.0 ** 112  # (times 2^12 log2(e) beyond 2^120)
+    bad[0, T - 1, :G] = True
+    o = bsa.bsa_cache_attn(q, both.cache, both.tab, dev(start), 64, scale=scale)
+    assert torch.isnan(o[torch.as_tensor(bad, device="cuda")]).all()
+    ref, size, logit = C.attn(both.ref, np.where(bad[..., None], 0, host(q)), both.table, start, scale=scale)
+    check_attn(torch.nan_to_num(o), ref, size, logit, n, D, dtype, ~bad)

@@ -209,3 +209,8 @@ def test_workspace_sizes_belong_to_a_device(bsa, monkeypatch):
     current[0] = 0
     for dev in (0, 1, 0):  # what the calls allocate: the tensors' device counts, not the current one
         assert bsa._workspace_bytes(dev, "bsa_cache_attn_workspace_bytes", 1, 1, 4, 2, 64) == 72 * sms[dev]
+
+
+@pytest.mark.parametrize("scale,status", [(3e38, 1), (-0.125, 1)])
+def test_attention_refuses_scales_that_leave_float32(bsa, scale, status):
+    assert _attn(bsa, scale=scale) == status
