@@ -23,8 +23,9 @@
 // of both signs stay near the result's own size, and the matrix unit's truncating
 // sums cost them nothing (with code, 1e-4 of the result at 6000 tokens).
 // All of these operands are exact. For float16's range each query row is
-// scaled by a power of two, and the reference M of a row keeps 2^(x - M) v_scale
-// below 2^15.
+// scaled by a power of two, and so are a row's weights of each group of 64 value
+// channels: 2^(x - M) v_scale 2^e is kept below 2^15, with M near the row's largest
+// score and e near 8 - log2 of the group's largest 2^(x - M) v_scale.
 //
 // All units' tiles lie in one line, cut into equal pieces for CTAs that are all
 // resident at once; a unit that several CTAs share leaves one part for each, which a
@@ -46,12 +47,33 @@ constexpr int kCaWarps = 4;  // in two pairs: a tile goes to a pair, 32 tokens t
 constexpr int kCaThreads = kCaWarps * 32;
 constexpr int kCaMaxExtra = 6;  // (see CaPlan)
 constexpr int kCaMaxSeqs = 4096;  // sequences whose plan fits in shared memory
-// Where a raised reference puts log2 of the largest weight times scale. Later ones may reach 2^15 before the next raise,
-// and a raise weighs a tile twice: from 8 on 2^7 times the largest so far is left, with scores of deviation 2 most rows'
-// last raise (many rows: 33.2 us, 36.2 from 12 on). What float16's smallest number costs is 2^-33 of the largest, below the
-// float32 sums' rounding. float32 queries keep the finer 12.
+// A row's reference M is at least its largest score of the time when it was last raised, and a group's factor 2^e
+// puts the largest weight times scale of that time between 2^kCaRaise and 2^(kCaRaise + 1). Later ones may reach 2^15
+// before the next raise, and a raise weighs a tile twice: from 8 on at least 2^6 times the largest so far is left, with
+// scores of deviation 2 most rows' last raise (many rows: 33.2 us, 36.2 from 12 on). A weight times scale is off by
+// half of float16's smallest number at most, 2^-33 of the group's largest; for float32 queries 2^-37.
+// Each group has a factor of its own, so that small scales beside large ones keep their accuracy, and M leaves the
+// scales out, so that the sums of weights, and of weights times zeros, stay near one however small the scales are.
 template <typename T>
 constexpr float kCaRaise = sizeof(T) == 4 ? 12.0f : 8.0f;
+constexpr float kCaMaxSum = 0x1p40f;      // a thread's sum of weights beyond it raises M
+constexpr float kCaFirstFactor = 0x1p126f;  // 2^e of a group without a scale: the first one overflows and lowers it
+
+// A raise of the reference from `old` to `now` at which the group's largest log2(weight times scale) + `now` is `most`:
+// changes the factor, and returns what the group's sums are to be multiplied by (f = 2^(old - now)).
+template <typename T>
+__device__ __forceinline__ float lower_factor(float& factor, float old, float now, float f, float most) {
+  const float e = static_cast<float>(static_cast<int>(__float_as_uint(factor) >> 23) - 127);
+  // never above what the sums so far had (fminf and fmaxf drop a NaN, which comes of infinite scores)
+  const float to = fmaxf(fminf(ceilf(fminf(kCaRaise<T> - (most - now), e + (now - old))), 126.0f), -126.0f);
+  factor = __uint_as_float(static_cast<uint32_t>(static_cast<int>(to) + 127) << 23);
+  const float by = fmaxf(fminf(to - e, 126.0f), -126.0f);
+  return f * __uint_as_float(static_cast<uint32_t>(static_cast<int>(by) + 127) << 23);
+}
+// 1 / factor of a power of two between 2^-126 and 2^126.
+__device__ __forceinline__ float factor_inverse(float factor) {
+  return __uint_as_float((254u << 23) - __float_as_uint(factor));
+}
 constexpr float kCaNone = -0x1.fffffep127f;  // reference of a row that has seen nothing: no finite score is below it
 
 // How many query rows a unit has and how they fill the products' eight columns: each once, or (FOLD = 2, up to four
@@ -459,12 +481,12 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
     }
     low_limit = start + row0 / G + 1;
 
-    float m[2], l[2], z[2][kGroups], acc[kWords][2][4];
+    float m[2], l[2], z[2][kGroups], factor[2][kGroups], acc[kWords][2][4];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       m[c] = kCaNone, l[c] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < kGroups; ++j) z[c][j] = 0.0f;
+      for (int j = 0; j < kGroups; ++j) z[c][j] = 0.0f, factor[c][j] = kCaFirstFactor;
     }
 #pragma unroll
     for (int w = 0; w < kWords; ++w)
@@ -539,8 +561,8 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
             xs[u][at] = v;
           }
         }
-      // weights against the references as they stand, times the values' scales, in float16; what a row does not
-      // see must not count, not even as 0 * NaN
+      // weights against the references as they stand, times the groups' factors and the values' scales, in float16;
+      // what a row does not see must not count, not even as 0 * NaN
       float p[kSoft][4], sum[2];
       uint32_t w16[kSoft][kGroups][2], high = 0;
       auto weigh = [&]() {
@@ -561,7 +583,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
               float w[2];
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                w[c] = p[e][2 * i + c] * vs;
+                w[c] = p[e][2 * i + c] * factor[c][j] * vs;
                 if (kEdge && pos + r0 + 16 * (e + half) + 8 * i + g >= limit[c]) w[c] = 0.0f;
               }
               w16[e][j][i] = pack_f16(w[0], w[1]);
@@ -571,33 +593,36 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
       };
       weigh();
       const float most = fmaxf(sum[0], sum[1]);
-      // Is a weight times scale at 2^15 or above (0x7800), or a sum of weights beyond 2^90 (scales near zero)?
-      // Scales are not negative, so the codes of the float16 halves rank as they do.
-      if (__any_sync(0xffffffffu, max_u16x2(high, 0x78007800u) != 0x78007800u || most > 0x1p90f)) {
-        // raise the references so that the largest weight times scale is 2^kCaRaise
+      // Is one at 2^15 or above (0x7800; an infinite weight times 0 is a NaN and above it too), or a sum of weights
+      // beyond kCaMaxSum? Scales are not negative, so the codes of the float16 halves rank as they do.
+      if (__any_sync(0xffffffffu, max_u16x2(high, 0x78007800u) != 0x78007800u || most > kCaMaxSum)) {
+        // raise the references to the largest scores, so that no weight is above 1, and lower the factors
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float u = -CUDART_INF_F;
+          float u[1 + kGroups];  // the largest score, and with log2 of the value's scale
 #pragma unroll
-          for (int e = 0; e < kSoft; ++e)
+          for (int j = 0; j < 1 + kGroups; ++j) {
+            u[j] = -CUDART_INF_F;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float vmax = 0x1p-48f;
+            for (int e = 0; e < kSoft; ++e)
 #pragma unroll
-              for (int j = 0; j < kGroups; ++j) vmax = fmaxf(vmax, __uint_as_float(vsz[e][i][j] << 16));
-              u = fmaxf(u, xs[e][2 * i + c] + __log2f(vmax));
-            }
+              for (int i = 0; i < 2; ++i)
+                u[j] = fmaxf(u[j], xs[e][2 * i + c] + (j ? __log2f(__uint_as_float(vsz[e][i][j - 1 + !j] << 16)) : 0.0f));
 #pragma unroll
-          for (int d = 4; d < 32; d *= 2) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, d));
-          const float now = fmaxf(m[c], u - kCaRaise<T>), f = fast_exp2(m[c] - now);
+            for (int d = 4; d < 32; d *= 2) u[j] = fmaxf(u[j], __shfl_xor_sync(0xffffffffu, u[j], d));
+          }
+          const float old = m[c], now = fmaxf(old, u[0]), f = fast_exp2(old - now);
           m[c] = now;
           l[c] *= f;
 #pragma unroll
-          for (int j = 0; j < kGroups; ++j) z[c][j] *= f;
+          for (int j = 0; j < kGroups; ++j) {
+            z[c][j] *= f;
+            const float by = lower_factor<T>(factor[c][j], old, now, f, u[1 + j]);
 #pragma unroll
-          for (int w = 0; w < kWords; ++w)
+            for (int w = 2 * j; w < 2 * j + 2; ++w)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) acc[w][k][c] *= f, acc[w][k][2 + c] *= f;
+              for (int k = 0; k < 2; ++k) acc[w][k][c] *= by, acc[w][k][2 + c] *= by;
+          }
         }
         weigh();
       }
@@ -617,7 +642,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const bool seen = !kEdge || pos + r0 + 16 * (e + half) + 8 * i + g < limit[c];
-              w[c] = seen ? p[e][2 * i + c] * vs : 0.0f;
+              w[c] = seen ? p[e][2 * i + c] * factor[c][j] * vs : 0.0f;
               if (seen) z[c][j] = fmaf(p[e][2 * i + c], vz, z[c][j]);
             }
             if constexpr (kSplit == 2)
@@ -665,11 +690,12 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
     float aside_m[2];
     bool aside = false;
     auto sums_of = [&](int c, int w, float f, float zero) {
-      const float f0 = kCentre ? f : f * 0x1p24f, f1 = kCentre ? f : f * 0x1p20f;
+      constexpr float kLo = kCentre ? 1.0f : 0x1p24f, kHi = kCentre ? 1.0f : 0x1p20f;
+      const float back = factor_inverse(factor[c][w / 2]);
       float hi[2] = {acc[w][0][2 + c], acc[w][1][2 + c]};
       if constexpr (!kCentre) hi[0] -= acc[w][0][c], hi[1] -= acc[w][1][c];
-      return make_float4(fmaf(acc[w][0][c], f0, zero), fmaf(hi[0], f1, zero), fmaf(acc[w][1][c], f0, zero),
-                         fmaf(hi[1], f1, zero));
+      return make_float4(fmaf(acc[w][0][c] * kLo * back, f, zero), fmaf(hi[0] * kHi * back, f, zero),
+                         fmaf(acc[w][1][c] * kLo * back, f, zero), fmaf(hi[1] * kHi * back, f, zero));
     };
     // the sums so far at reference m + log2(1 / f), with `zero` for each channel
     auto put_aside = [&](int c, float f, float old, const float (&zero)[kGroups]) {
@@ -857,9 +883,9 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
   __shared__ uint64_t full[kStages];
   __shared__ int tile_pos[kStages], next_pos[32];
   __shared__ const uint8_t* next_src[32];
-  __shared__ __align__(16) float s_mul[kRows], s_qsum[kGroups][kRows], s_m[kRows];
+  __shared__ __align__(16) float s_mul[kRows], s_qsum[kGroups][kRows], s_m[kRows], s_factor[kGroups][kRows];
   __shared__ __align__(16) int s_limit[kRows];
-  __shared__ float s_cand[kCaWarps][kRows], s_l[kCaWarps][kRows], s_z[kCaWarps][kGroups][kRows];
+  __shared__ float s_cand[1 + kGroups][kCaWarps][kRows], s_l[kCaWarps][kRows], s_z[kCaWarps][kGroups][kRows];
   __shared__ int s_flag[kCaWarps], abort_flag;
   pdl_launch_dependents();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, G = H / Hkv, g = lane / 4, t4 = lane % 4;
@@ -957,7 +983,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
       if (t4 == 0) {
         s_mul[r] = score_factor(amax, 24 - up, scale_log2);
 #pragma unroll
-        for (int j = 0; j < kGroups; ++j) s_qsum[j][r] = sum[j] * scale_log2;
+        for (int j = 0; j < kGroups; ++j) s_qsum[j][r] = sum[j] * scale_log2, s_factor[j][r] = kCaFirstFactor;
         s_limit[r] = r < rows ? start + row / G + 1 : 0;
         s_m[r] = kCaNone;
       }
@@ -1051,10 +1077,12 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
             }
           }
       };
-      // weights against the references as they stand, times the values' scales, in float16, to shared memory. True
-      // where one times its token's larger scale is above 2^15, or one is beyond 2^90 (scales near zero).
+      // weights against the references as they stand, times the groups' factors and the values' scales, in float16, to
+      // shared memory. True where one is at 2^15 or above (or a NaN, see the other kernel), or a weight beyond
+      // kCaMaxSum.
       auto weigh = [&](auto masked) -> bool {
-        float most[2] = {0.0f, 0.0f};
+        float most = 0.0f;
+        uint32_t high = 0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
           {
@@ -1066,18 +1094,19 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
               float lo, hi;
               f2_split(f2_sub(xs[nt][i], ref), lo, hi);
               lo = fast_exp2(lo), hi = fast_exp2(hi);
-              most[i] = fmax3(most[i], lo, hi);
+              most = fmax3(most, lo, hi);
               p[nt][i] = f2(lo, hi);
 #pragma unroll
               for (int j = 0; j < kGroups; ++j) {
                 float wl, wh;
-                f2_split(f2_mul(p[nt][i], vs[j][i]), wl, wh);
+                f2_split(f2_mul(f2_mul(p[nt][i], load_f2(s_factor[j] + col)), vs[j][i]), wl, wh);
                 if constexpr (decltype(masked)::value) {
                   const int2 lim = *reinterpret_cast<const int2*>(s_limit + col);
                   if (p0 + 8 * i >= lim.x) wl = 0.0f;
                   if (p0 + 8 * i >= lim.y) wh = 0.0f;
                 }
                 w16[j][i] = pack_f16(wl, wh);
+                high = max_u16x2(high, w16[j][i]);
               }
             }
 #pragma unroll
@@ -1085,14 +1114,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
               reinterpret_cast<uint2*>(sp)[(((buf * kGroups + j) * 4 + warp) * NT + nt) * 32 + lane] =
                   make_uint2(transpose8x8(w16[j][0]), transpose8x8(w16[j][1]));
           }
-        bool over = false;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float vmax = __uint_as_float(vsz[i][0] << 16);
-          if constexpr (kGroups == 2) vmax = fmaxf(vmax, __uint_as_float(vsz[i][1] << 16));
-          over = over || most[i] * vmax > 32768.0f || most[i] > 0x1p90f;
-        }
-        return __any_sync(0xffffffffu, over);
+        return __any_sync(0xffffffffu, max_u16x2(high, 0x78007800u) != 0x78007800u || most > kCaMaxSum);
       };
       if (pos >= 0) {
         if (edge)
@@ -1104,14 +1126,13 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
       // before it is weighed)
       const bool flag = pos >= 0 && (fresh || (edge ? weigh(std::true_type{}) : weigh(std::false_type{})));
       if (flag) {
-        // the references that would make the largest weight times scale 1
-        float lv[2];
+        // the largest scores, and with log2 of the value's scale in each group
+        float lv[1 + kGroups][2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float vmax = 0x1p-48f;
+          lv[0][i] = 0.0f;
 #pragma unroll
-          for (int j = 0; j < kGroups; ++j) vmax = fmaxf(vmax, __uint_as_float(vsz[i][j] << 16));
-          lv[i] = __log2f(vmax);
+          for (int j = 0; j < kGroups; ++j) lv[1 + j][i] = __log2f(__uint_as_float(vsz[i][j] << 16));
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -1119,40 +1140,52 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
           f2_split(xs[nt][0], e[0], e[1]);
           f2_split(xs[nt][1], f[0], f[1]);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float top = fmaxf(e[c] + lv[0], f[c] + lv[1]);
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            if (g == 0) s_cand[warp][nt * 8 + 2 * t4 + c] = top;
-          }
+            for (int j = 0; j < 1 + kGroups; ++j) {
+              float top = fmaxf(e[c] + lv[j][0], f[c] + lv[j][1]);
+#pragma unroll
+              for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+              if (g == 0) s_cand[j][warp][nt * 8 + 2 * t4 + c] = top;
+            }
         }
       }
       if (lane == 0) s_flag[warp] = flag;
       if (__syncthreads_or(flag)) {
         fresh = false;
-        // raise the references so that the largest weight times scale is 2^kCaRaise, and weigh again (a NaN stays one)
-        float now[NT][2];
+        // raise the references to the largest scores, lower the factors, and weigh again (a NaN stays one). Each warp
+        // sees to the factor of the group that its channels are in.
+        constexpr int kPerGroup = kCaWarps / kGroups;
+        float now[NT][2], factor[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const int col = nt * 8 + 2 * t4 + c;
-            float top = -CUDART_INF_F;
+            const int col = nt * 8 + 2 * t4 + c, j = warp / kPerGroup;
+            float top = -CUDART_INF_F, most = -CUDART_INF_F;
 #pragma unroll
             for (int w = 0; w < kCaWarps; ++w)
-              if (s_flag[w]) top = fmaxf(top, s_cand[w][col]);
-            const float old = s_m[col], f = fast_exp2(old - (now[nt][c] = fmaxf(old, top - kCaRaise<__nv_bfloat16>)));
+              if (s_flag[w]) top = fmaxf(top, s_cand[0][w][col]), most = fmaxf(most, s_cand[1 + j][w][col]);
+            const float old = s_m[col], f = fast_exp2(old - (now[nt][c] = fmaxf(old, top)));
+            factor[nt][c] = s_factor[j][col];
+            const float a = lower_factor<__nv_bfloat16>(factor[nt][c], old, now[nt][c], f, most);
             const uint64_t by = c ? f2(1.0f, f) : f2(f, 1.0f);
             l[nt] = f2_mul(l[nt], by);
 #pragma unroll
-            for (int j = 0; j < kGroups; ++j) z[j][nt] = f2_mul(z[j][nt], by);
+            for (int i = 0; i < kGroups; ++i) z[i][nt] = f2_mul(z[i][nt], by);
 #pragma unroll
-            for (int k = 0; k < kMt; ++k) acc[k][nt][c] *= f, acc[k][nt][2 + c] *= f;
+            for (int k = 0; k < kMt; ++k) acc[k][nt][c] *= a, acc[k][nt][2 + c] *= a;
           }
         __syncthreads();
-        if (warp == 0 && g == 0) {
+        if (warp % kPerGroup == 0 && g == 0) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) s_m[nt * 8 + 2 * t4] = now[nt][0], s_m[nt * 8 + 2 * t4 + 1] = now[nt][1];
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int col = nt * 8 + 2 * t4 + c;
+              if (warp == 0) s_m[col] = now[nt][c];
+              s_factor[warp / kPerGroup][col] = factor[nt][c];
+            }
         }
         __syncthreads();
         if (pos >= 0) weigh(std::true_type{});
@@ -1258,13 +1291,14 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
 #pragma unroll
         for (int w = 0; w < kCaWarps; ++w) sum += s_l[w][r], zero += s_z[w][word / 2][r];
         const float by = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
+        const float back = factor_inverse(s_factor[word / 2][r]);
         const int row = row0 + r;
         __nv_bfloat16* to = o + ((static_cast<long>(b) * s.T + row / G) * H + h * G + row % G) * D;
 #pragma unroll
         for (int k = 0; k < kMt; ++k) {
           const int ch = word * 32 + 4 * g + (D == 128 ? 2 * k : 2 * (warp % 2));
-          const float v0 = fmaf(acc[k][nt][c], 0x1p24f, zero) * by,
-                      v1 = fmaf(acc[k][nt][2 + c] - acc[k][nt][c], 0x1p20f, zero) * by;
+          const float v0 = fmaf(acc[k][nt][c] * 0x1p24f, back, zero) * by,
+                      v1 = fmaf((acc[k][nt][2 + c] - acc[k][nt][c]) * 0x1p20f, back, zero) * by;
           if (whole)
             *reinterpret_cast<uint32_t*>(to + ch) = pack_bf16x2(v0, v1);
           else

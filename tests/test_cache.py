@@ -751,3 +751,98 @@ def test_attn_large_queries_times_a_large_scale(bsa, D, dtype, G, T):
     assert torch.isnan(o[torch.as_tensor(bad, device="cuda")]).all()
     ref, size, logit = C.attn(both.ref, np.where(bad[..., None], 0, host(q)), both.table, start, scale=scale)
     check_attn(torch.nan_to_num(o), ref, size, logit, n, D, dtype, ~bad)
+
+
+@pytest.mark.parametrize("dtype,G,T", FORMS, ids=lambda x: str(x))
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_values_of_every_size(bsa, D, dtype, G, T):
+    """Values whose scales lie between 2^-122 and 2^97, the accuracy relative to them throughout."""
+    rng = np.random.default_rng(27)
+    Hk, n = 2, 200
+    k, v = randn(rng, 1, n, Hk, D, offset=1), torch.as_tensor(rng.standard_normal((1, n, Hk, D)), device="cuda").float()
+    q, start = randn(rng, 1, T, Hk * G, D, dtype=dtype, scale=1.5), np.array([n - T])
+    for v_scale in (1e-36, 1e-31, 1e-26, 1e-22, 1e-18, 1e20, 1e30):
+        both = Both(bsa, rng, 1, 4, Hk, D, 64)
+        both.write(k, (v * v_scale).bfloat16(), np.array([0]))
+        ref, size, logit = C.attn(both.ref, host(q), both.table, start)
+        o = bsa.bsa_cache_attn(q, both.cache, both.tab, dev(start), 64)
+        check_attn(o, ref, size, logit, n, D, dtype, np.ones((1, T, Hk * G), bool))
+
+
+@pytest.mark.parametrize("dtype,G,T", FORMS, ids=lambda x: str(x))
+def test_attn_value_groups_of_different_sizes(bsa, dtype, G, T):
+    """The two groups of 64 channels differ by powers of two: each keeps its own accuracy."""
+    rng = np.random.default_rng(28)
+    D, Hk, n = 128, 2, 300
+    k, v = randn(rng, 1, n, Hk, D, offset=1), torch.as_tensor(rng.standard_normal((1, n, Hk, D)), device="cuda").float()
+    q, start = randn(rng, 1, T, Hk * G, D, dtype=dtype, scale=1.5), np.array([n - T])
+    for e in (-100, -30, -20, -10, 10, 20, 30, 100):
+        both = Both(bsa, rng, 1, 5, Hk, D, 64)
+        x = v * 2.0 ** (-e // 2)
+        x[..., 64:] *= 2.0 ** e
+        both.write(k, x.bfloat16(), np.array([0]))
+        ref, size, logit = C.attn(both.ref, host(q), both.table, start)
+        o = bsa.bsa_cache_attn(q, both.cache, both.tab, dev(start), 64)
+        check_attn(o, ref, size, logit, n, D, dtype, np.ones((1, T, Hk * G), bool))
+
+
+@pytest.mark.parametrize("G", [1, 7])
+@pytest.mark.parametrize("e", [-30, -20, 20, 30])
+def test_attn_float32_groups_keep_float32(bsa, G, e):
+    """Beside a group that is 2^30 times larger or smaller: the criterion of the test of float32 queries, by group."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    Hk, D, bs, n = 2, 128, 64, 6000
+    cache, k_sum = bsa.bsa_cache_alloc(94, Hk, D, bs)
+    table, zero = torch.randperm(94, generator=g, device="cuda").int().view(1, -1), dev([0])
+    k, v = (torch.randn(1, n, Hk, D, generator=g, device="cuda") for _ in "kv")
+    v[..., 64:] *= 2.0 ** e
+    bsa.bsa_cache_write(k, v, cache, k_sum, table, zero, bs)
+    kk, vv = bsa.bsa_cache_read(cache, table, zero, n, bs, dtype=torch.float32)
+    kk, vv = (x[0].repeat_interleave(G, 1) for x in (kk, vv))
+    q = torch.randn(1, 1, Hk * G, D, generator=g, device="cuda") * 1.5
+    got = bsa.bsa_cache_attn(q, cache, table, dev([n - 1]), bs)[0, 0]
+    ref, plain = _formula(q[0, 0], kk, vv, torch.float64), _formula(q[0, 0], kk, vv, torch.float32)
+    for part in (slice(0, 64), slice(64, 128)):
+        err = lambda x: float((x[:, part].double() - ref[:, part]).norm() / ref[:, part].norm())  # noqa: E731
+        assert err(got) <= 4 * err(plain), (part, err(got), err(plain))
+
+
+@pytest.mark.parametrize("dtype,G,T", FORMS, ids=lambda x: str(x))
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_groups_of_one_large_value(bsa, D, dtype, G, T):
+    """A group of equal values has scale 0 and says nothing of how far weights may grow: values of 1e25 throughout, and
+    (D = 128) beside ordinary ones, with sharp scores that rise along the sequence."""
+    rng = np.random.default_rng(29)
+    Hk, n = 2, 400
+    k = randn(rng, 1, n, Hk, D, offset=np.linspace(0, 1, n)[:, None, None])
+    q, start = randn(rng, 1, T, Hk * G, D, dtype=dtype, scale=3, offset=1), np.array([n - T])
+    both = Both(bsa, rng, 1, 7, Hk, D, 64)
+    v = randn(rng, 1, n, Hk, D)
+    v[..., :64] = 1e25
+    both.write(k, v, np.array([0]))
+    ref, size, logit = C.attn(both.ref, host(q), both.table, start)
+    o = bsa.bsa_cache_attn(q, both.cache, both.tab, dev(start), 64)
+    check_attn(o, ref, size, logit, n, D, dtype, np.ones((1, T, Hk * G), bool))
+
+
+@pytest.mark.parametrize("dtype,G,T", FORMS, ids=lambda x: str(x))
+@pytest.mark.parametrize("rise", [0.3, -0.3])
+def test_attn_scores_that_rise_as_the_values_shrink(bsa, dtype, G, T, rise):
+    """Scores from 0 to 75 (or back), and values that shrink (grow) as their weights grow (shrink): the weights'
+    references and the groups' factors move far apart."""
+    rng = np.random.default_rng(30)
+    D, Hk, n = 128, 1, 250
+    i = torch.arange(n, device="cuda", dtype=torch.float32) if rise > 0 else torch.arange(n, 0, -1, device="cuda").float()
+    k = torch.zeros(1, n, Hk, D, device="cuda")
+    k[0, :, 0, 0] = i
+    v = torch.as_tensor(rng.standard_normal((1, n, Hk, D)), device="cuda").float()
+    v *= torch.exp(-abs(rise) * i + 20).view(1, n, 1, 1)
+    q = torch.zeros(1, T, Hk * G, D, device="cuda", dtype=DT[dtype])
+    q[..., 0] = 0.3 * D ** 0.5
+    q[:, :, 1:, 0] *= 0.5
+    both = Both(bsa, rng, 1, 4, Hk, D, 64)
+    both.write(k, v, np.array([0]))
+    start = np.array([n - T])
+    ref, size, logit = C.attn(both.ref, host(q), both.table, start)
+    o = bsa.bsa_cache_attn(q, both.cache, both.tab, dev(start), 64)
+    check_attn(o, ref, size, logit, n, D, dtype, np.ones((1, T, Hk * G), bool))
