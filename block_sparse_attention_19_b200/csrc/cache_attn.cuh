@@ -683,10 +683,12 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
       }
     };
 
-    // Sums kept in the matrix unit lose up to half a unit of their last place at every step, always downwards (1e-4 of
-    // the result after 6000 tokens, where values of both signs nearly cancel). So every kAside tiles they go to this
-    // thread's places of the join buffer, in float32, at the references of that time.
-    constexpr int kAside = 64;
+    // Sums kept in the matrix unit lose up to a unit of their last place at every step, always downwards: after 2 kAside
+    // steps about 2^-24 kAside of the sums of codes, which is 500 times as much of a result in which values of both signs
+    // nearly cancel (131072 tokens). So every kAside tiles they go to this thread's places of the join buffer, in
+    // float32, at the references of that time. Eight rows of D = 64 over 131072 tokens on one CTA: error 1.87e-3 with 16,
+    // 2.3e-3 with 32, 3.8e-3 with 64 (rounding the output alone: 1.68e-3); dense 32768-token batch: 61.3, 60.6, 60.5 us.
+    constexpr int kAside = 16;
     float aside_m[2];
     bool aside = false;
     auto sums_of = [&](int c, int w, float f, float zero) {

@@ -846,3 +846,33 @@ def test_attn_scores_that_rise_as_the_values_shrink(bsa, dtype, G, T, rise):
     ref, size, logit = C.attn(both.ref, host(q), both.table, start)
     o = bsa.bsa_cache_attn(q, both.cache, both.tab, dev(start), 64)
     check_attn(o, ref, size, logit, n, D, dtype, np.ones((1, T, Hk * G), bool))
+
+
+@pytest.mark.parametrize("G,T", [(1, 1), (4, 1), (8, 1), (4, 3)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_long_rows_stay_at_the_outputs_rounding(bsa, D, G, T):
+    """131072 tokens on one CTA (more units than CTAs). Beside the output's rounding, which the float32 formula rounded
+    once has too: the weights' rounding to float16 (2^-12 on average, independent, so 2^-12 of the result), and what
+    sums in the matrix unit lose, up to 2^-23 of them at each step: over 32 steps of a growing sum 2^-20 of it on
+    average, a quarter of 32 2^-23, of a sum of the size of the values' zeros."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    B, Hk, bs, n = 40, 16, 256, 131072
+    P = n // bs
+    cache, k_sum = bsa.bsa_cache_alloc(P, Hk, D, bs)
+    table = torch.arange(P, device="cuda", dtype=torch.int32)
+    k, v = (torch.randn(1, n, Hk, D, generator=g, device="cuda").bfloat16() for _ in "kv")
+    bsa.bsa_cache_write(k, v, cache, k_sum, table.view(1, -1), dev([0]), bs)
+    kk, vv = bsa.bsa_cache_read(cache, table.view(1, -1), dev([0]), n, bs, dtype=torch.float32)
+    q = torch.randn(1, T, Hk * G, D, generator=g, device="cuda").bfloat16()
+    o = bsa.bsa_cache_attn(q.expand(B, -1, -1, -1).contiguous(), cache, table.expand(B, -1).contiguous(),
+                           dev([n - T] * B), bs)
+    total = np.zeros(2)
+    for h in range(Hk):
+        x = kk[0, :, h].double() @ q[0, T - 1, h * G].double() / D ** 0.5
+        p = x.softmax(0)
+        ref = p @ vv[0, :, h].double()
+        plain = ((kk[0, :, h] @ q[0, T - 1, h * G].float() / D ** 0.5).softmax(0) @ vv[0, :, h]).bfloat16()
+        zeros = (p @ vv[0, :, h].double().view(n, -1, 64).abs().amax(-1)).repeat_interleave(64)
+        err = lambda y: float((y.double() - ref).norm() / ref.norm())  # noqa: E731
+        total += err(o[0, T - 1, h * G]), err(plain) + 2.0 ** -12 + 2.0 ** -20 * float(zeros.norm() / ref.norm())
+    assert total[0] <= total[1], total / Hk
