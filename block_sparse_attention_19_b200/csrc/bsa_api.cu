@@ -1361,9 +1361,9 @@ template <typename E, int D, int FOLD, typename... Args>
 cudaError_t launch_cache_attn_narrow(Args... args) {
   return launch_cache_attn<E, D, bsa::CaShape<D, FOLD>>(bsa::cache_attn_kernel<E, D, FOLD>, args...);
 }
-template <int D, int NT, typename... Args>
+template <int NT, typename... Args>
 cudaError_t launch_cache_attn_wide(Args... args) {
-  return launch_cache_attn<__nv_bfloat16, D, bsa::CaWide<D, NT>>(bsa::cache_attn_wide_kernel<D, NT>, args...);
+  return launch_cache_attn<__nv_bfloat16, bsa::kCaWideD, bsa::CaWide<NT>>(bsa::cache_attn_wide_kernel<NT>, args...);
 }
 
 // Calls f with a value of the element type and the head size as a constant.
@@ -1489,8 +1489,7 @@ bsa_status bsa_cache_block_topk(const void* q, const float* k_sum, const int32_t
 size_t bsa_cache_attn_workspace_bytes(int B, int T, int H, int H_kv, int D) {
   if (check_cache_dims(B, T, H, H_kv, D, 64) != BSA_OK) return 0;
   // the plan; two parts of a unit's query rows for each CTA, float32 and bfloat16 queries alike
-  const long rows = std::max({8 * bsa::CaShape<128, 1>::kCtas, 32 * bsa::CaWide<128, 4>::kCtas,
-                              40 * bsa::CaWide<128, 5>::kCtas});
+  const long rows = std::max({8 * bsa::CaShape<128, 1>::kCtas, 32 * bsa::CaWide<4>::kCtas, 40 * bsa::CaWide<5>::kCtas});
   return (static_cast<size_t>(B) + 1) * sizeof(int4) + static_cast<size_t>(sm_count()) * rows * 2 * (D + 2) * sizeof(float);
 }
 
@@ -1520,18 +1519,23 @@ bsa_status bsa_cache_attn(const void* q, const void* cache, const int32_t* page_
       return launch(q, cache, idx, o, workspace, seqs, B, H, H_kv, topk, sl, stream);
     };
     // Query rows of a (sequence, key/value head): up to four are folded (everything between the products once for two
-    // runs of tokens: dense 32768-token batch, four rows, 59 us against 63.5), up to eight fill the products' columns
-    // once. More go to the kernel whose warps share a tile, in units of equal size of up to 40 (40 rows, eight padded
-    // sequences of up to 16384 tokens: 27 us, 28 in units of 8 rows of the other kernel). float32 queries, whose
-    // operands come in two parts, stay with the first.
+    // runs of tokens: dense 32768-token batch, four rows, 61 us against 65), up to eight fill the products' columns
+    // once, and more make several units of eight. At D = 128 more than eight bfloat16 rows go to the kernel whose warps
+    // share a tile, in units of equal size of up to 40. Eight sequences, two heads, us with it / with units of eight:
+    //   rows                            9         16        24        32        40        64         80
+    //   D = 128, 32768 tokens           38 / 41   38 / 41   47 / 55   57 / 68   72 / 82   100 / 123  128 / 151
+    //   D = 128, up to 16384, ragged    18 / 19   19 / 20   22 / 23   26 / 27   29 / 30   37 / 41    45 / 48
+    //   D = 64, 32768 tokens            31 / 27   31 / 27   36 / 35   43 / 43   55 / 51   74 / 76    97 / 92
+    //   D = 64, up to 16384, ragged     16 / 15   17 / 15   19 / 17   22 / 19   25 / 21   29 / 28    36 / 32
+    // float32 queries, whose operands come in two parts, stay with the first.
     const long long rows = static_cast<long long>(T) * (H / H_kv);
-    if constexpr (sizeof(E) == 2) {
+    if constexpr (sizeof(E) == 2 && kD == bsa::kCaWideD) {
       if (rows > 8) {
         const long long units = (rows + 39) / 40, nt = ((rows + units - 1) / units + 7) / 8;
-        if (nt <= 2) return run([](auto... a) { return launch_cache_attn_wide<kD, 2>(a...); });
-        if (nt == 3) return run([](auto... a) { return launch_cache_attn_wide<kD, 3>(a...); });
-        if (nt == 4) return run([](auto... a) { return launch_cache_attn_wide<kD, 4>(a...); });
-        return run([](auto... a) { return launch_cache_attn_wide<kD, 5>(a...); });
+        if (nt <= 2) return run([](auto... a) { return launch_cache_attn_wide<2>(a...); });
+        if (nt == 3) return run([](auto... a) { return launch_cache_attn_wide<3>(a...); });
+        if (nt == 4) return run([](auto... a) { return launch_cache_attn_wide<4>(a...); });
+        return run([](auto... a) { return launch_cache_attn_wide<5>(a...); });
       }
     }
     if (rows <= 4) return run([](auto... a) { return launch_cache_attn_narrow<E, kD, 2>(a...); });

@@ -818,26 +818,29 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
 
 // ------------------------------------------------------------------ many query rows
 //
-// From nine query rows on (bfloat16) the work between the products and the
+// From nine query rows on (bfloat16, D = 128) the work between the products and the
 // products themselves outweigh the unpacking, and a warp cannot hold the sums of
-// all channels for all rows. So the four warps of a CTA share a tile: each scores
+// all channels for all rows. (At D = 64 it can, and the kernel above in units of
+// eight rows is the faster one: see the measurements where it is chosen.) So the four warps of a CTA share a tile: each scores
 // 16 of its 64 tokens against all rows, leaves the weights times the values'
 // scales in shared memory in the order of the products' second operand, and after
-// one barrier sums 32 (D = 64: 16) of the channels over all 64 tokens. The rows'
+// one barrier sums 32 of the channels over all 64 tokens. The rows'
 // references are the CTA's, in shared memory; a tile whose weights would leave
 // float16 raises them and is weighed again. Bound: the matrix instructions, 16 NT
-// (D = 128) for 16 tokens at 2.2 cycles of an SM each, 700 cycles a tile at 40 rows
+// for 16 tokens at 2.2 cycles of an SM each, 700 cycles a tile at 40 rows
 // against 400 for its bytes; measured, 1850: eight warps an SM do not hide the
 // chain of products, exponentials, barrier and products (profiled at 2150, before
 // references left more room: issue 40%, matrix unit 30%, shared memory 45% busy;
 // three CTAs an SM, with spills, 86 -> 110 us for 32768 tokens). Two teams of four warps with half the rows each
 // took 1.4 times as long, since both unpack every tile.
-template <int D, int NT>
+constexpr int kCaWideD = 128;
+template <int NT>
 struct CaWide {
+  static constexpr int D = kCaWideD;
   static constexpr int kRows = 8 * NT;
   static constexpr int kCtas = NT <= 4 ? 3 : 2;
   static constexpr int kExtra = 4;  // (see CaPlan)
-  static constexpr int kStages = 4 * 128 / D;
+  static constexpr int kStages = 4;
   static constexpr int kGroups = D / 64, kSteps = D / 16;
   static constexpr int kQWords = kSteps * NT * 64;            // query operands: [step][nt][lane][2]
   static constexpr int kPWords = 2 * kGroups * 4 * NT * 64;   // weights: [buffer][group][16 tokens][nt][lane][2]
@@ -869,14 +872,14 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {  // (may be
   return d;
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
+template <int NT>
+__global__ void __launch_bounds__(kCaThreads, CaWide<NT>::kCtas)
     cache_attn_wide_kernel(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict__ cache,
                            const int32_t* __restrict__ idx, __nv_bfloat16* o, float* ws, CacheSeqs s, int B, int H,
                            int Hkv, int topk, float scale_log2, int4* plan_out) {
-  using W = CaWide<D, NT>;
-  constexpr int kStages = W::kStages, kRows = W::kRows, kTile = cache_tile_bytes(D), kGroups = W::kGroups;
-  constexpr int kWords = D / 32, kMt = D / 64;  // 32-channel words; 16-channel products of a warp
+  using W = CaWide<NT>;
+  constexpr int D = W::D, kStages = W::kStages, kRows = W::kRows, kTile = cache_tile_bytes(D), kGroups = W::kGroups;
+  constexpr int kWords = D / 32, kMt = 2;  // 32-channel words (one a warp); 16-channel products of a warp
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
   extern __shared__ __align__(128) uint8_t smem[];
   uint32_t* sq = reinterpret_cast<uint32_t*>(smem + kStages * kTile);
@@ -939,6 +942,8 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
     const int stop = min(first + n, end);
     const int h = plan.head(u.unit), row0 = plan.row0(u.unit, kRows);
     const int rows = min(kRows, u.count * G - row0);  // rows with a query (may be <= 0)
+
+    const int group = warp / 2;  // of this warp's value channels
 
     // ---------------- the queries as the score products' second operand (float16, odd channels / 16: see above)
     constexpr int kPer = (NT + kCaWarps - 1) / kCaWarps;
@@ -1157,19 +1162,18 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
         fresh = false;
         // raise the references to the largest scores, lower the factors, and weigh again (a NaN stays one). Each warp
         // sees to the factor of the group that its channels are in.
-        constexpr int kPerGroup = kCaWarps / kGroups;
         float now[NT][2], factor[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const int col = nt * 8 + 2 * t4 + c, j = warp / kPerGroup;
+            const int col = nt * 8 + 2 * t4 + c;
             float top = -CUDART_INF_F, most = -CUDART_INF_F;
 #pragma unroll
             for (int w = 0; w < kCaWarps; ++w)
-              if (s_flag[w]) top = fmaxf(top, s_cand[0][w][col]), most = fmaxf(most, s_cand[1 + j][w][col]);
+              if (s_flag[w]) top = fmaxf(top, s_cand[0][w][col]), most = fmaxf(most, s_cand[1 + group][w][col]);
             const float old = s_m[col], f = fast_exp2(old - (now[nt][c] = fmaxf(old, top)));
-            factor[nt][c] = s_factor[j][col];
+            factor[nt][c] = s_factor[group][col];
             const float a = lower_factor<__nv_bfloat16>(factor[nt][c], old, now[nt][c], f, most);
             const uint64_t by = c ? f2(1.0f, f) : f2(f, 1.0f);
             l[nt] = f2_mul(l[nt], by);
@@ -1179,14 +1183,14 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
             for (int k = 0; k < kMt; ++k) acc[k][nt][c] *= a, acc[k][nt][2 + c] *= a;
           }
         __syncthreads();
-        if (warp % kPerGroup == 0 && g == 0) {
+        if (warp % 2 == 0 && g == 0) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const int col = nt * 8 + 2 * t4 + c;
               if (warp == 0) s_m[col] = now[nt][c];
-              s_factor[warp / kPerGroup][col] = factor[nt][c];
+              s_factor[group][col] = factor[nt][c];
             }
         }
         __syncthreads();
@@ -1223,7 +1227,6 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
           add_up(std::true_type{});
         else
           add_up(std::false_type{});
-        const int word = D == 128 ? warp : warp / 2, j = word / 2;
         // a tile's products start from zero and are added in float32 (see the other kernel)
         float sum[kMt][NT][4];
 #pragma unroll
@@ -1231,16 +1234,16 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
           uint32_t vw[2][1], av[kMt][4];
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            get_words(base + cache_v_offset(D) + (kt * 8 + t4 + 4 * i) * D + (g ^ (2 * t4)) * (D / 8) + word * 4, vw[i]);
+            get_words(base + cache_v_offset(D) + (kt * 8 + t4 + 4 * i) * D + (g ^ (2 * t4)) * (D / 8) + warp * 4, vw[i]);
 #pragma unroll
           for (int k = 0; k < kMt; ++k) {
-            const uint32_t pick = D == 128 ? (k ? 0x4341u : 0x4240u) : (warp % 2 ? 0x4341u : 0x4240u);
+            const uint32_t pick = k ? 0x4341u : 0x4240u;
             av[k][1] = __byte_perm(vw[0][0], 0, pick), av[k][0] = av[k][1] & kLow;
             av[k][3] = __byte_perm(vw[1][0], 0, pick), av[k][2] = av[k][3] & kLow;
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const uint2 bp = reinterpret_cast<const uint2*>(sp)[(((buf * kGroups + j) * 4 + kt) * NT + nt) * 32 + lane];
+            const uint2 bp = reinterpret_cast<const uint2*>(sp)[(((buf * kGroups + group) * 4 + kt) * NT + nt) * 32 + lane];
 #pragma unroll
             for (int k = 0; k < kMt; ++k)
               if (kt == 0)
@@ -1282,7 +1285,6 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
     __syncthreads();
     const bool whole = first >= begin && first + n <= end;
     float* part = part_of<kRows, D>(ws, blockIdx.x, first < begin ? 0 : 1);
-    const int word = D == 128 ? warp : warp / 2;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1291,14 +1293,14 @@ __global__ void __launch_bounds__(kCaThreads, (CaWide<D, NT>::kCtas))
         if (r >= rows) continue;
         float sum = 0.0f, zero = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kCaWarps; ++w) sum += s_l[w][r], zero += s_z[w][word / 2][r];
+        for (int w = 0; w < kCaWarps; ++w) sum += s_l[w][r], zero += s_z[w][group][r];
         const float by = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
-        const float back = factor_inverse(s_factor[word / 2][r]);
+        const float back = factor_inverse(s_factor[group][r]);
         const int row = row0 + r;
         __nv_bfloat16* to = o + ((static_cast<long>(b) * s.T + row / G) * H + h * G + row % G) * D;
 #pragma unroll
         for (int k = 0; k < kMt; ++k) {
-          const int ch = word * 32 + 4 * g + (D == 128 ? 2 * k : 2 * (warp % 2));
+          const int ch = warp * 32 + 4 * g + 2 * k;
           const float v0 = fmaf(acc[k][nt][c] * 0x1p24f, back, zero) * by,
                       v1 = fmaf((acc[k][nt][2 + c] - acc[k][nt][c]) * 0x1p20f, back, zero) * by;
           if (whole)
