@@ -888,10 +888,10 @@ __global__ void __launch_bounds__(kCaThreads, CaWide<NT>::kCtas)
   __shared__ uint64_t full[kStages];
   __shared__ int tile_pos[kStages], next_pos[32];
   __shared__ const uint8_t* next_src[32];
-  __shared__ __align__(16) float s_mul[kRows], s_qsum[kGroups][kRows], s_m[kRows], s_factor[kGroups][kRows];
+  __shared__ __align__(16) float s_mul[kRows], s_qsum[kGroups][kRows], s_ref[kRows], s_factor[kGroups][kRows];
   __shared__ __align__(16) int s_limit[kRows];
-  __shared__ float s_cand[1 + kGroups][kCaWarps][kRows], s_l[kCaWarps][kRows], s_z[kCaWarps][kGroups][kRows];
-  __shared__ int s_flag[kCaWarps], abort_flag;
+  __shared__ float s_top[1 + kGroups][kRows], s_l[kCaWarps][kRows], s_z[kCaWarps][kGroups][kRows];
+  __shared__ int abort_flag;
   pdl_launch_dependents();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, G = H / Hkv, g = lane / 4, t4 = lane % 4;
   if (threadIdx.x == 0) {
@@ -992,7 +992,7 @@ __global__ void __launch_bounds__(kCaThreads, CaWide<NT>::kCtas)
 #pragma unroll
         for (int j = 0; j < kGroups; ++j) s_qsum[j][r] = sum[j] * scale_log2, s_factor[j][r] = kCaFirstFactor;
         s_limit[r] = r < rows ? start + row / G + 1 : 0;
-        s_m[r] = kCaNone;
+        s_ref[r] = kCaNone;
       }
     }
     const int low_limit = start + row0 / G + 1;  // positions below it are seen by all rows
@@ -1094,7 +1094,7 @@ __global__ void __launch_bounds__(kCaThreads, CaWide<NT>::kCtas)
         for (int nt = 0; nt < NT; ++nt)
           {
             const int col = nt * 8 + 2 * t4;
-            const uint64_t ref = load_f2(s_m + col);
+            const uint64_t ref = load_f2(s_ref + col);
             uint32_t w16[kGroups][2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -1132,49 +1132,48 @@ __global__ void __launch_bounds__(kCaThreads, CaWide<NT>::kCtas)
       // (every warp takes every barrier here, whatever it saw of the tile; a unit's first tile sets the references
       // before it is weighed)
       const bool flag = pos >= 0 && (fresh || (edge ? weigh(std::true_type{}) : weigh(std::false_type{})));
-      if (flag) {
-        // the largest scores, and with log2 of the value's scale in each group
-        float lv[1 + kGroups][2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          lv[0][i] = 0.0f;
-#pragma unroll
-          for (int j = 0; j < kGroups; ++j) lv[1 + j][i] = __log2f(__uint_as_float(vsz[i][j] << 16));
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float e[2], f[2];
-          f2_split(xs[nt][0], e[0], e[1]);
-          f2_split(xs[nt][1], f[0], f[1]);
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int j = 0; j < 1 + kGroups; ++j) {
-              float top = fmaxf(e[c] + lv[j][0], f[c] + lv[j][1]);
-#pragma unroll
-              for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-              if (g == 0) s_cand[j][warp][nt * 8 + 2 * t4 + c] = top;
-            }
-        }
-      }
-      if (lane == 0) s_flag[warp] = flag;
       if (__syncthreads_or(flag)) {
         fresh = false;
-        // raise the references to the largest scores, lower the factors, and weigh again (a NaN stays one). Each warp
-        // sees to the factor of the group that its channels are in.
-        float now[NT][2], factor[NT][2];
+        // Raise the references to the largest scores of the tile, lower the factors, and weigh again (a NaN stays one).
+        // What each thread has of a column, the largest score and with log2 of the value's scale in each group, meets
+        // in the weights' place: they are to be written anew, and every warp is past the tile before this one.
+        constexpr int kStride = kCaThreads + 4;  // floats of a list (reading it is free of conflicts)
+        static_assert((1 + kGroups) * NT * 2 * kStride <= W::kPWords && (1 + kGroups) * kRows <= kCaThreads);
+        float* cand = reinterpret_cast<float*>(sp);
+        if (pos >= 0) {
+#pragma unroll
+          for (int j = 0; j < 1 + kGroups; ++j) {
+            const float lv0 = j ? __log2f(__uint_as_float(vsz[0][j - 1 + !j] << 16)) : 0.0f;
+            const float lv1 = j ? __log2f(__uint_as_float(vsz[1][j - 1 + !j] << 16)) : 0.0f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float e[2], f[2];
+              f2_split(xs[nt][0], e[0], e[1]);
+              f2_split(xs[nt][1], f[0], f[1]);
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                cand[((j * NT + nt) * 2 + c) * kStride + threadIdx.x] = fmaxf(e[c] + lv0, f[c] + lv1);
+            }
+          }
+        }
+        __syncthreads();
+        if (threadIdx.x < (1 + kGroups) * kRows) {
+          const int list = threadIdx.x / 4, col = list / 2 % NT * 8 + 2 * t4 + list % 2;
+          float top = -CUDART_INF_F;
+#pragma unroll 8
+          for (int i = 0; i < kCaThreads / 4; ++i) top = fmaxf(top, cand[list * kStride + i * 4 + t4]);
+          s_top[list / (2 * NT)][col] = top;
+        }
+        __syncthreads();
+        // each warp's sums follow the factor of the group that its channels are in
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int col = nt * 8 + 2 * t4 + c;
-            float top = -CUDART_INF_F, most = -CUDART_INF_F;
-#pragma unroll
-            for (int w = 0; w < kCaWarps; ++w)
-              if (s_flag[w]) top = fmaxf(top, s_cand[0][w][col]), most = fmaxf(most, s_cand[1 + group][w][col]);
-            const float old = s_m[col], f = fast_exp2(old - (now[nt][c] = fmaxf(old, top)));
-            factor[nt][c] = s_factor[group][col];
-            const float a = lower_factor<__nv_bfloat16>(factor[nt][c], old, now[nt][c], f, most);
+            const float old = s_ref[col], now = fmaxf(old, s_top[0][col]), f = fast_exp2(old - now);
+            float factor = s_factor[group][col];
+            const float a = lower_factor<__nv_bfloat16>(factor, old, now, f, s_top[1 + group][col]);
             const uint64_t by = c ? f2(1.0f, f) : f2(f, 1.0f);
             l[nt] = f2_mul(l[nt], by);
 #pragma unroll
@@ -1183,15 +1182,12 @@ __global__ void __launch_bounds__(kCaThreads, CaWide<NT>::kCtas)
             for (int k = 0; k < kMt; ++k) acc[k][nt][c] *= a, acc[k][nt][2 + c] *= a;
           }
         __syncthreads();
-        if (warp % 2 == 0 && g == 0) {
+        if (threadIdx.x < kRows) {
+          const float old = s_ref[threadIdx.x], now = fmaxf(old, s_top[0][threadIdx.x]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int col = nt * 8 + 2 * t4 + c;
-              if (warp == 0) s_m[col] = now[nt][c];
-              s_factor[group][col] = factor[nt][c];
-            }
+          for (int j = 0; j < kGroups; ++j)
+            lower_factor<__nv_bfloat16>(s_factor[j][threadIdx.x], old, now, 1.0f, s_top[1 + j][threadIdx.x]);
+          s_ref[threadIdx.x] = now;
         }
         __syncthreads();
         if (pos >= 0) weigh(std::true_type{});
@@ -1308,7 +1304,7 @@ __global__ void __launch_bounds__(kCaThreads, CaWide<NT>::kCtas)
           else
             *reinterpret_cast<float2*>(part + 2 * kRows + r * D + ch) = make_float2(v0, v1);
         }
-        if (!whole && warp == 0 && g == 0) part[r] = s_m[r], part[kRows + r] = sum;
+        if (!whole && warp == 0 && g == 0) part[r] = s_ref[r], part[kRows + r] = sum;
       }
     __syncthreads();
   }
