@@ -1329,18 +1329,22 @@ cudaError_t launch_cache_attn(void (*kern)(const E*, const uint8_t*, const int32
                               const void* q, const void* cache, const int32_t* idx, void* o, void* ws,
                               const bsa::CacheSeqs& seqs, int B, int H, int Hkv, int topk, float scale_log2,
                               void* stream) {
-  static bool attr_set[64] = {false};
+  static unsigned fixed[64] = {0};  // what a CTA takes beside its dynamic memory: its static memory, and 1 KB reserved
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev >= 64 || !attr_set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(Shape::smem(bsa::kCaMaxSeqs)));
+  unsigned more = dev < 64 ? fixed[dev] : 0;
+  if (!more) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(Shape::smem(bsa::kCaMaxSeqs)));
+    cudaFuncAttributes attr;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, kern);
     if (e != cudaSuccess) return e;
-    if (dev < 64) attr_set[dev] = true;
+    more = static_cast<unsigned>(attr.sharedSizeBytes) + 1024;
+    if (dev < 64) fixed[dev] = more;
   }
-  // with a long table of sequences fewer CTAs fit an SM's 228 KB (each takes 1 KB more, and static memory)
+  // all CTAs are to be resident at once: with a long table of sequences fewer fit an SM's 228 KB
   const size_t smem = Shape::smem(B);
-  const unsigned per_sm = std::min<unsigned>(Shape::kCtas, 228 * 1024 / (smem + 3072));
+  const unsigned per_sm = std::min<unsigned>(Shape::kCtas, 228 * 1024 / ((smem + more + 127) / 128 * 128));
   const unsigned ctas = per_sm * sm_count();
   int4* plan = static_cast<int4*>(ws);  // the plan, then the parts
   float* parts = reinterpret_cast<float*>(plan + 1 + B);

@@ -876,3 +876,45 @@ def test_attn_long_rows_stay_at_the_outputs_rounding(bsa, D, G, T):
         err = lambda y: float((y.double() - ref).norm() / ref.norm())  # noqa: E731
         total += err(o[0, T - 1, h * G]), err(plain) + 2.0 ** -12 + 2.0 ** -20 * float(zeros.norm() / ref.norm())
     assert total[0] <= total[1], total / Hk
+
+
+@pytest.mark.parametrize("dtype,D,G", [("bf16", 64, 2), ("bf16", 128, 40), ("bf16", 128, 5), ("f32", 128, 1)])
+@pytest.mark.parametrize("B", [2800, 4096])
+def test_attn_thousands_of_sequences(bsa, dtype, D, G, B):
+    """Up to the most sequences that a call takes, some of them empty, against the formula in 64 bits on what is read
+    back (its float32 rounding of the values, and the tolerance of the long ragged batch, whose logits stay below 60)."""
+    g = torch.Generator(device="cuda").manual_seed(10)
+    bs, P, most = 64, 3, 150
+    cache, k_sum = bsa.bsa_cache_alloc(B * P, 1, D, bs)
+    cache.fill_(0xFF)
+    table = torch.randperm(B * P, generator=g, device="cuda").int().view(B, P)
+    n = torch.randint(1, most + 1, (B,), generator=g, device="cuda").int()
+    k, v = (torch.randn(B, most, 1, D, generator=g, device="cuda").to(DT[dtype]) for _ in "kv")
+    zero = torch.zeros_like(n)
+    bsa.bsa_cache_write(k, v, cache, k_sum, table, zero, bs, count=n)
+    q = torch.randn(B, 1, G, D, generator=g, device="cuda").to(DT[dtype])
+    start = n - 1
+    start[::7] = -1
+    out = torch.full_like(q, 7.0)
+    ws = torch.empty(bsa.bsa_cache_attn_workspace_bytes(B, 1, G, 1, D), dtype=torch.uint8, device="cuda")
+    o = bsa.bsa_cache_attn(q, cache, table, start, bs, workspace=ws, out=out)
+    assert bool((o[::7] == 7).all())
+    kk, vv = (x[:, :, 0].double() for x in bsa.bsa_cache_read(cache, table, zero, most, bs, dtype=torch.float32, count=n))
+    seen = torch.arange(most, device="cuda") < n[:, None]
+    x = torch.einsum("bgd,bnd->bgn", q[:, 0].double(), kk) / D ** 0.5
+    w = torch.where(seen[:, None], x, -torch.inf).softmax(-1)
+    parts = vv.abs().view(B, most, -1, 64)
+    parts = (parts + 2.3 * parts.amax(-1, keepdim=True)).view(B, most, D)
+    ref, size = (torch.einsum("bgn,bnd->bgd", w, y) for y in (vv, parts))
+    f32 = dtype == "f32"
+    tol = (2.0 ** -24 if f32 else 2.0 ** -8) * ref.abs() + (
+        (2.0 ** -22 if f32 else 2.0 ** -11) + 2 * ((D + 8) * U + (2.0 ** -21 if f32 else 0)) * 60 + (most / 4 + 64) * U) * size
+    live = torch.arange(B, device="cuda") % 7 != 0
+    assert bool(((o[:, 0].double() - ref).abs() <= tol)[live].all())
+    if B == 2800 and G == 40:
+        # A CTA has four tiles of 9216 bytes, 30720 of operands, 44800 of sequences, some 4 KB of static memory and 1 KB
+        # reserved: an SM's 228 KB hold one, not two. The work, a tile and four more for a unit that begins, is cut for
+        # that many CTAs; its piece for each stands first in the workspace.
+        tiles = ((start[live] + 64) // 64 + 4).sum().item()
+        sms = torch.cuda.get_device_properties(0).multi_processor_count
+        assert ws[:4].view(torch.int32).item() == -(-tiles // sms)
