@@ -145,16 +145,6 @@ struct Octet<float> {
   }
   static __device__ __forceinline__ void limits(Range m, float& mx, float& mn) { mx = m.x, mn = m.y; }
 };
-__device__ __forceinline__ void load_octet(const __nv_bfloat16* x, float (&f)[8]) {
-  Octet<__nv_bfloat16> o;
-  o.load(x);
-  o.floats(f);
-}
-__device__ __forceinline__ void load_octet(const float* x, float (&f)[8]) {
-  Octet<float> o;
-  o.load(x);
-  o.floats(f);
-}
 __device__ __forceinline__ void store_octet(__nv_bfloat16* x, const float (&f)[8]) {
   *reinterpret_cast<uint4*>(x) =
       make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
@@ -163,9 +153,6 @@ __device__ __forceinline__ void store_octet(float* x, const float (&f)[8]) {
   reinterpret_cast<float4*>(x)[0] = make_float4(f[0], f[1], f[2], f[3]);
   reinterpret_cast<float4*>(x)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
-
-// The value that a code stands for: the product is exact, the sum rounds once.
-__device__ __forceinline__ float cache_value(float scale, float zero, float code) { return fmaf(scale, code, zero); }
 
 __device__ __forceinline__ void unpack_sz(uint32_t sz, float& scale, float& zero) {
   scale = __uint_as_float(sz << 16);

@@ -918,3 +918,16 @@ def test_attn_thousands_of_sequences(bsa, dtype, D, G, B):
         tiles = ((start[live] + 64) // 64 + 4).sum().item()
         sms = torch.cuda.get_device_properties(0).multi_processor_count
         assert ws[:4].view(torch.int32).item() == -(-tiles // sms)
+
+
+def test_block_topk_past_2_31_elements_of_the_sums(bsa):
+    Hk, D, bs, P, topk = 16, 128, 64, 300, 40
+    g = torch.Generator(device="cuda").manual_seed(11)
+    low = torch.randn(P, Hk, D, generator=g, device="cuda") * bs
+    q, start = torch.randn(1, 1, Hk, D, generator=g, device="cuda"), dev([P * bs - 1])
+    here = torch.arange(P, device="cuda", dtype=torch.int32)[None]
+    want = bsa.bsa_cache_block_topk(q, low, here, start, topk, bs)
+    pages = (1 << 20) + P  # of 2048 sums each
+    k_sum = torch.zeros(pages, Hk, D, device="cuda")
+    k_sum[-P:] = low
+    assert torch.equal(bsa.bsa_cache_block_topk(q, k_sum, here + pages - P, start, topk, bs), want)

@@ -125,3 +125,22 @@ def test_block_topk_forces_nothing_without_new_tokens():
     table, q = np.arange(4)[None], np.ones((1, 1, 1, 64))
     idx, _ = C.block_topk(q, np.ones((4, 1, 64)), table, np.array([200]), 2, 64, np.array([0]), force_diag=True)
     assert idx.tolist() == [[[0, 1]]]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_layout_uses_every_code_scale_and_zero_once(D):
+    """Each of the 128 D four-bit places belongs to one channel of one token, keys in the first half, the low four bits
+    to even channels; so does each scale and zero to one group. Places are numbered in base 16, a digit at a time."""
+    one = torch.tensor([1.0, 0.0]).bfloat16().view(torch.uint8).numpy()
+    place = np.zeros((2, 64, D), np.int64)
+    for digit in range(4):
+        n = np.arange(128 * D) >> (4 * digit) & 15
+        tile = np.r_[(n[0::2] | n[1::2] << 4).astype(np.uint8), np.tile(one, 2 * D)]
+        place += np.stack(C.tile_values(tile)).astype(np.int64) << (4 * digit)
+    assert np.array_equal(np.sort(place.reshape(-1)), np.arange(128 * D))
+    assert (place[0] < 64 * D).all() and (place % 2 == np.arange(D) % 2).all()
+    groups = 2 * D  # of keys and values; their numbers are bfloat16 values
+    for codes, pair in ((0x00, lambda i: (0, i)), (0x11, lambda i: (i, 0))):
+        sz = torch.tensor([pair(i) for i in range(groups)]).bfloat16().view(torch.uint8).numpy().reshape(-1)
+        v = np.stack(C.tile_values(np.r_[np.full(64 * D, codes, np.uint8), sz])).reshape(2, 64, D // 64, 64)
+        assert (v == v[..., :1]).all() and np.array_equal(v[..., 0].reshape(-1), np.arange(groups))
