@@ -931,3 +931,18 @@ def test_block_topk_past_2_31_elements_of_the_sums(bsa):
     k_sum = torch.zeros(pages, Hk, D, device="cuda")
     k_sum[-P:] = low
     assert torch.equal(bsa.bsa_cache_block_topk(q, k_sum, here + pages - P, start, topk, bs), want)
+
+
+@pytest.mark.parametrize("B,Hk", [(1, 1), (3, 7)])
+def test_block_topk_of_the_longest_rows(bsa, B, Hk):
+    """49152 blocks, the most that a call takes: one CTA an SM, clusters of eight."""
+    D, bs, P = 64, 64, 49152
+    g = torch.Generator(device="cuda").manual_seed(12)
+    k_sum = torch.randn(P, Hk, D, generator=g, device="cuda")
+    table = torch.stack([torch.randperm(P, generator=g, device="cuda") for _ in range(B)]).int()
+    q = torch.randn(B, 1, Hk, D, generator=g, device="cuda")
+    start = dev([P * bs - 1, P * bs // 2, 700][:B])
+    for topk in (1, 3000, 20000):
+        got = bsa.bsa_cache_block_topk(q, k_sum, table, start, topk, bs)
+        want, _ = C.block_topk(host(q), host(k_sum), table.cpu().numpy(), start.cpu().numpy(), topk, bs)
+        assert np.array_equal(got.cpu().numpy(), want)
