@@ -1354,7 +1354,7 @@ cudaError_t launch_cache_attn(void (*kern)(const E*, const uint8_t*, const int32
                  static_cast<E*>(o), parts, seqs, B, H, Hkv, topk, scale_log2, plan);
   if (e != cudaSuccess) return e;
   // A plain launch: as a programmatic one its waiting CTAs and the next call's early ones share the SMs so that
-  // some of the latter start late (a run of dense calls: 79 against 59 us each).
+  // some of the latter start late (a run of dense calls: 79 against 59 us each when it was tried).
   bsa::cache_attn_join_kernel<E, D, Shape::kRows>
       <<<static_cast<unsigned>(B) * seqs.T * H, bsa::kCaJoinWarps * 32, 0, st>>>(static_cast<E*>(o), parts, plan, seqs.T,
                                                                                  H, Hkv);
@@ -1523,7 +1523,7 @@ bsa_status bsa_cache_attn(const void* q, const void* cache, const int32_t* page_
       return launch(q, cache, idx, o, workspace, seqs, B, H, H_kv, topk, sl, stream);
     };
     // Query rows of a (sequence, key/value head): up to four are folded (everything between the products once for two
-    // runs of tokens: dense 32768-token batch, four rows, 61 us against 65), up to eight fill the products' columns
+    // runs of tokens: dense 32768-token batch, four rows, 60 us against 66.5), up to eight fill the products' columns
     // once, and more make several units of eight. At D = 128 more than eight bfloat16 rows go to the kernel whose warps
     // share a tile, in units of equal size of up to 40. Eight sequences, two heads, us with it / with units of eight:
     //   rows                            9         16        24        32        40        64         80

@@ -236,8 +236,8 @@ __device__ __forceinline__ uint32_t quantise_octet(const Octet<T>& x, uint32_t& 
 // on float32 pairs, minima and maxima on bfloat16 pairs, and the eight lanes of a
 // group compute eight octets' scales apart (325 us without that). 131072 tokens of
 // 16 heads, D = 128, bf16: 270 us for 1.37 GB, 5.1 TB/s; 87 instructions an octet
-// keep the SMs busier than the memory. One token of 64 sequences: about 4 us of
-// latencies (length, page, older keys, new ones).
+// keep the SMs busier than the memory (profiled: issue 62%, the memory's bus 62%). One token of 64 sequences: about 4 us of
+// latencies (length, page, older keys, new ones); with the reading back 6.6 us in a captured run, 18.8 issued from Python.
 template <typename T, int D>
 __global__ void __launch_bounds__(128) cache_write_kernel(const T* __restrict__ k, const T* __restrict__ v,
                                                           uint8_t* cache, float* k_sum, CacheSeqs s, int Hkv,
@@ -468,8 +468,9 @@ __global__ void __launch_bounds__(128) cache_read_kernel(const uint8_t* __restri
 // ascending order.
 // The bytes of the sums bound it (B H_kv blocks D 4 bytes) where there are many;
 // a short row is a chain of latencies: lengths, pages, sums, three histograms.
-// 32 rows x 4 heads of up to 1024 blocks, D = 128: 17 us (scoring 8, at the memory's
-// rate; selecting 3); 4096 blocks of 8 heads: 15 us; 128 blocks: 4.8 us.
+// 32 rows x 4 heads of up to 1024 blocks, D = 128: 17 us (lengths, pages and queries 3.4,
+// scoring 10.3, selecting 3); 4096 blocks of 8 heads: 15 us (3.4, 4.3, 7.1); 128 blocks: 4.9 us
+// in a captured run, 13 issued from Python (the host's time).
 // The dot products run in float64 and are rounded to float32 once, so that which
 // blocks are kept does not depend on an order of summation.
 constexpr int kCacheSelThreads = 256, kCacheSelWarps = kCacheSelThreads / 32;

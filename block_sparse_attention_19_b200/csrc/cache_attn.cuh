@@ -29,10 +29,11 @@
 //
 // All units' tiles lie in one line, cut into equal pieces for CTAs that are all
 // resident at once; a unit that several CTAs share leaves one part for each, which a
-// second launch joins. Measured on one B200 (6.55 TB/s copied): 16 sequences of
-// 32768 tokens, 4 heads, four query rows each: 59 us for 302 MB, 5.1 TB/s; 15% of
+// second launch joins. Measured on one B200 (6.55 TB/s copied), device time of a call in a captured run: 16
+// sequences of 32768 tokens, 4 heads, four query rows each: 60 us for 302 MB, 5.0 TB/s; 15% of
 // the blocks of up to 131072 tokens: 35 us; one sequence of 397 tokens: 8 us, of
-// which 2 are the joining launch. In the long run a tile costs its bytes' time;
+// which 2 are the joining launch. (Issued one by one from Python: 63, 37 and 17 us; the last is the host's time
+// for a call.) In the long run a tile costs its bytes' time, 0.214 us of an SM;
 // the rest is a chain that every call has: lengths, plan, page, first tile (4 us),
 // the last tiles' sums (1.3 us), the joining (2 to 4.5 us).
 #pragma once
@@ -50,7 +51,7 @@ constexpr int kCaMaxSeqs = 4096;  // sequences whose plan fits in shared memory
 // A row's reference M is at least its largest score of the time when it was last raised, and a group's factor 2^e
 // puts the largest weight times scale of that time between 2^kCaRaise and 2^(kCaRaise + 1). Later ones may reach 2^15
 // before the next raise, and a raise weighs a tile twice: from 8 on at least 2^6 times the largest so far is left, with
-// scores of deviation 2 most rows' last raise (many rows: 33.2 us, 36.2 from 12 on). A weight times scale is off by
+// scores of deviation 2 most rows' last raise (40 rows, padded batch: 28.2 us, 34.5 from 12 on; dense: 60.2, 61.8). A weight times scale is off by
 // half of float16's smallest number at most, 2^-33 of the group's largest; for float32 queries 2^-37.
 // Each group has a factor of its own, so that small scales beside large ones keep their accuracy, and M leaves the
 // scales out, so that the sums of weights, and of weights times zeros, stay near one however small the scales are.
@@ -183,8 +184,8 @@ __device__ __forceinline__ float score_factor(float amax, int e, float scale_log
 // Beginning a unit (its queries, its first tile's references, the sums of the one
 // before) takes a CTA as long as `extra` tiles, so the pieces are equal in tiles
 // and beginnings together: a unit weighs its tiles and `extra` more, which come
-// before them. (Ragged batch of 48: 16.6 us with six, 17.7 with two, 18.3 with none;
-// 40 rows: 28.0 with four, 29.0 with two, 33.1 with none.)
+// before them. (Ragged batch of 48: 17.1 us with six, 18.2 with two, 19.1 with none;
+// 40 rows: 28.2 with four, 29.0 with two, 33.1 with none.)
 struct CaPlan {
   const int4* seqs;  // [B]: tiles before the sequence, weight before it, start, count
   int per_seq;       // units of a sequence
@@ -687,7 +688,7 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
     // steps about 2^-24 kAside of the sums of codes, which is 500 times as much of a result in which values of both signs
     // nearly cancel (131072 tokens). So every kAside tiles they go to this thread's places of the join buffer, in
     // float32, at the references of that time. Eight rows of D = 64 over 131072 tokens on one CTA: error 1.87e-3 with 16,
-    // 2.3e-3 with 32, 3.8e-3 with 64 (rounding the output alone: 1.68e-3); dense 32768-token batch: 61.3, 60.6, 60.5 us.
+    // 2.3e-3 with 32, 3.8e-3 with 64 (rounding the output alone: 1.68e-3); the dense 32768-token batch takes 1% longer with 16 than with 64.
     constexpr int kAside = 16;
     float aside_m[2];
     bool aside = false;
@@ -828,9 +829,10 @@ __global__ void __launch_bounds__(kCaThreads, (CaShape<D, FOLD>::kCtas))
 // references are the CTA's, in shared memory; a tile whose weights would leave
 // float16 raises them and is weighed again. Bound: the matrix instructions, 16 NT
 // for 16 tokens at 2.2 cycles of an SM each, 700 cycles a tile at 40 rows
-// against 400 for its bytes; measured, 1850: eight warps an SM do not hide the
-// chain of products, exponentials, barrier and products (profiled at 2150, before
-// references left more room: issue 40%, matrix unit 30%, shared memory 45% busy;
+// against 400 for its bytes; measured, 1900 (0.98 us): eight warps an SM do not hide the
+// chain of products, exponentials, barrier and products (profiled at 40 rows, 758 instructions of a warp a tile:
+// issue 35%, matrix unit 30%, shared memory's data path 48% busy; 2.0 of 5.6 cycles between a warp's instructions are
+// fixed latencies, 0.8 shared memory, 0.5 the barrier;
 // three CTAs an SM, with spills, 86 -> 110 us for 32768 tokens). Two teams of four warps with half the rows each
 // took 1.4 times as long, since both unpack every tile.
 constexpr int kCaWideD = 128;

@@ -453,7 +453,8 @@ size_t bsa_cache_bytes(int num_pages, int H_kv, int D, int block_size);
  *   zero = bf16(min x), scale = bf16((max x - zero) * fl(1/15)) (0 where that
  *   is below 2^-126), code = clamp(rint((x - zero) * fl(1/scale)), 0, 15),
  *   rint to even. A group that holds a NaN or an infinity, or whose range
- *   passes float32, gets NaN for scale and zero and reads back as NaN.
+ *   passes float32 or zero bfloat16, gets NaN for scale and zero and reads back
+ *   as NaN.
  * k_sum is the float32 sum of the page's keys as they read back, over its
  * tokens up to the call's last one: rewriting from a smaller start (tokens
  * that were drafted and rejected) leaves no trace of the replaced rows, and
@@ -499,10 +500,15 @@ size_t bsa_cache_attn_workspace_bytes(int B, int T, int H, int H_kv, int D);
  * idx is NULL. A row that sees no token gives zeros; rows t >= count[b] of o
  * are left as they are. The new tokens' own keys and values are read from the
  * cache: write them first. q, o: [B, T, H, D]; o must not be q. Scores, the
- * softmax's sums and the output sums are float32; bfloat16 queries' softmax
- * weights times the values' scales are rounded to float16 for the tensor cores
- * (relative 2^-11, and 2^-33 of the row's largest weight times scale over all
- * channels), float32 queries' parts are split in two. workspace: device
+ * softmax's sums and the output sums are float32 (sums of products over up to
+ * 512 tokens are the tensor cores', which truncate). For the tensor cores,
+ * - weights times the values' scales are rounded: for bfloat16 queries to
+ *   float16, relative 2^-11 and 2^-33 of the row's largest in the channel's
+ *   group of 64, for float32 queries to two float16 parts, 2^-22 and 2^-37
+ *   (both 2^-25 of the largest where its scale is 2^-126, the smallest there is);
+ * - float32 query elements to two float16 parts, 2^-22 and 2^-38 of the row's
+ *   largest element; bfloat16 ones are exact, but for 2^-34 of the largest.
+ * Values below 2^56 in size cannot overflow the sums. workspace: device
  * memory of bsa_cache_attn_workspace_bytes() bytes, 16-byte aligned, not used
  * by an overlapping call. B <= 4096. Deterministic. A query row with a NaN, an
  * infinity or an element of 2^117 or more in size gives NaN (zeros where it
